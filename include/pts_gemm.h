@@ -312,6 +312,103 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, const gemm_group_problem_t *prob
 gemm_status_t gemm_query_grouped(gemm_handle_t h, const gemm_group_problem_t *problems, int64_t count,
                                  gemm_dtype_t dtype, gemm_sched_t sched, gemm_launch_info_t *info);
 
+/* ---- a layer of experts ---------------------------------------------------
+ * The operators of a layer whose tokens each go to top_k of `experts` weight
+ * matrices.  The row counts of the experts are device data from start to end:
+ * nothing is read back and every call is asynchronous, so a whole layer can be
+ * queued, or captured into a CUDA graph, without knowing where its tokens go.
+ *
+ *   gemm_expert_sort     expert ids -> offsets, row_of, src_of
+ *   gemm_expert_gather   tokens -> rows in expert order
+ *   gemm_run_experts     the experts' products (gemm_run_nibble: the same for few
+ *                        rows with 4-bit weights)
+ *   gemm_expert_combine  rows -> tokens, weighted
+ *
+ * and, backward, gemm_expert_combine_grad, gemm_run_experts_dgrad,
+ * gemm_run_experts_wgrad and gemm_expert_combine without weights (the gradient
+ * of the gather).
+ *
+ * Shared arrays (device, int32):
+ *   offsets  experts + 1: the rows of expert e are offsets[e] .. offsets[e + 1] - 1
+ *            (offsets[0] = 0, never decreasing, the last at most `rows`).
+ *   row_of   tokens x top_k: the row of assignment (t, j), or -1 if it has none.
+ *   src_of   tokens x top_k: the assignment t * top_k + j of a row, or -1.
+ * Rows at or behind offsets[experts] belong to no expert: the calls below
+ * neither read nor write them.  The calls stay inside the arrays whatever the
+ * device data holds (offsets are clamped to [0, rows], a row_of outside the
+ * rows counts as -1); an expert whose offsets decrease has no rows.
+ * All arrays are contiguous, rows of a multiple of 16 bytes, 16-byte aligned
+ * (int32 and fp32 arrays: 4-byte), and outputs do not overlap inputs.  Of the
+ * handle's options these calls use cta_group, max_clusters, group_size_m,
+ * timeout_ns (gemm_run_experts and its gradients) and overlap_launch. */
+
+/* Sort tokens * top_k assignments by expert, stably: rows of one expert are in
+ * the order of t * top_k + j.  An id outside [0, experts) marks an assignment
+ * without a row (a padded token, an expert another device holds).  Writes
+ * offsets (all of it), row_of (all) and src_of (-1 behind the last row).
+ * experts in [1, GEMM_EXPERT_SORT_MAX_EXPERTS]; tokens * top_k < 2^31, top_k >= 1. */
+#define GEMM_EXPERT_SORT_MAX_EXPERTS 1024
+gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t experts,
+                               const int32_t *expert_ids, int32_t *offsets, int32_t *row_of, int32_t *src_of,
+                               void *stream);
+
+/* Xs[row_of[t, j]] = X[t].  X: tokens x dim, Xs: tokens * top_k x dim, of any
+ * of the dtypes (bits are copied). */
+gemm_status_t gemm_expert_gather(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *X,
+                                 const int32_t *row_of, void *Xs, gemm_dtype_t dtype, void *stream);
+
+/* Y[t] = sum_j weights[t, j] * Ys[row_of[t, j]] over the assignments that have
+ * a row, summed in fp32 in the order of j and rounded once; a token without
+ * any gets zeros.  Ys: tokens * top_k x dim, Y: tokens x dim, fp16 or bf16;
+ * weights: tokens x top_k fp32, or NULL for ones (the gradient of
+ * gemm_expert_gather). */
+gemm_status_t gemm_expert_combine(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *Ys,
+                                  const int32_t *row_of, const float *weights, void *Y, gemm_dtype_t dtype,
+                                  void *stream);
+
+/* The gradient of gemm_expert_combine: dYs[row_of[t, j]] = weights[t, j] * dY[t]
+ * and dweights[t, j] = sum_d dY[t, d] * Ys[row_of[t, j], d] (fp32; 0 for an
+ * assignment without a row). */
+gemm_status_t gemm_expert_combine_grad(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *dY,
+                                       const void *Ys, const int32_t *row_of, const float *weights, void *dYs,
+                                       float *dweights, gemm_dtype_t dtype, void *stream);
+
+/* C[r] = A[r] . B_e for every row r of every expert e, one launch.
+ * A: rows x K; B: experts x N x K (each expert's matrix as gemm_run's B);
+ * C: rows x N.  dtypes, scales, size rules and K == 0 as in gemm_run (rows
+ * takes the place of M; experts < 2^31). */
+gemm_status_t gemm_run_experts(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *A,
+                               const void *B, const int32_t *offsets, void *C, gemm_dtype_t dtype, float scale_a,
+                               float scale_b, void *stream);
+
+/* Its gradient for the rows: dA[r, k] = sum_n dC[r, n] * B_e[n, k].  fp16 or
+ * bf16; B is read as it is stored, no transposed copy is made. */
+gemm_status_t gemm_run_experts_dgrad(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                     const void *dC, const void *B, const int32_t *offsets, void *dA,
+                                     gemm_dtype_t dtype, void *stream);
+
+/* Its gradient for the weights: dB_e[n, k] = sum over expert e's rows of
+ * dC[r, n] * A[r, k]; all of dB (experts x N x K) is written, zeros for an
+ * expert without rows.  fp16 or bf16. */
+gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                     const void *dC, const void *A, const int32_t *offsets, void *dB,
+                                     gemm_dtype_t dtype, void *stream);
+
+/* C[r, n] = sum_k A[r, k] * (q_e[n, k] - z_e[n, k / group]) * s_e[n, k / group]
+ * for the rows r of expert e: a token's products with 4-bit weights.
+ *   A: rows x K, C: rows x N, fp16 or bf16;
+ *   B: experts x N x K/2 bytes, q[n, 2i] the low and q[n, 2i + 1] the high half
+ *      of byte i of row n;
+ *   scales: experts x N x ceil(K / group), of A's type;
+ *   zeros: uint8 in 0..15, same shape as scales, or NULL for 8 everywhere;
+ *   offsets: as above, or NULL with experts == 1 (every row uses that matrix).
+ * group: 32, 64 or 128 (the last group may be short); K % 32 == 0, N % 8 == 0.
+ * Products are exact and sums fp32.  Made for a few rows per expert: the cost is
+ * the weights' bytes, read once for every 32 rows of an expert. */
+gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,
+                              const void *A, const void *B, const void *scales, const uint8_t *zeros,
+                              const int32_t *offsets, void *C, gemm_dtype_t dtype, void *stream);
+
 /* ---- tensor-pipe peak probe (a measurement aid, not a GEMM) -------------
  * Every SM (cta_group 1) or SM pair (cta_group 2) issues `mmas` back-to-back
  * tcgen05.mma of one k-step of the GEMM's tile (128 x 256 per CTA, 256 x 256

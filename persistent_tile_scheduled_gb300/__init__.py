@@ -10,4 +10,6 @@ from .gemm import (GEMM_BF16, GEMM_DEBUG_CLC_STOP_AT, GEMM_DEBUG_FAULT_SKIP_TMA,
                    gemm_check, gemm_create, gemm_destroy, gemm_query, gemm_query_grouped, gemm_read_debug, gemm_run,
                    gemm_run_grouped, gemm_run_host, gemm_run_host_batch, gemm_run_noalloc, gemm_status_string, gemm_tensor_peak_probe, load,
                    make_opts)
+from .experts import (gemm_expert_combine, gemm_expert_combine_grad, gemm_expert_gather, gemm_expert_sort,  # noqa: F401
+                      gemm_run_experts, gemm_run_experts_dgrad, gemm_run_experts_wgrad, gemm_run_nibble)
 from ._build import build  # noqa: F401

@@ -1,0 +1,282 @@
+// C ABI of the expert layer's operators: argument checks, tensor maps and
+// launches.  Declared in pts_gemm.h.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "expert_launch.h"
+#include "gemm_ctx.h"
+
+using namespace pts;
+
+namespace {
+
+constexpr int64_t kLim = (int64_t(1) << 31) - 1;
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool is16(gemm_dtype_t d) { return d == GEMM_F16 || d == GEMM_BF16; }
+
+gemm_status_t launched(cudaError_t e)
+{
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? GEMM_OK : cuda_fail(e);
+}
+
+gemm_status_t on_device(const gemm_ctx *h)
+{
+    return cudaSetDevice(h->device) == cudaSuccess ? GEMM_OK : cuda_fail(cudaErrorInvalidDevice);
+}
+
+bool overlap(const gemm_ctx *h) { return h->opts.overlap_launch >= 0; }
+
+// Common checks of the row kernels: tokens x top_k assignments, rows of dim elements.
+gemm_status_t check_rows(gemm_ctx *h, int64_t tokens, int64_t top_k, int64_t dim, int es)
+{
+    if (h == nullptr || tokens < 0 || top_k < 1 || dim < 0 || dim > kLim) return GEMM_ERR_INVALID_ARG;
+    if (top_k > kLim || tokens > kLim || tokens * top_k > kLim) return GEMM_ERR_INVALID_ARG;
+    if ((dim * es) % 16 != 0) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+// One product of the experts.  features / contraction / out_rows as in
+// ExpertParams; W and X as in expert_gemm.cuh.
+gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *W,
+                          const void *X, const int32_t *offsets, void *out, gemm_dtype_t dtype, float out_scale,
+                          cudaStream_t stream)
+{
+    const int64_t features = mode == EXPERT_FWD ? N : K;
+    const int64_t contraction = mode == EXPERT_FWD ? K : N;   // (WGRAD: an expert's rows)
+    const int kelems = dtype == GEMM_E4M3 ? 128 : 64;
+    // Variant.  See DESIGN for the measurements behind both rules.
+    int cg = h->opts.cta_group;
+    int bn = kExpertTileN;
+    if (cg == 0) cg = 2;
+    if (mode == EXPERT_FWD && h->opts.cta_group != 2 && rows <= int64_t(kExpertTileNFew) * experts) {
+        cg = 1;
+        bn = kExpertTileNFew;
+    }
+    int stages = kMaxStages;
+    while (stages > 2 && expert_smem_bytes(cg, bn, stages) > h->max_smem_optin) --stages;
+    const int smem = expert_smem_bytes(cg, bn, stages);
+    const int kind = static_cast<int>(dtype);
+    const ExpertOps ops = mode == EXPERT_FWD ? expert_ops_fwd(kind, cg, bn)
+                          : mode == EXPERT_DGRAD ? expert_ops_dgrad(kind, cg)
+                                                 : expert_ops_wgrad(kind, cg);
+    int &resident = h->expert_clusters[kind][mode][bn == kExpertTileNFew ? 2 : cg - 1];
+    if (resident == 0) {
+        int n = 0;
+        if (ops.prepare(smem, h->sm_count, &n) != cudaSuccess) return cuda_fail(cudaErrorInvalidValue);
+        if (n < 1) return GEMM_ERR_CUDA;
+        resident = n;
+    }
+    // tiles: at most one short one per expert on top of the rows' own
+    const int64_t tf = (features + kRowsPerCta * cg - 1) / (kRowsPerCta * cg);
+    const int64_t used = rows < experts ? rows : experts;
+    const int64_t tiles = mode == EXPERT_WGRAD ? experts * tf * ((N + bn - 1) / bn) : (rows / bn + used) * tf;
+    if (tiles > (int64_t(1) << 30)) return GEMM_ERR_INVALID_ARG;
+    int64_t clusters = h->opts.max_clusters > 0 && h->opts.max_clusters < resident ? h->opts.max_clusters : resident;
+    if (clusters > tiles) clusters = tiles;
+
+    CUtensorMap mw, mx, mxs, mo;
+    std::memset(&mw, 0, sizeof(mw));
+    mx = mxs = mo = mw;
+    bool ok = true;
+    if (mode == EXPERT_WGRAD) {
+        ok = encode_map3(h, &mw, W, 1, rows, K, dtype, 64, 64) && encode_map3(h, &mx, X, 1, rows, N, dtype, 64, 64);
+        mxs = mx;
+        ok = ok && encode_map3(h, &mo, out, experts, N, K, dtype, 64, 32);
+    } else {
+        if (contraction > 0) {
+            ok = mode == EXPERT_FWD ? encode_map3(h, &mw, W, experts, N, K, dtype, kRowsPerCta, kelems)
+                                    : encode_map3(h, &mw, W, experts, N, K, dtype, 64, 64);
+            ok = ok && encode_map3(h, &mx, X, 1, rows, contraction, dtype, static_cast<uint32_t>(bn / cg), kelems)
+                 && encode_map3(h, &mxs, X, 1, rows, contraction, dtype, 16, kelems);
+        }
+        ok = ok
+             && encode_map3(h, &mo, out, 1, rows, features, dtype == GEMM_E4M3 ? GEMM_BF16 : dtype, 64, 32);
+    }
+    if (!ok) return GEMM_ERR_INVALID_ARG;
+
+    ExpertParams p{};
+    p.rows = static_cast<int32_t>(rows);
+    p.experts = static_cast<int32_t>(experts);
+    p.features = static_cast<int32_t>(features);
+    p.contraction = static_cast<int32_t>(contraction);
+    p.out_rows = static_cast<int32_t>(N);
+    p.stages = stages;
+    p.group_m = h->opts.group_size_m;
+    p.out_scale = out_scale;
+    p.offsets = offsets;
+    p.out = out;
+    p.timeout_ns = h->opts.timeout_ns;
+    p.status = h->d_status;
+    return launched(ops.launch(mw, mx, mxs, mo, p, static_cast<int>(clusters) * cg, smem, stream, overlap(h)));
+}
+
+gemm_status_t check_product(gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, const int32_t *offsets)
+{
+    if (h == nullptr || rows < 0 || experts < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (rows > kLim || experts > kLim || N > kLim || K > kLim) return GEMM_ERR_INVALID_ARG;
+    if (experts > 0 && (offsets == nullptr || !aligned4(offsets))) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t experts,
+                               const int32_t *expert_ids, int32_t *offsets, int32_t *row_of, int32_t *src_of,
+                               void *stream)
+{
+    gemm_status_t st = check_rows(h, tokens, top_k, 0, 2);
+    if (st != GEMM_OK) return st;
+    if (experts < 1 || experts > kMaxExpertsSorted || offsets == nullptr || !aligned4(offsets)) return GEMM_ERR_INVALID_ARG;
+    const int64_t n = tokens * top_k;
+    if (n > 0 && (expert_ids == nullptr || row_of == nullptr || src_of == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned4(expert_ids) || !aligned4(row_of) || !aligned4(src_of)) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    return launched(launch_expert_sort(expert_ids, n, static_cast<int>(experts), offsets, row_of, src_of,
+                                       static_cast<cudaStream_t>(stream), overlap(h)));
+}
+
+gemm_status_t gemm_expert_gather(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *X,
+                                 const int32_t *row_of, void *Xs, gemm_dtype_t dtype, void *stream)
+{
+    if (dtype < GEMM_F16 || dtype > GEMM_E4M3) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(dtype);
+    gemm_status_t st = check_rows(h, tokens, top_k, dim, es);
+    if (st != GEMM_OK) return st;
+    if (tokens == 0 || dim == 0) return GEMM_OK;
+    if (X == nullptr || Xs == nullptr || row_of == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(Xs) || !aligned4(row_of)) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    return launched(launch_expert_gather(X, row_of, Xs, static_cast<int>(tokens), static_cast<int>(top_k),
+                                         static_cast<int>(dim * es / 16), static_cast<cudaStream_t>(stream), overlap(h)));
+}
+
+gemm_status_t gemm_expert_combine(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *Ys,
+                                  const int32_t *row_of, const float *weights, void *Y, gemm_dtype_t dtype,
+                                  void *stream)
+{
+    if (!is16(dtype)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_rows(h, tokens, top_k, dim, 2);
+    if (st != GEMM_OK) return st;
+    if (tokens == 0 || dim == 0) return GEMM_OK;
+    if (Ys == nullptr || Y == nullptr || row_of == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (!aligned16(Ys) || !aligned16(Y) || !aligned4(row_of) || !aligned4(weights)) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    return launched(launch_expert_combine(static_cast<int>(dtype), Ys, row_of, weights, Y, static_cast<int>(tokens),
+                                          static_cast<int>(top_k), static_cast<int>(dim / 8),
+                                          static_cast<cudaStream_t>(stream), overlap(h)));
+}
+
+gemm_status_t gemm_expert_combine_grad(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *dY,
+                                       const void *Ys, const int32_t *row_of, const float *weights, void *dYs,
+                                       float *dweights, gemm_dtype_t dtype, void *stream)
+{
+    if (!is16(dtype)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_rows(h, tokens, top_k, dim, 2);
+    if (st != GEMM_OK) return st;
+    if (tokens == 0) return GEMM_OK;
+    if (row_of == nullptr || weights == nullptr || dweights == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (dim > 0 && (dY == nullptr || Ys == nullptr || dYs == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned16(dY) || !aligned16(Ys) || !aligned16(dYs) || !aligned4(row_of) || !aligned4(weights)
+        || !aligned4(dweights))
+        return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    return launched(launch_expert_combine_grad(static_cast<int>(dtype), dY, Ys, row_of, weights, dYs, dweights,
+                                               static_cast<int>(tokens), static_cast<int>(top_k),
+                                               static_cast<int>(dim / 8), static_cast<cudaStream_t>(stream),
+                                               overlap(h)));
+}
+
+gemm_status_t gemm_run_experts(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *A,
+                               const void *B, const int32_t *offsets, void *C, gemm_dtype_t dtype, float scale_a,
+                               float scale_b, void *stream)
+{
+    if (dtype < GEMM_F16 || dtype > GEMM_E4M3) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_product(h, rows, experts, N, K, offsets);
+    if (st != GEMM_OK) return st;
+    if ((K * elem_bytes(dtype)) % 16 != 0 || (N * 2) % 16 != 0) return GEMM_ERR_INVALID_ARG;
+    float scale = 1.0f;
+    if (dtype == GEMM_E4M3) {
+        if (!(scale_a > 0.0f) || !(scale_b > 0.0f) || !std::isfinite(scale_a) || !std::isfinite(scale_b))
+            return GEMM_ERR_INVALID_ARG;
+        scale = static_cast<float>(1.0 / (static_cast<double>(scale_a) * static_cast<double>(scale_b)));
+    }
+    if (rows == 0 || experts == 0 || N == 0) return GEMM_OK;
+    if (C == nullptr || !aligned16(C)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (A == nullptr || B == nullptr || !aligned16(A) || !aligned16(B))) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    return run_product(h, EXPERT_FWD, rows, experts, N, K, B, A, offsets, C, dtype, scale,
+                       static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_run_experts_dgrad(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                     const void *dC, const void *B, const int32_t *offsets, void *dA,
+                                     gemm_dtype_t dtype, void *stream)
+{
+    if (!is16(dtype)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_product(h, rows, experts, N, K, offsets);
+    if (st != GEMM_OK) return st;
+    if ((K * 2) % 16 != 0 || (N * 2) % 16 != 0) return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || experts == 0 || K == 0) return GEMM_OK;
+    if (dA == nullptr || !aligned16(dA)) return GEMM_ERR_INVALID_ARG;
+    if (N > 0 && (dC == nullptr || B == nullptr || !aligned16(dC) || !aligned16(B))) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    return run_product(h, EXPERT_DGRAD, rows, experts, N, K, B, dC, offsets, dA, dtype, 1.0f,
+                       static_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                     const void *dC, const void *A, const int32_t *offsets, void *dB,
+                                     gemm_dtype_t dtype, void *stream)
+{
+    if (!is16(dtype)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_product(h, rows, experts, N, K, offsets);
+    if (st != GEMM_OK) return st;
+    if ((K * 2) % 16 != 0 || (N * 2) % 16 != 0) return GEMM_ERR_INVALID_ARG;
+    if (experts == 0 || N == 0 || K == 0) return GEMM_OK;
+    if (dB == nullptr || !aligned16(dB)) return GEMM_ERR_INVALID_ARG;
+    if (rows > 0 && (dC == nullptr || A == nullptr || !aligned16(dC) || !aligned16(A))) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0)   // every sum is empty
+        return launched(cudaMemsetAsync(dB, 0, static_cast<size_t>(experts) * N * K * 2, s));
+    return run_product(h, EXPERT_WGRAD, rows, experts, N, K, A, dC, offsets, dB, dtype, 1.0f, s);
+}
+
+gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,
+                              const void *A, const void *B, const void *scales, const uint8_t *zeros,
+                              const int32_t *offsets, void *C, gemm_dtype_t dtype, void *stream)
+{
+    if (!is16(dtype) || h == nullptr || rows < 0 || experts < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (rows > kLim || experts > kLim || N > kLim || K > kLim) return GEMM_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return GEMM_ERR_INVALID_ARG;
+    if (K % 32 != 0 || N % 8 != 0) return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || experts == 0 || N == 0) return GEMM_OK;
+    if ((offsets == nullptr && experts != 1) || !aligned4(offsets)) return GEMM_ERR_INVALID_ARG;
+    if (C == nullptr || !aligned16(C)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (A == nullptr || B == nullptr || scales == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(scales) || !aligned16(zeros)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = on_device(h);
+    if (st != GEMM_OK) return st;
+    NibbleParams p{};
+    p.rows = static_cast<int32_t>(rows);
+    p.experts = static_cast<int32_t>(experts);
+    p.N = static_cast<int32_t>(N);
+    p.K = static_cast<int32_t>(K);
+    p.group = static_cast<int32_t>(group);
+    p.groups = static_cast<int32_t>((K + group - 1) / group);
+    p.a = A;
+    p.b = static_cast<const uint8_t *>(B);
+    p.scales = scales;
+    p.zeros = zeros;
+    p.offsets = offsets;
+    p.c = C;
+    return launched(launch_nibble(static_cast<int>(dtype), p, h->sm_count, static_cast<cudaStream_t>(stream), overlap(h)));
+}
+
+}  // extern "C"

@@ -1,0 +1,333 @@
+// Rows to the experts and back: assignments sorted by expert, the rows copied
+// into that order, and the experts' rows summed with weights, with gradients.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "expert_launch.h"
+#include "ptx.cuh"
+
+namespace pts {
+
+namespace {
+
+// ---- sort --------------------------------------------------------------------
+//
+// A stable counting sort in one launch: one cluster of up to 8 CTAs, CTA c and
+// in it warp w taking consecutive stretches of the assignments.  A warp counts
+// its stretch per expert (a histogram of its own in shared memory, so the order
+// of the counts is that of the assignments and no atomics are needed), the
+// counts are summed over warps, CTAs (through distributed shared memory) and
+// experts, and the warp walks its stretch again handing out rows.
+constexpr int kSortMaxWarps = 32;
+constexpr int kSortMaxCtas = 8;
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
+    expert_sort_kernel(const int32_t *__restrict__ ids, int n, int experts, int32_t *__restrict__ offsets,
+                       int32_t *__restrict__ row_of, int32_t *__restrict__ src_of)
+{
+    extern __shared__ uint32_t sm[];
+    const int warps = static_cast<int>(blockDim.x >> 5);
+    uint32_t *hist = sm;                        // [warps][experts]
+    uint32_t *total = sm + warps * experts;     // [experts], this CTA's counts
+    uint32_t *scan = total + experts;           // [warps]
+    const int warp = static_cast<int>(threadIdx.x >> 5);
+    const int lane = static_cast<int>(lane_id());
+    const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+    uint32_t *mine = hist + warp * experts;
+
+    for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) hist[i] = 0u;
+    const int per_warp = ((n + ctas * warps - 1) / (ctas * warps) + 31) / 32 * 32;
+    const long long first = static_cast<long long>(cta * warps + warp) * per_warp;
+    const int lo = static_cast<int>(first < n ? first : n);
+    const int hi = n - lo < per_warp ? n : lo + per_warp;
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // count
+    for (int b = lo; b < hi; b += 32) {
+        const int i = b + lane;
+        const int id = i < hi ? ids[i] : -1;
+        const bool held = id >= 0 && id < experts;
+        const uint32_t peers = __match_any_sync(0xffffffffu, held ? id : -1);
+        if (held && (peers & ((1u << lane) - 1u)) == 0) mine[id] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    // exclusive over the warps, per expert
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+        uint32_t s = 0;
+        for (int w = 0; w < warps; ++w) {
+            const uint32_t c = hist[w * experts + e];
+            hist[w * experts + e] = s;
+            s += c;
+        }
+        total[e] = s;
+    }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    // start of each expert's rows: over all CTAs and the experts before it;
+    // `carry` runs over blocks of blockDim.x experts
+    uint32_t carry = 0;
+    for (int e0 = 0; e0 < experts; e0 += static_cast<int>(blockDim.x)) {
+        const int e = e0 + static_cast<int>(threadIdx.x);
+        uint32_t all = 0, below = 0;
+        if (e < experts) {
+            if (ctas > 1) {
+                for (int c = 0; c < ctas; ++c) {
+                    const uint32_t v = ld_cluster_u32(mapa(smem_u32(total + e), static_cast<uint32_t>(c)));
+                    all += v;
+                    if (c < cta) below += v;
+                }
+            } else {
+                all = total[e];
+            }
+        }
+        uint32_t incl = all;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, s);
+            if (lane >= s) incl += o;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        uint32_t before = carry, block = 0;
+        for (int w = 0; w < warps; ++w) {
+            const uint32_t v = scan[w];
+            if (w < warp) before += v;
+            block += v;
+        }
+        const uint32_t start = before + incl - all;
+        if (e < experts) {
+            if (cta == 0) offsets[e] = static_cast<int32_t>(start);
+            for (int w = 0; w < warps; ++w) hist[w * experts + e] += start + below;
+        }
+        carry += block;
+        __syncthreads();
+    }
+    if (cta == 0 && threadIdx.x == 0) offsets[experts] = static_cast<int32_t>(carry);
+
+    // hand out rows
+    for (int b = lo; b < hi; b += 32) {
+        const int i = b + lane;
+        const int id = i < hi ? ids[i] : -1;
+        const bool held = id >= 0 && id < experts;
+        const uint32_t peers = __match_any_sync(0xffffffffu, held ? id : -1);
+        const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
+        uint32_t row = 0;
+        if (held) row = mine[id] + rank;
+        __syncwarp();
+        if (held && rank == 0) mine[id] += __popc(peers);
+        __syncwarp();
+        if (i < hi) row_of[i] = held ? static_cast<int32_t>(row) : -1;
+        if (held) src_of[row] = i;
+    }
+    // rows behind the last held assignment have no source
+    for (long long r = static_cast<long long>(carry) + cta * static_cast<long long>(blockDim.x) + threadIdx.x; r < n;
+         r += static_cast<long long>(ctas) * blockDim.x)
+        src_of[r] = -1;
+    if (ctas > 1) cluster_sync();   // no CTA leaves while another may read its counts
+}
+
+// ---- rows ----------------------------------------------------------------------
+
+template <int KIND>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 t;
+        if constexpr (KIND == 0)
+            t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        else
+            t = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+    }
+}
+
+template <int KIND>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (KIND == 0) {
+            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Xs[row_of[t, j]] = X[t]: a block per token, 16 bytes per thread and step,
+// read once and written top_k times.
+__global__ void __launch_bounds__(256) expert_gather_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ row_of,
+                                                            uint4 *__restrict__ xs, int tokens, int top_k, int chunks)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long t = blockIdx.x;
+    const long long n = static_cast<long long>(tokens) * top_k;
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        const uint4 v = x[t * chunks + c];
+        for (int j = 0; j < top_k; ++j) {
+            const int32_t r = row_of[t * top_k + j];
+            if (r >= 0 && r < n) xs[static_cast<long long>(r) * chunks + c] = v;
+        }
+    }
+}
+
+// Y[t] = sum_j w[t, j] Ys[row_of[t, j]], in 32 bits in the order of j.
+template <int KIND>
+__global__ void __launch_bounds__(256)
+    expert_combine_kernel(const uint4 *__restrict__ ys, const int32_t *__restrict__ row_of, const float *__restrict__ w,
+                          uint4 *__restrict__ y, int tokens, int top_k, int chunks)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long t = blockIdx.x;
+    const long long n = static_cast<long long>(tokens) * top_k;
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        float acc[8] = {};
+        for (int j = 0; j < top_k; ++j) {
+            const int32_t r = row_of[t * top_k + j];
+            if (r < 0 || r >= n) continue;
+            float f[8];
+            unpack8<KIND>(ys[static_cast<long long>(r) * chunks + c], f);
+            const float s = w ? w[t * top_k + j] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(s, f[i], acc[i]);
+        }
+        y[t * chunks + c] = pack8<KIND>(acc);
+    }
+}
+
+// dYs[row] = w[t, j] dY[t], dw[t, j] = <dY[t], Ys[row]> with row = row_of[t, j];
+// dw is 0 where there is no row.
+template <int KIND>
+__global__ void __launch_bounds__(256)
+    expert_combine_grad_kernel(const uint4 *__restrict__ dy, const uint4 *__restrict__ ys,
+                               const int32_t *__restrict__ row_of, const float *__restrict__ w, uint4 *__restrict__ dys,
+                               float *__restrict__ dw, int tokens, int top_k, int chunks)
+{
+    __shared__ float part[8];
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long t = blockIdx.x;
+    const long long n = static_cast<long long>(tokens) * top_k;
+    for (int j = 0; j < top_k; ++j) {
+        const int32_t r = row_of[t * top_k + j];
+        float dot = 0.0f;
+        if (r >= 0 && r < n) {
+            const float s = w[t * top_k + j];
+            for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+                float d[8], f[8];
+                unpack8<KIND>(dy[t * chunks + c], d);
+                unpack8<KIND>(ys[static_cast<long long>(r) * chunks + c], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot = fmaf(d[i], f[i], dot);
+                    d[i] *= s;
+                }
+                dys[static_cast<long long>(r) * chunks + c] = pack8<KIND>(d);
+            }
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+        if (lane_id() == 0) part[threadIdx.x >> 5] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float all = 0.0f;
+            for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) all += part[i];
+            dw[t * top_k + j] = all;
+        }
+        __syncthreads();
+    }
+}
+
+template <class... P, class... A>
+cudaError_t go(void (*kernel)(P...), long long grid, int block, size_t smem, int cluster, cudaStream_t stream,
+               bool overlap, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(block), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    int n = 0;
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    cfg.numAttrs = static_cast<unsigned>(n);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// threads of a row kernel: one 16-byte chunk each, up to 256
+int row_threads(int chunks) { return chunks >= 256 ? 256 : (chunks + 31) / 32 * 32; }
+
+}  // namespace
+
+cudaError_t launch_expert_sort(const int32_t *ids, int64_t n, int experts, int32_t *offsets, int32_t *row_of,
+                               int32_t *src_of, cudaStream_t stream, bool overlap)
+{
+    int warps = static_cast<int>((n + 127) / 128);
+    warps = warps < 1 ? 1 : (warps > kSortMaxWarps ? kSortMaxWarps : warps);
+    int ctas = 1;
+    while (ctas < kSortMaxCtas && n > 8192ll * ctas) ctas *= 2;
+    const size_t smem = (static_cast<size_t>(warps + 1) * experts + warps) * sizeof(uint32_t);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    return go(expert_sort_kernel, ctas, warps * 32, smem, ctas, stream, overlap, ids, static_cast<int>(n), experts,
+              offsets, row_of, src_of);
+}
+
+cudaError_t launch_expert_gather(const void *x, const int32_t *row_of, void *xs, int tokens, int top_k, int chunks,
+                                 cudaStream_t stream, bool overlap)
+{
+    return go(expert_gather_kernel, tokens, row_threads(chunks), 0, 1, stream, overlap, static_cast<const uint4 *>(x),
+              row_of, static_cast<uint4 *>(xs), tokens, top_k, chunks);
+}
+
+cudaError_t launch_expert_combine(int kind, const void *ys, const int32_t *row_of, const float *w, void *y, int tokens,
+                                  int top_k, int chunks, cudaStream_t stream, bool overlap)
+{
+    return go(kind == 0 ? expert_combine_kernel<0> : expert_combine_kernel<1>, tokens, row_threads(chunks), 0, 1, stream,
+              overlap, static_cast<const uint4 *>(ys), row_of, w, static_cast<uint4 *>(y), tokens, top_k, chunks);
+}
+
+cudaError_t launch_expert_combine_grad(int kind, const void *dy, const void *ys, const int32_t *row_of, const float *w,
+                                       void *dys, float *dw, int tokens, int top_k, int chunks, cudaStream_t stream,
+                                       bool overlap)
+{
+    return go(kind == 0 ? expert_combine_grad_kernel<0> : expert_combine_grad_kernel<1>, tokens, row_threads(chunks), 0,
+              1, stream, overlap, static_cast<const uint4 *>(dy), static_cast<const uint4 *>(ys), row_of, w,
+              static_cast<uint4 *>(dys), dw, tokens, top_k, chunks);
+}
+
+}  // namespace pts

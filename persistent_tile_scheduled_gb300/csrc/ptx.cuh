@@ -117,6 +117,15 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t pred, uint32_t
                  : "memory");
 }
 
+// The same on a barrier given by its shared::cluster address (own or peer CTA).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster_if(uint32_t pred, uint32_t cluster_bar, uint32_t bytes)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+                 "@q mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%1], %2;\n\t}" ::"r"(pred),
+                 "r"(cluster_bar), "r"(bytes)
+                 : "memory");
+}
+
 // Non-blocking probe of phase `parity`; cluster-scope acquire so that arrivals
 // and async writes made by the peer CTA of a pair are visible afterwards.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
@@ -174,6 +183,27 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t pred, uint32_t dst, co
                  : "memory");
 }
 
+// 3-D forms of the two loads above.
+__device__ __forceinline__ void tma_load_3d(uint32_t pred, uint32_t dst, const void *tmap, uint32_t bar, int x,
+                                            int y, int z)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+                 "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%1], [%2, {%4, %5, %6}], [%3];\n\t}" ::"r"(pred),
+                 "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t pred, uint32_t dst, const void *tmap,
+                                                 uint32_t cluster_bar, int x, int y, int z)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+                 "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".cta_group::2 [%1], [%2, {%4, %5, %6}], [%3];\n\t}" ::"r"(pred),
+                 "r"(dst), "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // Bring a 2-D box of the tensor into L2 (no shared-memory destination, no
 // completion); out-of-bounds parts are ignored.
 __device__ __forceinline__ void tma_prefetch_2d(uint32_t pred, const void *tmap, int x, int y)
@@ -192,6 +222,14 @@ __device__ __forceinline__ void tma_store_2d_if(uint32_t pred, const void *tmap,
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
                  "@q cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%1, {%3, %4}], [%2];\n\t}"
                  ::"r"(pred), "l"(tmap), "r"(src), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d_if(uint32_t pred, const void *tmap, uint32_t src, int x, int y, int z)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+                 "@q cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%1, {%3, %4, %5}], [%2];\n\t}"
+                 ::"r"(pred), "l"(tmap), "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 
@@ -298,6 +336,34 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
                    "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
                    "=r"(r[31])
                  : "r"(taddr)
+                 : "memory");
+}
+
+// 16 lanes x 64 consecutive 32-bit columns in the accumulator fragment layout:
+// for column block j (8 columns), thread t gets row t / 4 columns
+// 2 (t % 4), + 1 in r[4j], r[4j + 1] and row t / 4 + 8 in r[4j + 2], r[4j + 3].
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                   "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+                   "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements, each stored transposed: thread t
+// holds elements 2 (t % 4), + 1 of row t / 4 of matrix i in r[i]; column c of
+// matrix i goes to the 16 bytes at the address that thread 8 i + c gives.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0),
+                 "r"(r1), "r"(r2), "r"(r3)
                  : "memory");
 }
 

@@ -23,9 +23,12 @@ GEMM_DEBUG_FAULT_SKIP_TMA = 0x4
 
 EXPORTED = ("gemm_create", "gemm_run", "gemm_run_host", "gemm_query", "gemm_check",
             "gemm_read_debug", "gemm_destroy", "gemm_status_string", "gemm_run_noalloc",
-            "gemm_run_host_batch", "gemm_run_grouped", "gemm_query_grouped", "gemm_tensor_peak_probe")
+            "gemm_run_host_batch", "gemm_run_grouped", "gemm_query_grouped", "gemm_tensor_peak_probe",
+            "gemm_expert_sort", "gemm_expert_gather", "gemm_expert_combine", "gemm_expert_combine_grad",
+            "gemm_run_experts", "gemm_run_experts_dgrad", "gemm_run_experts_wgrad", "gemm_run_nibble")
 GEMM_NOALLOC_MAX_WORK_ITEMS = 16384
 GEMM_GROUPED_MAX_PROBLEMS = 65536
+GEMM_EXPERT_SORT_MAX_EXPERTS = 1024
 
 
 class gemm_opts_t(ctypes.Structure):
@@ -116,6 +119,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     dp = ctypes.POINTER(ctypes.c_double)
     lib.gemm_tensor_peak_probe.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, i64, dp, dp, dp]
     lib.gemm_tensor_peak_probe.restype = st
+    dt = ctypes.c_int
+    for name, args in (("gemm_expert_sort", [vp, i64, i64, i64, vp, vp, vp, vp, vp]),
+                       ("gemm_expert_gather", [vp, i64, i64, i64, vp, vp, vp, dt, vp]),
+                       ("gemm_expert_combine", [vp, i64, i64, i64, vp, vp, vp, vp, dt, vp]),
+                       ("gemm_expert_combine_grad", [vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, dt, vp]),
+                       ("gemm_run_experts", [vp, i64, i64, i64, i64, vp, vp, vp, vp, dt, f32, f32, vp]),
+                       ("gemm_run_experts_dgrad", [vp, i64, i64, i64, i64, vp, vp, vp, vp, dt, vp]),
+                       ("gemm_run_experts_wgrad", [vp, i64, i64, i64, i64, vp, vp, vp, vp, dt, vp]),
+                       ("gemm_run_nibble", [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, dt, vp])):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = args, st
     lib.gemm_status_string.argtypes = [ctypes.c_int]
     lib.gemm_status_string.restype = ctypes.c_char_p
     _lib = lib
