@@ -81,8 +81,12 @@ struct NibbleParams {
     const uint8_t *zeros;     // experts x N x groups, or null (8)
     const int32_t *offsets;   // experts + 1, or null (one expert has every row)
     void *c;                  // rows x N, 16-bit
+    uint64_t timeout_ns;
+    int32_t *status;
 };
 
-cudaError_t launch_nibble(int kind, const NibbleParams &p, int sms, cudaStream_t stream, bool overlap);
+constexpr int kNibFeatures = 32;   // features per CTA, rows of the weights' TMA box (128 bytes wide)
+
+cudaError_t launch_nibble(int kind, const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap);
 
 }  // namespace pts

@@ -214,6 +214,14 @@ __device__ __forceinline__ void tma_prefetch_2d(uint32_t pred, const void *tmap,
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(uint32_t pred, const void *tmap, int x, int y, int z)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+                 "@q cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%1, {%2, %3, %4}];\n\t}" ::"r"(pred),
+                 "l"(tmap), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // TMA store of a shared-memory box, only where `pred` is non-zero.
