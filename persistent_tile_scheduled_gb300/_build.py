@@ -22,7 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libpts_gemm.so")
 UNITS = ["gemm_cg1.cu", "gemm_cg2.cu", "gemm_narrow.cu", "gemm_narrow_cg2.cu", "gemm_api.cu", "gemm_noalloc.cu",
-         "peak_probe.cu", "expert_fwd.cu", "expert_dgrad.cu", "expert_wgrad.cu", "expert_route.cu", "nibble.cu",
+         "peak_probe.cu", "expert_fwd.cu", "expert_dgrad.cu", "expert_wgrad.cu", "expert_route.cu", "nibble_f16.cu",
+         "nibble_bf16.cu",
          "expert_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

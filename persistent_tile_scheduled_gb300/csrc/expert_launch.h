@@ -71,7 +71,7 @@ cudaError_t launch_expert_combine_grad(int kind, const void *dy, const void *ys,
                                        void *dys, float *dw, int tokens, int top_k, int chunks, cudaStream_t stream,
                                        bool overlap);
 
-// ---- few rows times 4-bit weights (nibble.cu) ---------------------------------
+// ---- few rows times 4-bit weights (nibble.cuh) ---------------------------------
 
 struct NibbleParams {
     int32_t rows, experts, N, K, group, groups;
@@ -81,12 +81,15 @@ struct NibbleParams {
     const uint8_t *zeros;     // experts x N x groups, or null (8)
     const int32_t *offsets;   // experts + 1, or null (one expert has every row)
     void *c;                  // rows x N, 16-bit
+    int32_t ctas;             // the grid: one CTA per SM
     uint64_t timeout_ns;
     int32_t *status;
 };
 
 constexpr int kNibFeatures = 32;   // features per CTA, rows of the weights' TMA box (128 bytes wide)
+constexpr int kNibStageK = 256;    // contraction per unit of work
 
-cudaError_t launch_nibble(int kind, const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap);
+cudaError_t launch_nibble_f16(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap);
+cudaError_t launch_nibble_bf16(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap);
 
 }  // namespace pts

@@ -1,0 +1,4 @@
+// Few rows times 4-bit weights, bf16 rows.
+#define PTS_NIBBLE_KIND 1
+#define PTS_NIBBLE_LAUNCH launch_nibble_bf16
+#include "nibble.cuh"

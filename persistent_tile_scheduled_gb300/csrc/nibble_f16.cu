@@ -1,0 +1,4 @@
+// Few rows times 4-bit weights, fp16 rows.
+#define PTS_NIBBLE_KIND 0
+#define PTS_NIBBLE_LAUNCH launch_nibble_f16
+#include "nibble.cuh"
