@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     const uint32_t full0 = bar0;                             // + 8*s
     const uint32_t empty0 = bar0 + 8 * kMaxStages;           // + 8*s
     const uint32_t fix0 = bar0 + 16 * kMaxStages;            // + 8*s (WGRAD)
-    const uint32_t acc_full0 = bar0 + 24 * kMaxStages;       // + 8*b
+    const uint32_t peer0 = bar0 + 24 * kMaxStages;           // + 8*s (WGRAD, leader)
+    const uint32_t acc_full0 = bar0 + 32 * kMaxStages;       // + 8*b
     const uint32_t acc_empty0 = acc_full0 + 16;              // + 8*b
     const uint32_t ring_full0 = acc_empty0 + 16;             // + 8*r
     const uint32_t ring_empty0 = ring_full0 + 8 * kRing;     // + 8*r
@@ -107,9 +108,12 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, CG);   // each CTA announces its own bytes
+            mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
-            mbar_init(fix0 + 8 * s, 1);
+            if (MODE == EXPERT_WGRAD) {
+                mbar_init(fix0 + 8 * s, 1);
+                mbar_init(peer0 + 8 * s, 1);
+            }
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
@@ -230,10 +234,9 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 const uint32_t fb = (fix ? fix0 : full0) + 8 * stage;
                 const bool pair = CG == 2 && !fix;
                 const uint32_t fbc = pair ? mapa(fb, 0u) : fb;
-                if (pair)
-                    mbar_arrive_expect_tx_cluster_if(one, fbc, tx);
-                else
-                    mbar_arrive_expect_tx_if(one, fb, tx);
+                // a pair's leader announces both CTAs' bytes; a stage that is cleared first
+                // is announced by each CTA to itself
+                if (!pair || leader) mbar_arrive_expect_tx_if(one, fb, pair ? CG * tx : tx);
                 for (int j = 0; j < nk; ++j) {
                     const uint32_t da = sA + stage * SA + j * (SA / KBS);
                     const uint32_t db = sB + stage * SB + j * (SB / KBS);
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
         // for this CTA's loads of it, clear the rows behind the end in both
         // operands, and hand the stage to the MMA warp.
         int stage = 0;
-        uint32_t phases = 0;   // bit s: the parity of fix barrier s that comes next
+        uint32_t phases = 0;   // bit s: the parity of fix (and peer) barrier s that comes next
         for (int i = 0;; ++i) {
             ExpertItem t;
             if (ring_read(i, t) <= 0) break;
@@ -531,7 +534,6 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             }
             const int s = (stage + stages_used - 1) % S;
             if (!ctl.wait_all(fix0 + 8 * s, (phases >> s) & 1u, WHERE_FULL)) break;
-            phases ^= 1u << s;
             const int j = (t.nkb - 1) % KBS;
             const uint32_t rem = static_cast<uint32_t>(t.c_rows - (t.nkb - 1) * KELEMS);   // 1 .. 63
             const uint32_t end = (rem + 15u) & ~15u;
@@ -546,10 +548,13 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (CG == 2)
-                mbar_arrive_cluster_if(one, mapa(full0 + 8 * s, 0u));
-            else
+            if (CG == 2 && !leader) {
+                mbar_arrive_cluster_if(one, mapa(peer0 + 8 * s, 0u));
+            } else {   // the stage is whole when the peer's part is cleared too
+                if (CG == 2 && !ctl.wait_all(peer0 + 8 * s, (phases >> s) & 1u, WHERE_FULL)) break;
                 mbar_arrive_if(one, full0 + 8 * s);
+            }
+            phases ^= 1u << s;
             stage = (stage + stages_used) % S;
         }
         __syncwarp();

@@ -117,15 +117,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t pred, uint32_t
                  : "memory");
 }
 
-// The same on a barrier given by its shared::cluster address (own or peer CTA).
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster_if(uint32_t pred, uint32_t cluster_bar, uint32_t bytes)
-{
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
-                 "@q mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%1], %2;\n\t}" ::"r"(pred),
-                 "r"(cluster_bar), "r"(bytes)
-                 : "memory");
-}
-
 // Non-blocking probe of phase `parity`; cluster-scope acquire so that arrivals
 // and async writes made by the peer CTA of a pair are visible afterwards.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
