@@ -82,14 +82,15 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     std::memset(&mw, 0, sizeof(mw));
     mx = mxs = mo = mw;
     bool ok = true;
+    const uint32_t stage_rows = static_cast<uint32_t>(64 * kb_per_stage(cg));   // contraction rows of a stage
     if (mode == EXPERT_WGRAD) {
-        ok = encode_map3(h, &mw, W, 1, rows, K, dtype, 64, 64) && encode_map3(h, &mx, X, 1, rows, N, dtype, 64, 64);
+        ok = encode_map3(h, &mw, W, 1, rows, K, dtype, stage_rows, 64) && encode_map3(h, &mx, X, 1, rows, N, dtype, stage_rows, 64);
         mxs = mx;
         ok = ok && encode_map3(h, &mo, out, experts, N, K, dtype, 64, 32);
     } else {
         if (contraction > 0) {
             ok = mode == EXPERT_FWD ? encode_map3(h, &mw, W, experts, N, K, dtype, kRowsPerCta, kelems)
-                                    : encode_map3(h, &mw, W, experts, N, K, dtype, 64, 64);
+                                    : encode_map3(h, &mw, W, experts, N, K, dtype, stage_rows, 64);
             ok = ok && encode_map3(h, &mx, X, 1, rows, contraction, dtype, static_cast<uint32_t>(bn / cg), kelems)
                  && encode_map3(h, &mxs, X, 1, rows, contraction, dtype, 16, kelems);
         }

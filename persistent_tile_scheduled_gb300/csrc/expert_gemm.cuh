@@ -45,12 +45,14 @@ struct ExpertItem {
     int c0, c_rows;             // WGRAD: first contraction row, contraction rows
 };
 
-// Shared-memory descriptor of an MN-major operand: 64-feature blocks 8192
-// bytes apart (64 contraction rows of 128 bytes), groups of 8 contraction rows
-// 1024 bytes apart, version 1, 128-byte swizzle.
+// Shared-memory descriptor of an MN-major operand: 64-feature blocks `rows`
+// contraction rows of 128 bytes apart, groups of 8 contraction rows 1024 bytes
+// apart, version 1, 128-byte swizzle.
+template <int ROWS>
 __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr)
 {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(ROWS * 128 / 16) << 16) | (64ull << 32)
+           | (1ull << 46) | (2ull << 61);
 }
 
 template <int KIND, int MODE, int CG, int BN>
@@ -59,18 +61,18 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                   const __grid_constant__ CUtensorMap tmXs, const __grid_constant__ CUtensorMap tmO,
                   const ExpertParams p)
 {
-    // tmW: boxes of 128 features x one k-block (MN-major: 64 x 64); tmX: boxes
-    // of BN / CG rows x one k-block, tmXs: of 16 rows (MN-major: both 64 x 64);
+    // tmW: boxes of 128 features x one k-block (MN-major: 64 features x a stage); tmX: boxes
+    // of BN / CG rows x one k-block, tmXs: of 16 rows (MN-major: both as tmW);
     // tmO: the store box, 32 features x 64 rows
     constexpr bool kWmn = MODE != EXPERT_FWD;     // the operand's features are contiguous, the contraction is not
     constexpr bool kXmn = MODE == EXPERT_WGRAD;
     constexpr int KBS = kb_per_stage(CG);
-    constexpr int SA = stage_bytes_a(CG);
-    constexpr int SB = stage_bytes_b(CG, BN);
+    constexpr int SA = KBS * kRowsPerCta * kKBlockBytes;
+    constexpr int SB = KBS * (BN / CG) * kKBlockBytes;
     constexpr int KELEMS = (KIND == 2) ? kKBlockBytes : kKBlockBytes / 2;
     constexpr int kXRows = BN / CG;               // this CTA's share of a tile's accumulator columns
     constexpr int kGran = 16 * CG;
-    constexpr uint32_t kBlock = 64 * 128;         // an MN-major block: 64 contraction rows of 128 bytes
+    constexpr uint32_t kBlock = KBS * 64 * 128;   // an MN-major block: a stage's contraction rows of 128 bytes
     constexpr uint32_t kAccCols = 2 * BN;
 
     extern __shared__ uint8_t smem_raw[];
@@ -228,7 +230,9 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                     break;
                 }
                 const int nk = t.nkb - kb < KBS ? t.nkb - kb : KBS;
-                const uint32_t tx = static_cast<uint32_t>(nk) * (SA / KBS + static_cast<uint32_t>(xloads) * xbox);
+                // (an MN-major box always spans the stage; rows behind the contraction are not read)
+                const uint32_t tx = (kWmn ? SA : static_cast<uint32_t>(nk) * (SA / KBS))
+                                    + static_cast<uint32_t>(kXmn ? xloads : nk * xloads) * xbox;
                 // a stage that ends inside a 16-row step first goes to the clearing warp of this CTA
                 const bool fix = kXmn && kb + KBS >= t.nkb && (t.c_rows & 15) != 0;
                 const uint32_t fb = (fix ? fix0 : full0) + 8 * stage;
@@ -237,33 +241,27 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 // a pair's leader announces both CTAs' bytes; a stage that is cleared first
                 // is announced by each CTA to itself
                 if (!pair || leader) mbar_arrive_expect_tx_if(one, fb, pair ? CG * tx : tx);
-                for (int j = 0; j < nk; ++j) {
-                    const uint32_t da = sA + stage * SA + j * (SA / KBS);
-                    const uint32_t db = sB + stage * SB + j * (SB / KBS);
-                    const int c = (kb + j) * KELEMS;
-                    auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
-                        if (pair)
-                            tma_load_3d_pair(one, dst, m, fbc, x, y, z);
-                        else
-                            tma_load_3d(one, dst, m, fbc, x, y, z);
-                    };
-                    if constexpr (MODE == EXPERT_FWD) {
-                        load(da, &tmW, c, wf, t.e);
-                    } else {
+                auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
+                    if (pair)
+                        tma_load_3d_pair(one, dst, m, fbc, x, y, z);
+                    else
+                        tma_load_3d(one, dst, m, fbc, x, y, z);
+                };
+                const uint32_t da = sA + stage * SA, db = sB + stage * SB;
+                const int c = kb * KELEMS;
+                if constexpr (kWmn) {
 #pragma unroll
-                        for (int b = 0; b < kRowsPerCta / 64; ++b) {
-                            if constexpr (MODE == EXPERT_DGRAD)
-                                load(da + b * kBlock, &tmW, wf + 64 * b, c, t.e);
-                            else
-                                load(da + b * kBlock, &tmW, wf + 64 * b, t.c0 + c, 0);
-                        }
-                    }
-                    for (int b = 0; b < xloads; ++b) {
-                        if constexpr (kXmn)
-                            load(db + b * kBlock, mx, xrow + 64 * b, t.c0 + c, 0);
-                        else
-                            load(db + b * xbox, mx, c, xrow + 16 * b, 0);
-                    }
+                    for (int b = 0; b < kRowsPerCta / 64; ++b)
+                        load(da + b * kBlock, &tmW, wf + 64 * b, t.c0 + c, MODE == EXPERT_DGRAD ? t.e : 0);
+                } else {
+                    for (int j = 0; j < nk; ++j) load(da + j * (SA / KBS), &tmW, c + j * KELEMS, wf, t.e);
+                }
+                if constexpr (kXmn) {
+                    for (int b = 0; b < xloads; ++b) load(db + b * kBlock, mx, xrow + 64 * b, t.c0 + c, 0);
+                } else {
+                    for (int j = 0; j < nk; ++j)
+                        for (int b = 0; b < xloads; ++b)
+                            load(db + j * (SB / KBS) + b * xbox, mx, c + j * KELEMS, xrow + 16 * b, 0);
                 }
                 ++issued;
                 if (++stage == S) {
@@ -319,10 +317,11 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
 #pragma unroll
                     for (int j = 0; j < KBS; ++j) {
                         if (j >= nk) break;
-                        const uint32_t aa = sA + stage * SA + j * (SA / KBS);
-                        const uint32_t ab = sB + stage * SB + j * (SB / KBS);
-                        const uint64_t ad = kWmn ? smem_desc_mn_sw128(aa) : smem_desc_sw128(aa);
-                        const uint64_t bd = kXmn ? smem_desc_mn_sw128(ab) : smem_desc_sw128(ab);
+                        // (the next k-block of an MN-major stage: 64 rows on in every block)
+                        const uint32_t aa = sA + stage * SA + j * (kWmn ? 64 * 128 : SA / KBS);
+                        const uint32_t ab = sB + stage * SB + j * (kXmn ? 64 * 128 : SB / KBS);
+                        const uint64_t ad = kWmn ? smem_desc_mn_sw128<64 * KBS>(aa) : smem_desc_sw128(aa);
+                        const uint64_t bd = kXmn ? smem_desc_mn_sw128<64 * KBS>(ab) : smem_desc_sw128(ab);
                         // an instruction takes 32 bytes of a K-major row, or 16 contraction rows of 128 bytes
                         constexpr uint64_t da = kWmn ? 128 : 2, db = kXmn ? 128 : 2;
                         int steps = 4;
@@ -534,14 +533,13 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             }
             const int s = (stage + stages_used - 1) % S;
             if (!ctl.wait_all(fix0 + 8 * s, (phases >> s) & 1u, WHERE_FULL)) break;
-            const int j = (t.nkb - 1) % KBS;
-            const uint32_t rem = static_cast<uint32_t>(t.c_rows - (t.nkb - 1) * KELEMS);   // 1 .. 63
+            // rows of the stage that are the expert's, up to the end of their last step
+            const uint32_t rem = static_cast<uint32_t>(t.c_rows - (stages_used - 1) * KBS * KELEMS);
             const uint32_t end = (rem + 15u) & ~15u;
             const int xblocks = (t.n_len / CG + 63) / 64;
             for (int b = 0; b < kRowsPerCta / 64 + xblocks; ++b) {
-                const uint32_t blk = b < kRowsPerCta / 64
-                                         ? sA + s * SA + j * (SA / KBS) + b * kBlock
-                                         : sB + s * SB + j * (SB / KBS) + (b - kRowsPerCta / 64) * kBlock;
+                const uint32_t blk = b < kRowsPerCta / 64 ? sA + s * SA + b * kBlock
+                                                          : sB + s * SB + (b - kRowsPerCta / 64) * kBlock;
                 // rows of 128 bytes: 8 lanes to a row, 4 rows at a time
                 for (uint32_t r = rem + (lane >> 3); r < end; r += 4)
                     st_shared_v4(blk + r * 128 + (lane & 7u) * 16, 0u, 0u, 0u, 0u);
