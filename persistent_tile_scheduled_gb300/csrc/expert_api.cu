@@ -287,7 +287,7 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     CUtensorMap mb;
     std::memset(&mb, 0, sizeof(mb));
     if (K > 0 && !encode_map3(h, &mb, B, 1, experts * N, K / 2, GEMM_E4M3, kNibFeatures, 128)) return GEMM_ERR_INVALID_ARG;
-    return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, static_cast<cudaStream_t>(stream), overlap(h)));
+    return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, &h->nibble_prepared, static_cast<cudaStream_t>(stream), overlap(h)));
 }
 
 }  // extern "C"

@@ -89,7 +89,10 @@ struct NibbleParams {
 constexpr int kNibFeatures = 32;   // features per CTA, rows of the weights' TMA box (128 bytes wide)
 constexpr int kNibStageK = 256;    // contraction per unit of work
 
-cudaError_t launch_nibble_f16(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap);
-cudaError_t launch_nibble_bf16(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap);
+// prepared: the device's kernels whose shared-memory limit is raised, a bit each
+cudaError_t launch_nibble_f16(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream,
+                              bool overlap);
+cudaError_t launch_nibble_bf16(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream,
+                               bool overlap);
 
 }  // namespace pts

@@ -171,27 +171,71 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Xs[row_of[t, j]] = X[t]: a block per token, 16 bytes per thread and step,
-// read once and written top_k times.
-__global__ void __launch_bounds__(256) expert_gather_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ row_of,
-                                                            uint4 *__restrict__ xs, int tokens, int top_k, int chunks)
+// The copy below is bound by the rows' bytes, most of them written.  Every thread takes
+// PIECES 16-byte pieces, kRowThreads apart in the tokens' pieces counted
+// through: rows of any length fill whole blocks, and the loads of all its
+// pieces (and of 4 assignments of each) are on their way together.
+constexpr int kRowThreads = 256;
+constexpr int kGatherPieces = 2;
+
+// Token and place in it of piece i (0 .. PIECES - 1) of this thread.
+struct Piece {
+    long long token;
+    int at;
+};
+
+template <int PIECES>
+__device__ __forceinline__ void pieces_of(int tokens, int chunks, Piece (&q)[PIECES], bool (&there)[PIECES])
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const long long t = blockIdx.x;
-    const long long n = static_cast<long long>(tokens) * top_k;
-    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-        const uint4 v = x[t * chunks + c];
-        for (int j = 0; j < top_k; ++j) {
-            const int32_t r = row_of[t * top_k + j];
-            if (r >= 0 && r < n) xs[static_cast<long long>(r) * chunks + c] = v;
-        }
+    const long long first = static_cast<long long>(blockIdx.x) * (kRowThreads * PIECES);
+    const long long t0 = first / chunks;
+    const uint32_t rest = static_cast<uint32_t>(first - t0 * chunks) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const uint32_t local = rest + i * kRowThreads, over = local / static_cast<uint32_t>(chunks);
+        q[i].token = t0 + over;
+        q[i].at = static_cast<int>(local - over * chunks);
+        there[i] = q[i].token < tokens;
     }
 }
 
-// Y[t] = sum_j w[t, j] Ys[row_of[t, j]], in 32 bits in the order of j.
-template <int KIND>
-__global__ void __launch_bounds__(256)
+// Xs[row_of[t, j]] = X[t]: a row is read once and written top_k times.
+__global__ void __launch_bounds__(kRowThreads)
+    expert_gather_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ row_of, uint4 *__restrict__ xs,
+                         int tokens, int top_k, int chunks)
+{
+    pdl_launch_dependents();
+    const long long n = static_cast<long long>(tokens) * top_k;
+    Piece q[kGatherPieces];
+    bool there[kGatherPieces];
+    pieces_of(tokens, chunks, q, there);
+    pdl_wait();
+    uint4 v[kGatherPieces];
+#pragma unroll
+    for (int i = 0; i < kGatherPieces; ++i)
+        if (there[i]) v[i] = __ldcs(x + q[i].token * chunks + q[i].at);
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+        int32_t r[kGatherPieces][4];
+#pragma unroll
+        for (int i = 0; i < kGatherPieces; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[i][j] = there[i] && j0 + j < top_k ? __ldg(row_of + q[i].token * top_k + j0 + j) : -1;
+#pragma unroll
+        for (int i = 0; i < kGatherPieces; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r[i][j] >= 0 && r[i][j] < n) xs[static_cast<long long>(r[i][j]) * chunks + q[i].at] = v[i];
+    }
+}
+
+// Y[t] = sum_j w[t, j] Ys[row_of[t, j]], in 32 bits in the order of j.  A block
+// per token, S pieces per thread: a token's rows are looked up once, and S
+// pieces of two of its rows are on their way together.  (A thread per piece of
+// all tokens, as in the copy, looks rows up for every piece: 24 us where this
+// takes 18.4; 104 MB.)
+template <int KIND, int S>
+__global__ void __launch_bounds__(kRowThreads)
     expert_combine_kernel(const uint4 *__restrict__ ys, const int32_t *__restrict__ row_of, const float *__restrict__ w,
                           uint4 *__restrict__ y, int tokens, int top_k, int chunks)
 {
@@ -199,18 +243,42 @@ __global__ void __launch_bounds__(256)
     pdl_wait();
     const long long t = blockIdx.x;
     const long long n = static_cast<long long>(tokens) * top_k;
-    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-        float acc[8] = {};
-        for (int j = 0; j < top_k; ++j) {
-            const int32_t r = row_of[t * top_k + j];
-            if (r < 0 || r >= n) continue;
-            float f[8];
-            unpack8<KIND>(ys[static_cast<long long>(r) * chunks + c], f);
-            const float s = w ? w[t * top_k + j] : 1.0f;
+    for (int c0 = threadIdx.x; c0 < chunks; c0 += S * blockDim.x) {
+        float acc[S][8] = {};
+        for (int j = 0; j < top_k; j += 2) {
+            int32_t r[2];
+            float f[2] = {1.0f, 1.0f};
+            uint4 v[2][S];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(s, f[i], acc[i]);
+            for (int i = 0; i < 2; ++i) {
+                r[i] = j + i < top_k ? __ldg(row_of + t * top_k + j + i) : -1;
+                if (r[i] >= n) r[i] = -1;
+                if (w && j + i < top_k) f[i] = __ldg(w + t * top_k + j + i);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const int c = c0 + s * static_cast<int>(blockDim.x);
+                    if (r[i] >= 0 && c < chunks) v[i][s] = __ldcs(ys + static_cast<long long>(r[i]) * chunks + c);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (r[i] >= 0) {
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        float x[8];
+                        unpack8<KIND>(v[i][s], x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[s][e] = fmaf(f[i], x[e], acc[s][e]);
+                    }
+                }
         }
-        y[t * chunks + c] = pack8<KIND>(acc);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int c = c0 + s * static_cast<int>(blockDim.x);
+            if (c < chunks) y[t * chunks + c] = pack8<KIND>(acc[s]);
+        }
     }
 }
 
@@ -285,7 +353,13 @@ cudaError_t go(void (*kernel)(P...), long long grid, int block, size_t smem, int
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// threads of a row kernel: one 16-byte chunk each, up to 256
+// blocks of the kernels over all pieces
+long long piece_blocks(long long tokens, long long chunks, int pieces)
+{
+    return (tokens * chunks + kRowThreads * pieces - 1) / (kRowThreads * pieces);
+}
+
+// threads of a block per token: one 16-byte chunk each, up to 256
 int row_threads(int chunks) { return chunks >= 256 ? 256 : (chunks + 31) / 32 * 32; }
 
 }  // namespace
@@ -310,15 +384,35 @@ cudaError_t launch_expert_sort(const int32_t *ids, int64_t n, int experts, int32
 cudaError_t launch_expert_gather(const void *x, const int32_t *row_of, void *xs, int tokens, int top_k, int chunks,
                                  cudaStream_t stream, bool overlap)
 {
-    return go(expert_gather_kernel, tokens, row_threads(chunks), 0, 1, stream, overlap, static_cast<const uint4 *>(x),
+    return go(expert_gather_kernel, piece_blocks(tokens, chunks, kGatherPieces), kRowThreads, 0, 1, stream, overlap, static_cast<const uint4 *>(x),
               row_of, static_cast<uint4 *>(xs), tokens, top_k, chunks);
 }
 
 cudaError_t launch_expert_combine(int kind, const void *ys, const int32_t *row_of, const float *w, void *y, int tokens,
                                   int top_k, int chunks, cudaStream_t stream, bool overlap)
 {
-    return go(kind == 0 ? expert_combine_kernel<0> : expert_combine_kernel<1>, tokens, row_threads(chunks), 0, 1, stream,
-              overlap, static_cast<const uint4 *>(ys), row_of, w, static_cast<uint4 *>(y), tokens, top_k, chunks);
+    // Pieces per thread: as leave the fewest idle, the most of those (528 pieces
+    // of 16 bytes: 3 x 192 threads take 18.4 us, 4 x 160 take 20.3, 2 rounds of
+    // 2 x 256 take 21.8).  At most 2 where tokens are few, so that more warps
+    // share a token (64 tokens of 8 rows of 8 KB: 3.3 us, with 4 pieces 4.1).
+    int best = 1, best_threads = 32;
+    long long least = -1;
+    for (int s = 1; s <= (tokens <= 512 ? 2 : 4); ++s) {
+        int threads = ((chunks + s - 1) / s + 31) / 32 * 32;
+        threads = threads > kRowThreads ? kRowThreads : threads;
+        const long long slots = (chunks + s * threads - 1) / (s * threads) * static_cast<long long>(s) * threads;
+        if (least < 0 || slots <= least) least = slots, best = s, best_threads = threads;
+    }
+    const auto run = [&](auto kernel) {
+        return go(kernel, tokens, best_threads, 0, 1, stream, overlap, static_cast<const uint4 *>(ys), row_of, w,
+                  static_cast<uint4 *>(y), tokens, top_k, chunks);
+    };
+    switch (best) {
+    case 1: return run(kind == 0 ? expert_combine_kernel<0, 1> : expert_combine_kernel<1, 1>);
+    case 2: return run(kind == 0 ? expert_combine_kernel<0, 2> : expert_combine_kernel<1, 2>);
+    case 3: return run(kind == 0 ? expert_combine_kernel<0, 3> : expert_combine_kernel<1, 3>);
+    default: return run(kind == 0 ? expert_combine_kernel<0, 4> : expert_combine_kernel<1, 4>);
+    }
 }
 
 cudaError_t launch_expert_combine_grad(int kind, const void *dy, const void *ys, const int32_t *row_of, const float *w,

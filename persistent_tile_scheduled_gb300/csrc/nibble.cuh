@@ -457,13 +457,17 @@ cudaError_t go(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
 }
 
 template <int KIND, int GC, bool VEC>
-cudaError_t run(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap)
+cudaError_t run(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream, bool overlap)
 {
     constexpr int smem = 1024 + kNibWarps * kNibRing * (kNibStageBytes + 8);
     static_assert(kNibRing * kNibStageBytes >= kNibFeatures * (kNibRows + 1) * 4, "the sums fit in the ring");
     const auto kernel = p.zeros ? nibble_kernel<KIND, GC, VEC, true> : nibble_kernel<KIND, GC, VEC, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    const uint32_t bit = 1u << (((KIND * 3 + GC / 2) * 2 + VEC) * 2 + (p.zeros ? 1 : 0));   // (GC / 2: 0, 1, 2)
+    if (!(*prepared & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        *prepared |= bit;
+    }
     // at most `rows` experts have rows
     const int64_t experts = p.offsets ? (p.experts < p.rows ? p.experts : p.rows) : 1;
     const int64_t ctas = (static_cast<int64_t>(p.N) + kNibFeatures - 1) / kNibFeatures * experts;
@@ -472,20 +476,20 @@ cudaError_t run(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream
 }
 
 template <int KIND, int GC>
-cudaError_t by_alignment(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap)
+cudaError_t by_alignment(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream, bool overlap)
 {
-    return p.groups % NibScales<GC>::kGroups == 0 ? run<KIND, GC, true>(b, p, stream, overlap)
-                                                  : run<KIND, GC, false>(b, p, stream, overlap);
+    return p.groups % NibScales<GC>::kGroups == 0 ? run<KIND, GC, true>(b, p, prepared, stream, overlap)
+                                                  : run<KIND, GC, false>(b, p, prepared, stream, overlap);
 }
 
 }  // namespace
 
 // (one translation unit per kind: expert_launch.h names the two)
-cudaError_t PTS_NIBBLE_LAUNCH(const CUtensorMap &b, const NibbleParams &p, cudaStream_t stream, bool overlap)
+cudaError_t PTS_NIBBLE_LAUNCH(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream, bool overlap)
 {
-    return p.group == 32 ? by_alignment<PTS_NIBBLE_KIND, 1>(b, p, stream, overlap)
-           : p.group == 64 ? by_alignment<PTS_NIBBLE_KIND, 2>(b, p, stream, overlap)
-                           : by_alignment<PTS_NIBBLE_KIND, 4>(b, p, stream, overlap);
+    return p.group == 32 ? by_alignment<PTS_NIBBLE_KIND, 1>(b, p, prepared, stream, overlap)
+           : p.group == 64 ? by_alignment<PTS_NIBBLE_KIND, 2>(b, p, prepared, stream, overlap)
+                           : by_alignment<PTS_NIBBLE_KIND, 4>(b, p, prepared, stream, overlap);
 }
 
 }  // namespace pts

@@ -18,7 +18,7 @@ _OUT = {GEMM_F16: torch.float16, GEMM_BF16: torch.bfloat16, GEMM_E4M3: torch.bfl
 
 def _arg(x, dtype, count, what):
     """Address of `x`; a tensor must be a contiguous CUDA tensor of `dtype` with at least `count` elements."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     if x.dtype is not dtype or not x.is_cuda or not x.is_contiguous() or x.numel() < count:
         raise GemmError(GEMM_ERR_INVALID_ARG,
