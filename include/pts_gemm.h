@@ -404,7 +404,7 @@ gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t expe
  *   offsets: as above, or NULL with experts == 1 (every row uses that matrix).
  * group: 32, 64 or 128 (the last group may be short); K % 32 == 0, N % 8 == 0.
  * Products are exact and sums fp32.  Made for a few rows per expert: the cost is
- * the weights' bytes, read once for every 16 rows of an expert. */
+ * the weights' bytes, read once for every 8 rows of an expert. */
 gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,
                               const void *A, const void *B, const void *scales, const uint8_t *zeros,
                               const int32_t *offsets, void *C, gemm_dtype_t dtype, void *stream);

@@ -261,8 +261,8 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     if ((offsets == nullptr && experts != 1) || !aligned4(offsets)) return GEMM_ERR_INVALID_ARG;
     if (experts > kLim / N) return GEMM_ERR_INVALID_ARG;   // rows of the weights
     // the kernel counts its pieces of work in 32 bits
-    const double blocks = double(rows) / 16 + double(rows < experts ? rows : experts);
-    if (blocks * (double(N) / 32 + 1) * (double(K) / 256 + 1) > 2e9) return GEMM_ERR_INVALID_ARG;
+    const double blocks = double(rows) / 8 + double(rows < experts ? rows : experts);
+    if (blocks * (double(N) / 16 + 1) > 2e9) return GEMM_ERR_INVALID_ARG;
     if (C == nullptr || !aligned16(C)) return GEMM_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || B == nullptr || scales == nullptr)) return GEMM_ERR_INVALID_ARG;
     if (!aligned16(A) || !aligned16(B) || !aligned16(scales) || !aligned16(zeros)) return GEMM_ERR_INVALID_ARG;
@@ -287,7 +287,7 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     CUtensorMap mb;
     std::memset(&mb, 0, sizeof(mb));
     if (K > 0 && !encode_map3(h, &mb, B, 1, experts * N, K / 2, GEMM_E4M3, kNibFeatures, 128)) return GEMM_ERR_INVALID_ARG;
-    return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, &h->nibble_prepared, static_cast<cudaStream_t>(stream), overlap(h)));
+    return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, &h->nibble[dtype], static_cast<cudaStream_t>(stream), overlap(h)));
 }
 
 }  // extern "C"

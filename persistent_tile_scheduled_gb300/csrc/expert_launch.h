@@ -81,18 +81,26 @@ struct NibbleParams {
     const uint8_t *zeros;     // experts x N x groups, or null (8)
     const int32_t *offsets;   // experts + 1, or null (one expert has every row)
     void *c;                  // rows x N, 16-bit
-    int32_t ctas;             // the grid: one CTA per SM
+    int32_t ctas;             // SMs
+    int32_t cluster, k_warps; // set by the launch: CTAs and warps of a CTA that share a contraction
     uint64_t timeout_ns;
     int32_t *status;
 };
 
-constexpr int kNibFeatures = 32;   // features per CTA, rows of the weights' TMA box (128 bytes wide)
+constexpr int kNibFeatures = 32;   // features of a tile, rows of the weights' TMA box (128 bytes wide)
 constexpr int kNibStageK = 256;    // contraction per unit of work
+constexpr int kNibMaxCtas = 4;     // CTAs of a cluster
 
-// prepared: the device's kernels whose shared-memory limit is raised, a bit each
-cudaError_t launch_nibble_f16(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream,
+// What a handle keeps per dtype: the kernels whose shared-memory limit is
+// raised (a bit each), and the clusters of 2 and 4 CTAs the device holds.
+struct NibPrepared {
+    uint32_t kernels;
+    int clusters[2];
+};
+
+cudaError_t launch_nibble_f16(const CUtensorMap &b, const NibbleParams &p, NibPrepared *prepared, cudaStream_t stream,
                               bool overlap);
-cudaError_t launch_nibble_bf16(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream,
+cudaError_t launch_nibble_bf16(const CUtensorMap &b, const NibbleParams &p, NibPrepared *prepared, cudaStream_t stream,
                                bool overlap);
 
 }  // namespace pts

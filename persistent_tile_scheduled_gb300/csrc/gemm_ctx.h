@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/pts_gemm.h"
+#include "expert_launch.h"
 #include "gemm_params.h"
 
 namespace pts {
@@ -73,7 +74,7 @@ struct gemm_ctx {
     // experts' products: resident clusters per dtype, mode and variant (0: single CTAs, 1: pairs,
     // 2: single CTAs with the short row tile); 0 = not asked yet
     int expert_clusters[3][3][3] = {};
-    uint32_t nibble_prepared = 0;             // gemm_run_nibble: kernels whose shared-memory limit is raised
+    pts::NibPrepared nibble[2] = {};          // gemm_run_nibble, per dtype
 };
 
 namespace pts {

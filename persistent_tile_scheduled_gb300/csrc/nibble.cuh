@@ -19,15 +19,24 @@
 // the rows cut into e4m3 digits; that is exact too, but the instruction first
 // unpacks both operands to fp16: 71 us where this form took 41.)
 //
-// A CTA takes 32 features of one expert (or the one matrix); its 8 warps share
-// the contraction in whole units of 256 and add their sums up in shared memory
-// in a fixed order.  Each warp has a ring of units of its own, filled by TMA
-// (4 KB: 32 features x 128 contiguous bytes): the MMA wants thread t of a quad
-// to hold the 8 weights that are word t of a 16-byte chunk, where a thread's
-// own 16-byte load would hold 32 consecutive weights, whose quad spans 128 and
-// so up to four groups.  The 128-byte swizzle puts chunk c of row r at
-// c ^ (r % 8): no bank conflicts.  Two CTAs per SM keep the loads of one going
-// while the other starts or adds up.
+// The grid is one CTA of 16 warps per SM, and stays: features rarely divide
+// into 152 equal parts (16384 of them, 32 at a time, leave 16 % of the SMs idle
+// in the last round), so each taker gets an equal stretch of blocks of 16
+// features, which it walks 32 at a time.  The warps of a taker share the
+// contraction, a unit of 256 each: a warp then meets the same values of the
+// rows tile after tile and holds them in registers, where loading them for
+// every tile cost as many bytes from L2 as the weights.  A taker is a cluster
+// of 1, 2 or 4 CTAs, so that K up to 16384 has a warp per unit; for K below 4096
+// a CTA holds several takers.  (A CTA per 32 features and 8 warps, with the
+// rows loaded as they are needed: V7US us where this takes V8US; 8 rows, 16384 x
+// 8192, groups of 32 with zeros.)
+// Weights arrive by TMA, 32 features x 128 contiguous bytes per unit: the MMA
+// wants thread t of a quad to hold the 8 weights that are word t of a 16-byte
+// chunk, where a thread's own 16-byte load would hold 32 consecutive weights,
+// whose quad spans 128 and so up to four groups.  The 128-byte swizzle puts
+// chunk c of row r at c ^ (r % 8): no bank conflicts.  The warps' sums of a tile
+// meet in shared memory, those of a cluster's CTAs in the first one's, in a
+// fixed order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,10 +48,13 @@ namespace pts {
 
 namespace {
 
-constexpr int kNibWarps = 8;
-constexpr int kNibRing = 3;             // units in flight per warp
+constexpr int kNibWarps = 16;
+constexpr int kNibRing = 2;             // units in flight per warp
+constexpr int kNibRows = 8;             // rows at a time: one MMA's
+constexpr int kNibSlots = 8;            // tiles whose sums a cluster gathers before they are stored
 constexpr int kNibStageBytes = kNibFeatures * kNibStageK / 2;
-constexpr int kNibRows = 16;            // rows at a time
+constexpr int kNibPitch = kNibFeatures + 4;           // floats between rows of a tile's sums: no bank conflicts
+constexpr int kNibSums = kNibRows * kNibPitch;
 
 __device__ __forceinline__ uint32_t lds_u32(uint32_t addr)
 {
@@ -51,12 +63,38 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t addr)
     return v;
 }
 
-template <int KIND>
-__device__ __forceinline__ float widen(uint32_t bits)
+__device__ __forceinline__ float lds_f32(uint32_t addr)
 {
-    const uint16_t v = static_cast<uint16_t>(bits);
-    if constexpr (KIND == 0) return __half2float(*reinterpret_cast<const __half *>(&v));
-    else return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(&v));
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// the low (0) or high (1) half of `pair`
+template <int KIND>
+__device__ __forceinline__ float widen(uint32_t pair, int half)
+{
+    if constexpr (KIND == 0) {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&pair);
+        return half ? __high2float(h) : __low2float(h);
+    } else {
+        return __uint_as_float(half ? pair & 0xffff0000u : pair << 16);
+    }
 }
 
 // (a & b) | c
@@ -202,204 +240,38 @@ __device__ __forceinline__ NibScales<GC> ld_scales(const uint16_t *sp, const uin
     return r;
 }
 
-// Chunks of 32 of the rows' values that are on their way while the ones before
-// them are used.
-constexpr int kAhead = 2;
+// Blocks of 16 features are counted through the row blocks of all experts; a
+// taker's stretch of them is walked row block by row block.
+struct NibBlock {
+    int e, r0, cnt;    // its expert and rows
+};
 
-// The groups of half a unit (4 chunks of 32), times the rows:
-// acc += scale * (rows . (q - z)).  ALL: it has its 4 chunks, x holds the first
-// of them and, on return, those at xn; else the contraction ends in it and it
-// has `here`.  buf: chunk c of this thread's row is at buf ^ (c << 4).  xp: this
-// lane's row per block of 8.
-template <int KIND, int NT, int GC, bool ZEROS, bool ALL>
-__device__ __forceinline__ void half_sums(float (&acc)[NT][2][4], uint32_t buf, int g, uint4 (&x)[kAhead][NT],
-                                          const uint16_t *const (&xp)[NT], const uint16_t *const (&xn)[NT],
-                                          const NibScales<GC> &sc, int here)
+// A tile whose sums wait to be stored.
+struct NibTile {
+    int n0, features, r0, cnt;
+};
+
+// Row blocks of all experts.  Called by a whole warp.
+__device__ __forceinline__ int nib_blocks(const NibbleParams &p)
 {
-#pragma unroll
-    for (int gi = 0; gi < 4 / GC; ++gi) {
-        if (!ALL && gi * GC >= here) break;
-        // the four features of this thread: g, g + 8, g + 16, g + 24
-        float f[4];
-        uint32_t zv[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            f[q] = widen<KIND>(__shfl_sync(0xffffffffu, sc.s[gi / 2], g + 8 * q) >> (16 * (gi & 1)));
-            zv[q] = zero_bits<KIND>(0x08080808u, 0);
-            if constexpr (ZEROS) zv[q] = zero_bits<KIND>(__shfl_sync(0xffffffffu, sc.z[0], g + 8 * q), gi);
+    if (!p.offsets) return (p.rows + kNibRows - 1) / kNibRows;
+    int n = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 32) {
+        const int i = e0 + static_cast<int>(lane_id());
+        if (i < p.experts) {
+            const int a = max(0, min(__ldg(p.offsets + i), p.rows)), b = max(a, min(__ldg(p.offsets + i + 1), p.rows));
+            n += (b - a + kNibRows - 1) / kNibRows;
         }
-        float part[NT][2][4];
-#pragma unroll
-        for (int ci = 0; ci < GC; ++ci) {
-            const int c = gi * GC + ci;
-            if (!ALL && ci > 0 && c >= here) break;
-            const uint32_t from = buf ^ (static_cast<uint32_t>(c) << 4);
-            uint32_t w[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) expand<KIND>(lds_u32(from + q * 1024), zv[q], w[q]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                uint4 v;
-                if constexpr (ALL) {
-                    v = x[c % kAhead][j];
-                    x[c % kAhead][j] = ld_row(c + kAhead < 4 ? xp[j] + (c + kAhead) * 32 : xn[j] + (c + kAhead - 4) * 32);
-                } else {
-                    v = ld_row(xp[j] + c * 32);
-                }
-                // pairs (0, 4), (1, 5), (2, 6), (3, 7), as expand() leaves the weights
-                const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
-                const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    if (ci == 0)
-                        mma16816<KIND, true>(part[j][m], w[2 * m][0], w[2 * m + 1][0], w[2 * m][1], w[2 * m + 1][1], b0, b1);
-                    else
-                        mma16816<KIND, false>(part[j][m], w[2 * m][0], w[2 * m + 1][0], w[2 * m][1], w[2 * m + 1][1], b0, b1);
-                    mma16816<KIND, false>(part[j][m], w[2 * m][2], w[2 * m + 1][2], w[2 * m][3], w[2 * m + 1][3], b2, b3);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float &to = acc[j][q >> 1][2 * (q & 1) + k];
-                    to = fmaf(f[q], part[j][q >> 1][2 * (q & 1) + k], to);
-                }
     }
+    return __reduce_add_sync(0xffffffffu, n);
 }
 
-// Rows r0 .. r0 + cnt - 1 of the expert at rows row_b .. of the weights, cnt at
-// most 8 NT.  GC: chunks of 32 per group (group / 32).
-template <int KIND, int NT, int GC, bool VEC, bool ZEROS>
-__device__ __forceinline__ void nib_rows(const CUtensorMap &tmB, const NibbleParams &p, uint32_t ring, uint32_t bars,
-                                         uint32_t &phases, float *sums, int n0, int row_b, int r0, int cnt)
+// Expert and rows of a row block.  Called by a whole warp.
+__device__ __forceinline__ NibBlock nib_block(int block, const NibbleParams &p)
 {
-    constexpr int kGroups = NibScales<GC>::kGroups;
-    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id()), g = lane >> 2;
-    const uint32_t one = lane == 0 ? 1u : 0u;
-    const int units = (p.K + kNibStageK - 1) / kNibStageK;
-    const int s0 = units * warp / kNibWarps, s1 = units * (warp + 1) / kNibWarps;
-    auto load = [&](int s, int i) {
-        if (s < s1) {
-            mbar_arrive_expect_tx_if(one, bars + 8 * i, kNibStageBytes);
-            tma_load_3d(one, ring + i * kNibStageBytes, &tmB, bars + 8 * i, s * 128, row_b, 0);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < kNibRing; ++i) load(s0 + i, i);
-
-    float acc[NT][2][4] = {};
-    if (s0 < s1) {
-        // rows that are not there read the last one's values: their sums are not stored
-        const uint16_t *xp[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            xp[j] = static_cast<const uint16_t *>(p.a) + static_cast<long long>(r0 + min(8 * j + g, cnt - 1)) * p.K
-                    + static_cast<long long>(s0) * kNibStageK + (lane & 3) * 8;
-        // scales of this lane's feature (of the last one, where there is none)
-        const long long at = static_cast<long long>(row_b + min(lane, p.N - 1 - n0)) * p.groups;
-        const uint16_t *sp = static_cast<const uint16_t *>(p.scales) + at;
-        const uint8_t *zp = p.zeros + at;
-        NibScales<GC> next = ld_scales<GC, VEC, ZEROS>(sp, zp, s0 * kGroups, p.groups);
-        const int full = min(p.K / kNibStageK, s1);   // whole units end here
-        uint4 x[kAhead][NT] = {};
-        if (s0 < full) {
-#pragma unroll
-            for (int c = 0; c < kAhead; ++c)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) x[c][j] = ld_row(xp[j] + c * 32);
-        }
-        int i = 0;
-#pragma unroll 1
-        for (int s = s0; s < s1; ++s) {
-            NibScales<GC> sc = next;
-            next = ld_scales<GC, VEC, ZEROS>(sp, zp, min(s + 1, s1 - 1) * kGroups, p.groups);
-            if (!wait(bars + 8 * i, (phases >> i) & 1u, p)) break;
-            phases ^= 1u << i;
-            uint32_t buf = ring + i * kNibStageBytes + g * 144 + (lane & 3) * 4;
-            // two halves, in a loop: half the code to fetch where a warp has but a unit or two
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                if (s < full) {
-                    // where no whole unit follows, what is fetched ahead is not used
-                    const uint16_t *xn[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) xn[j] = h == 0 || s + 1 < full ? xp[j] + kNibStageK / 2 : xp[j];
-                    half_sums<KIND, NT, GC, ZEROS, true>(acc, buf, g, x, xp, xn, sc, 4);
-                } else {
-                    half_sums<KIND, NT, GC, ZEROS, false>(acc, buf, g, x, xp, xp, sc, p.K / 32 - s * 8 - h * 4);
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) xp[j] += kNibStageK / 2;
-                buf ^= 4u << 4;
-                // the second half's groups
-                if constexpr (GC == 1) sc.s[0] = sc.s[2], sc.s[1] = sc.s[3], sc.z[0] = sc.z[1];
-                if constexpr (GC == 2) sc.s[0] = sc.s[1], sc.z[0] >>= 16;
-                if constexpr (GC == 4) sc.s[0] >>= 16, sc.z[0] >>= 8;
-            }
-            __syncwarp();   // every lane is done with the unit before its slot is loaded again
-            load(s + kNibRing, i);
-            i = i + 1 == kNibRing ? 0 : i + 1;
-        }
-    }
-    __syncthreads();   // the ring's memory becomes the sums'
-    constexpr int kPitch = 8 * NT + 1;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float *to = sums + (warp * kNibFeatures + g + 8 * q) * kPitch + 8 * j + 2 * (lane & 3);
-            to[0] = acc[j][q >> 1][2 * (q & 1)];
-            to[1] = acc[j][q >> 1][2 * (q & 1) + 1];
-        }
-    __syncthreads();
-    for (int o = threadIdx.x; o < cnt * kNibFeatures; o += 32 * kNibWarps) {
-        const int r = o / kNibFeatures, f = o % kNibFeatures;
-        float v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kNibWarps; ++k) v += sums[(k * kNibFeatures + f) * kPitch + r];
-        if (n0 + f < p.N) nib_store<KIND>(p, r0 + r, n0 + f, v);
-    }
-}
-
-template <int KIND, int GC, bool VEC, bool ZEROS>
-__global__ void __launch_bounds__(32 * kNibWarps, 2)
-    nibble_kernel(const __grid_constant__ CUtensorMap tmB, const NibbleParams p)
-{
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    float *sums = reinterpret_cast<float *>(smem_raw + (base - raw));   // after the loop: [warp][feature][8 NT + 1]
-    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
-    const int tiles = (p.N + kNibFeatures - 1) / kNibFeatures;
-    const int slot = static_cast<int>(blockIdx.x) / tiles;   // which of the experts that have rows
-    const int n0 = (static_cast<int>(blockIdx.x) - slot * tiles) * kNibFeatures;
-    const uint32_t ring = base + warp * (kNibRing * kNibStageBytes);
-    const uint32_t bars = base + kNibWarps * kNibRing * kNibStageBytes + warp * (8 * kNibRing);
-    uint32_t phases = 0;   // bit i: the parity of ring barrier i that comes next
-
-    if (lane == 0) {
-        for (int i = 0; i < kNibRing; ++i) mbar_init(bars + 8 * i, 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
-    pdl_launch_dependents();
-    // one matrix: its place is known, so its first units may come into L2
-    // while the previous grid finishes (a prefetch changes no loaded value)
-    if (!p.offsets) {
-        const int units = (p.K + kNibStageK - 1) / kNibStageK, end = units * (warp + 1) / kNibWarps;
-        for (int s = units * warp / kNibWarps, i = 0; s < end && i < kNibRing; ++s, ++i)
-            tma_prefetch_3d(lane == 0 ? 1u : 0u, &tmB, s * 128, n0, 0);
-    }
-    pdl_wait();
-
-    // this CTA's expert: the slot-th that has rows
-    int e = 0, lo = 0, hi = p.rows;
+    const int lane = static_cast<int>(lane_id());
+    int e = 0, lo = 0, hi = p.rows, before = 0;
     if (p.offsets) {
-        int seen = 0;
-        bool found = false;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int i = e0 + lane;
             int a = 0, b = 0;
@@ -407,85 +279,292 @@ __global__ void __launch_bounds__(32 * kNibWarps, 2)
                 a = max(0, min(__ldg(p.offsets + i), p.rows));
                 b = max(a, min(__ldg(p.offsets + i + 1), p.rows));
             }
-            const uint32_t some = __ballot_sync(0xffffffffu, b > a);
-            // lane whose expert is the (slot - seen)-th set bit
-            const bool mine = ((some >> lane) & 1u) && __popc(some & ((1u << lane) - 1u)) == slot - seen;
-            const uint32_t at = __ballot_sync(0xffffffffu, mine);
-            if (at) {
-                const int src = __ffs(at) - 1;
+            const int n = (b - a + kNibRows - 1) / kNibRows;
+            int incl = n;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, s);
+                if (lane >= s) incl += o;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > block);
+            if (past) {
+                const int src = __ffs(past) - 1;
                 e = e0 + src;
                 lo = __shfl_sync(0xffffffffu, a, src);
                 hi = __shfl_sync(0xffffffffu, b, src);
-                found = true;
+                before += __shfl_sync(0xffffffffu, incl - n, src);
                 break;
             }
-            seen += __popc(some);
+            before += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (!found) return;
     }
-    const int row_b = e * p.N + n0;   // (experts * N < 2^31)
+    const int r0 = lo + (block - before) * kNibRows;
+    return NibBlock{e, r0, min(hi - r0, kNibRows)};
+}
 
-    for (int r0 = lo; r0 < hi; r0 += kNibRows) {
-        const int cnt = min(hi - r0, kNibRows);
-        if (cnt <= 8)
-            nib_rows<KIND, 1, GC, VEC, ZEROS>(tmB, p, ring, bars, phases, sums, n0, row_b, r0, cnt);
-        else
-            nib_rows<KIND, 2, GC, VEC, ZEROS>(tmB, p, ring, bars, phases, sums, n0, row_b, r0, cnt);
-        if (r0 + kNibRows < hi) {
-            fence_proxy_async_smem();   // the sums' accesses before the next rows' TMA loads
-            __syncthreads();
+// A unit times the rows: acc += sum over its groups of scale * (rows . (q - z)).
+// x: the rows' values, as the MMA takes them, zeros behind the contraction.
+// buf: chunk c of this thread's first feature is at buf ^ (c << 4).
+template <int KIND, int GC, bool ZEROS>
+__device__ __forceinline__ void unit_sums(float (&acc)[2][4], uint32_t buf, int g, const uint4 (&x)[8], const NibScales<GC> &sc)
+{
+    constexpr int kGroups = NibScales<GC>::kGroups;
+#pragma unroll
+    for (int gi = 0; gi < kGroups; ++gi) {
+        // the four features of this thread: g, g + 8, g + 16, g + 24
+        float f[4];
+        uint32_t zv[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f[q] = widen<KIND>(__shfl_sync(0xffffffffu, sc.s[gi / 2], g + 8 * q), gi & 1);
+            zv[q] = zero_bits<KIND>(0x08080808u, 0);
+            if constexpr (ZEROS) zv[q] = zero_bits<KIND>(__shfl_sync(0xffffffffu, sc.z[gi / 4], g + 8 * q), gi & 3);
+        }
+        float part[2][4];
+#pragma unroll
+        for (int ci = 0; ci < GC; ++ci) {
+            const int c = gi * GC + ci;
+            const uint32_t from = buf ^ (static_cast<uint32_t>(c) << 4);
+            uint32_t w[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) expand<KIND>(lds_u32(from + q * 1024), zv[q], w[q]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (ci == 0)
+                    mma16816<KIND, true>(part[m], w[2 * m][0], w[2 * m + 1][0], w[2 * m][1], w[2 * m + 1][1], x[c].x, x[c].y);
+                else
+                    mma16816<KIND, false>(part[m], w[2 * m][0], w[2 * m + 1][0], w[2 * m][1], w[2 * m + 1][1], x[c].x, x[c].y);
+                mma16816<KIND, false>(part[m], w[2 * m][2], w[2 * m + 1][2], w[2 * m][3], w[2 * m + 1][3], x[c].z, x[c].w);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                acc[q >> 1][2 * (q & 1) + k] = fmaf(f[q], part[q >> 1][2 * (q & 1) + k], acc[q >> 1][2 * (q & 1) + k]);
+    }
+}
+
+template <int KIND, int GC, bool VEC, bool ZEROS>
+__global__ void __launch_bounds__(32 * kNibWarps, 1)
+    nibble_kernel(const __grid_constant__ CUtensorMap tmB, const NibbleParams p)
+{
+    constexpr int kGroups = NibScales<GC>::kGroups;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sums0 = base + kNibWarps * kNibRing * kNibStageBytes;   // [2][warp][row][feature]
+    const uint32_t gather = sums0 + 2 * kNibWarps * kNibSums * 4;          // [slot][CTA][row][feature], in the first CTA
+    const uint32_t bars = gather + kNibSlots * kNibMaxCtas * kNibSums * 4;
+    __shared__ NibTile gathered[kNibSlots];
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t one = lane == 0 ? 1u : 0u;
+    const uint32_t ring = base + warp * (kNibRing * kNibStageBytes), my_bars = bars + warp * (8 * kNibRing);
+    const int ctas = p.cluster;
+    const int rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    // takers of this CTA (several only in clusters of one) and this warp's place in its own
+    const int kw = p.k_warps, group = warp / kw, takers = kNibWarps / kw;
+    const int first_unit = rank * kw + warp % kw, unit_step = ctas * kw;
+    const int units = (p.K + kNibStageK - 1) / kNibStageK;
+    const int mine = units > first_unit ? (units - first_unit + unit_step - 1) / unit_step : 0;   // this warp's units of a tile
+    const int all = (p.N + 15) / 16;
+
+    if (lane == 0) {
+        for (int i = 0; i < kNibRing; ++i) mbar_init(my_bars + 8 * i, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (this CTA has started)
+    pdl_launch_dependents();
+    auto begin_of = [&](int blocks, int part) -> int {
+        const int parts = static_cast<int>(gridDim.x) / ctas * takers;
+        return static_cast<int>(static_cast<long long>(blocks) * all * part / parts);
+    };
+    const int part = static_cast<int>(blockIdx.x) / ctas * takers + group;
+    if (!p.offsets && mine > 0) {
+        // one matrix: its place is known, so this warp's first unit may come
+        // into L2 while the previous grid finishes (a prefetch changes no
+        // loaded value)
+        const int blocks = (p.rows + kNibRows - 1) / kNibRows, h = begin_of(blocks, part);
+        if (h < begin_of(blocks, part + 1)) tma_prefetch_3d(one, &tmB, first_unit * 128, h % all * 16, 0);
+    }
+    pdl_wait();
+
+    const int blocks = nib_blocks(p);   // (blocks * all < 2^31: checked by the host)
+    int h = begin_of(blocks, part);
+    const int h_end = begin_of(blocks, part + 1);
+    int slot = 0, parity = 0, filled = 0;
+    uint32_t phases = 0;   // bit i: the parity of ring barrier i that comes next
+    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // (the others have started)
+
+    while (h < h_end) {
+        // the part of one row block that is this taker's: features n_begin .. n_end - 1
+        const int block = h / all, n16 = h - block * all, count = min(h_end - h, all - n16);
+        h += count;
+        const NibBlock rows = nib_block(block, p);
+        const int n_begin = n16 * 16, n_end = min((n16 + count) * 16, p.N);
+        const int row_b = rows.e * p.N;   // (experts * N < 2^31)
+        // ask for the next unit
+        int ld_n = n_begin, ld_unit = first_unit;
+        auto load = [&](int i) {
+            if (ld_n >= n_end || mine == 0) return;
+            mbar_arrive_expect_tx_if(one, my_bars + 8 * i, kNibStageBytes);
+            tma_load_3d(one, ring + i * kNibStageBytes, &tmB, my_bars + 8 * i, ld_unit * 128, row_b + ld_n, 0);
+            ld_unit += unit_step;
+            if (ld_unit >= units) ld_unit = first_unit, ld_n += kNibFeatures;
+        };
+        for (int i = 0; i < kNibRing; ++i) load(slot ^ i);
+
+        uint4 x[8];
+        auto load_rows = [&](int unit) {
+            // rows that are not there read the last one's values: their sums are not stored
+            const uint16_t *xp = static_cast<const uint16_t *>(p.a) + static_cast<long long>(rows.r0 + min(g, rows.cnt - 1)) * p.K
+                                 + unit * kNibStageK + t * 8;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                x[c] = make_uint4(0, 0, 0, 0);
+                if (unit * kNibStageK + c * 32 < p.K) x[c] = ld_row(xp + c * 32);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)   // pairs (0, 4), (1, 5), (2, 6), (3, 7), as expand() leaves the weights
+                x[c] = make_uint4(__byte_perm(x[c].x, x[c].z, 0x5410), __byte_perm(x[c].x, x[c].z, 0x7632),
+                                  __byte_perm(x[c].y, x[c].w, 0x5410), __byte_perm(x[c].y, x[c].w, 0x7632));
+        };
+        // scales of this lane's feature (of the last one, where there is none)
+        auto scales = [&](int n, int unit) {
+            const long long f = static_cast<long long>(row_b + min(n + lane, p.N - 1)) * p.groups;
+            return ld_scales<GC, VEC, ZEROS>(static_cast<const uint16_t *>(p.scales) + f, p.zeros + f, unit * kGroups, p.groups);
+        };
+        NibScales<GC> next = {};
+        if (mine > 0) {
+            next = scales(n_begin, first_unit);
+            if (mine == 1) load_rows(first_unit);
+        }
+
+        for (int n = n_begin; n < n_end; n += kNibFeatures) {
+            float acc[2][4] = {};
+            for (int unit = first_unit; unit < units; unit += unit_step) {
+                const NibScales<GC> sc = next;
+                // (behind the last one its own again)
+                const bool more = unit + unit_step < units;
+                next = scales(more || n + kNibFeatures >= n_end ? n : n + kNibFeatures, more ? unit + unit_step : first_unit);
+                if (mine > 1) load_rows(unit);
+                if (!wait(my_bars + 8 * slot, (phases >> slot) & 1u, p)) break;
+                phases ^= 1u << slot;
+                unit_sums<KIND, GC, ZEROS>(acc, ring + slot * kNibStageBytes + g * 144 + t * 4, g, x, sc);
+                __syncwarp();   // every lane is done with the unit before its slot is loaded again
+                load(slot);
+                slot ^= 1;
+            }
+            // the taker's warps add up; two sets of sums, so that one barrier per tile does
+            const uint32_t to = sums0 + ((parity * kNibWarps + warp) * kNibSums + 2 * t * kNibPitch + g) * 4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) sts_f32(to + (k * kNibPitch + 8 * q) * 4, acc[q >> 1][2 * (q & 1) + k]);
+            if (kw > 1) bar_sync(1 + group, 32 * kw);   // (at most 8 takers then: 9 of the 16 barriers)
+            else __syncwarp();
+            const int r = warp - group * kw;
+            for (int rr = r; rr < rows.cnt; rr += kw) {   // a warp per row, a lane per feature
+                const uint32_t from = sums0 + ((parity * kNibWarps + group * kw) * kNibSums + rr * kNibPitch + lane) * 4;
+                float v = 0.0f;
+#pragma unroll 4
+                for (int k = 0; k < kw; ++k) v += lds_f32(from + k * kNibSums * 4);
+                if (ctas > 1)
+                    st_cluster_f32(mapa(gather + ((filled * ctas + rank) * kNibSums + rr * kNibPitch + lane) * 4, 0u), v);
+                else if (n + lane < n_end)
+                    nib_store<KIND>(p, rows.r0 + rr, n + lane, v);
+            }
+            parity ^= 1;
+            if (ctas == 1) continue;
+            if (threadIdx.x == 0) gathered[filled] = NibTile{n, min(kNibFeatures, n_end - n), rows.r0, rows.cnt};
+            const bool end = h == h_end && n + kNibFeatures >= n_end;
+            if (++filled == kNibSlots || end) {
+                cluster_sync();
+                if (rank == 0)
+                    for (int o = warp; o < filled * kNibRows; o += kNibWarps) {
+                        const int s = o / kNibRows, i = o % kNibRows;
+                        const NibTile w = gathered[s];
+                        const uint32_t from = gather + (s * ctas * kNibSums + i * kNibPitch + lane) * 4;
+                        float v = 0.0f;
+                        for (int c = 0; c < ctas; ++c) v += lds_f32(from + c * kNibSums * 4);
+                        if (i < w.cnt && lane < w.features) nib_store<KIND>(p, w.r0 + i, w.n0 + lane, v);
+                    }
+                filled = 0;
+                if (!end) cluster_sync();   // the sums are read before the next ones come
+            }
         }
     }
 }
 
-template <class... P, class... A>
-cudaError_t go(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool overlap, A... args)
+template <int KIND, int GC, bool VEC, bool ZEROS>
+cudaError_t run(const CUtensorMap &b, NibbleParams p, NibPrepared *prepared, cudaStream_t stream, bool overlap)
 {
+    constexpr int smem = 1024 + kNibWarps * kNibRing * (kNibStageBytes + 8) + (2 * kNibWarps + kNibSlots * kNibMaxCtas) * kNibSums * 4;
+    const auto kernel = nibble_kernel<KIND, GC, VEC, ZEROS>;
+    const uint32_t bit = 1u << ((GC / 2 * 2 + VEC) * 2 + ZEROS);   // (GC / 2: 0, 1, 2)
+    if (!(prepared->kernels & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        prepared->kernels |= bit;
+    }
+    // Takers: of all ways to have a warp per unit, or several units per warp
+    // (which then loads the rows' values for each: taken as a third more), the
+    // one that leaves the fewest idle.
+    const int units = (p.K + kNibStageK - 1) / kNibStageK;
+    double least = 1e30;
+    for (int c = 1; c <= kNibMaxCtas; c *= 2)
+        for (int k = c == 1 ? 1 : kNibWarps; k <= kNibWarps; k *= 2) {
+            const int each = units > 0 ? (units + c * k - 1) / (c * k) : 1;
+            const double cost = static_cast<double>(each) * c * k * (each > 1 ? 1.33 : 1.0);
+            if (cost <= least) least = cost, p.cluster = c, p.k_warps = k;
+        }
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(block, 1, 1);
+    cudaLaunchAttribute attr[2];
+    cfg.blockDim = dim3(32 * kNibWarps, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    if (overlap) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (p.cluster > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
         cfg.numAttrs = 1;
+        int &resident = prepared->clusters[p.cluster / 2 - 1];
+        if (resident == 0) {   // as many as the device holds at once (a GPC's SMs need not divide by 4)
+            cfg.gridDim = dim3(static_cast<unsigned>(p.cluster), 1, 1);
+            cudaError_t e = cudaOccupancyMaxActiveClusters(&resident, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            if (resident < 1) return cudaErrorInvalidConfiguration;
+        }
+        cfg.gridDim = dim3(static_cast<unsigned>(resident * p.cluster), 1, 1);
+    } else {
+        cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), 1, 1);
     }
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <int KIND, int GC, bool VEC>
-cudaError_t run(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream, bool overlap)
-{
-    constexpr int smem = 1024 + kNibWarps * kNibRing * (kNibStageBytes + 8);
-    static_assert(kNibRing * kNibStageBytes >= kNibFeatures * (kNibRows + 1) * 4, "the sums fit in the ring");
-    const auto kernel = p.zeros ? nibble_kernel<KIND, GC, VEC, true> : nibble_kernel<KIND, GC, VEC, false>;
-    const uint32_t bit = 1u << (((KIND * 3 + GC / 2) * 2 + VEC) * 2 + (p.zeros ? 1 : 0));   // (GC / 2: 0, 1, 2)
-    if (!(*prepared & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        *prepared |= bit;
+    if (overlap) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
     }
-    // at most `rows` experts have rows
-    const int64_t experts = p.offsets ? (p.experts < p.rows ? p.experts : p.rows) : 1;
-    const int64_t ctas = (static_cast<int64_t>(p.N) + kNibFeatures - 1) / kNibFeatures * experts;
-    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    return go(kernel, static_cast<unsigned>(ctas), 32 * kNibWarps, smem, stream, overlap, b, p);
+    return cudaLaunchKernelEx(&cfg, kernel, b, p);
 }
 
 template <int KIND, int GC>
-cudaError_t by_alignment(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream, bool overlap)
+cudaError_t by_alignment(const CUtensorMap &b, const NibbleParams &p, NibPrepared *prepared, cudaStream_t stream, bool overlap)
 {
-    return p.groups % NibScales<GC>::kGroups == 0 ? run<KIND, GC, true>(b, p, prepared, stream, overlap)
-                                                  : run<KIND, GC, false>(b, p, prepared, stream, overlap);
+    if (p.groups % NibScales<GC>::kGroups == 0)
+        return p.zeros ? run<KIND, GC, true, true>(b, p, prepared, stream, overlap)
+                       : run<KIND, GC, true, false>(b, p, prepared, stream, overlap);
+    return p.zeros ? run<KIND, GC, false, true>(b, p, prepared, stream, overlap)
+                   : run<KIND, GC, false, false>(b, p, prepared, stream, overlap);
 }
 
 }  // namespace
 
 // (one translation unit per kind: expert_launch.h names the two)
-cudaError_t PTS_NIBBLE_LAUNCH(const CUtensorMap &b, const NibbleParams &p, uint32_t *prepared, cudaStream_t stream, bool overlap)
+cudaError_t PTS_NIBBLE_LAUNCH(const CUtensorMap &b, const NibbleParams &p, NibPrepared *prepared, cudaStream_t stream,
+                              bool overlap)
 {
     return p.group == 32 ? by_alignment<PTS_NIBBLE_KIND, 1>(b, p, prepared, stream, overlap)
            : p.group == 64 ? by_alignment<PTS_NIBBLE_KIND, 2>(b, p, prepared, stream, overlap)
