@@ -6,6 +6,7 @@
 
 #include "expert_launch.h"
 #include "gemm_ctx.h"
+#include "gemm_plan.h"
 
 using namespace pts;
 
@@ -48,11 +49,19 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     const int64_t features = mode == EXPERT_FWD ? N : K;
     const int64_t contraction = mode == EXPERT_FWD ? K : N;   // (WGRAD: an expert's rows)
     const int kelems = dtype == GEMM_E4M3 ? 128 : 64;
-    // Variant.  See DESIGN for the measurements behind both rules.
+    // Variant (cta_group 0).  Few rows per expert: the weights' bytes count, and
+    // tiles of 64 rows leave room for 8 stages of them (us on GB300, this / pairs:
+    // 64 rows over 8 experts of 4096^2 45.3 / 46.7, 256 45.7 / 47.5, 2048 over 64 of
+    // 2048^2 84.5 / 88.8; but 512 over 8 56.8 / 49.1, an expert's rows then being
+    // several tiles).  Else pairs from 14 k-blocks per tile, as in gemm_run: 16384
+    // over 32, K = 1024, 103 / 112 for singles, 300 over 19, K = 560, 6.6 / 5.7.  The
+    // weights' gradient counts the k-blocks of an average expert's rows: 4096 over
+    // 4 34.7 / 35.6, 6000 over 24 42.7 / 37.2, 64 over 8 89 / 45.
     int cg = h->opts.cta_group;
     int bn = kExpertTileN;
-    if (cg == 0) cg = 2;
-    if (mode == EXPERT_FWD && h->opts.cta_group != 2 && rows <= int64_t(kExpertTileNFew) * experts) {
+    const int64_t length = mode == EXPERT_WGRAD ? rows / experts : contraction;
+    if (cg == 0) cg = choose_cta_group((length + kelems - 1) / kelems);
+    if (mode == EXPERT_FWD && h->opts.cta_group != 2 && rows <= kExpertFewRows * experts) {
         cg = 1;
         bn = kExpertTileNFew;
     }

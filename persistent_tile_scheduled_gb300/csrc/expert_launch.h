@@ -42,7 +42,8 @@ __host__ __device__ constexpr int expert_smem_bytes(int cg, int bn, int stages)
 }
 
 constexpr int kExpertTileN = 256;       // rows of a tile
-constexpr int kExpertTileNFew = 64;     // rows of a tile when the experts have few
+constexpr int kExpertTileNFew = 64;     // rows of a tile when the experts have few:
+constexpr int64_t kExpertFewRows = 32;  // at most so many on average
 
 struct ExpertOps {
     cudaError_t (*prepare)(int smem, int sms, int *clusters);
