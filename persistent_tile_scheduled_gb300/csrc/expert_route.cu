@@ -43,17 +43,19 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
     uint32_t *mine = hist + warp * experts;
 
     for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) hist[i] = 0u;
-    const int per_warp = ((n + ctas * warps - 1) / (ctas * warps) + 31) / 32 * 32;
-    const long long first = static_cast<long long>(cta * warps + warp) * per_warp;
-    const int lo = static_cast<int>(first < n ? first : n);
-    const int hi = n - lo < per_warp ? n : lo + per_warp;
+    // (unsigned: a stretch may end within 32 of 2^31)
+    const uint32_t count = static_cast<uint32_t>(n), all_warps = static_cast<uint32_t>(ctas * warps);
+    const uint32_t per_warp = ((count + all_warps - 1) / all_warps + 31) / 32 * 32;
+    const unsigned long long first = static_cast<unsigned long long>(cta * warps + warp) * per_warp;
+    const uint32_t lo = first < count ? static_cast<uint32_t>(first) : count;
+    const uint32_t hi = count - lo < per_warp ? count : lo + per_warp;
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
 
     // count
-    for (int b = lo; b < hi; b += 32) {
-        const int i = b + lane;
+    for (uint32_t b = lo; b < hi; b += 32) {
+        const uint32_t i = b + static_cast<uint32_t>(lane);
         const int id = i < hi ? ids[i] : -1;
         const bool held = id >= 0 && id < experts;
         const uint32_t peers = __match_any_sync(0xffffffffu, held ? id : -1);
@@ -115,8 +117,8 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
     if (cta == 0 && threadIdx.x == 0) offsets[experts] = static_cast<int32_t>(carry);
 
     // hand out rows
-    for (int b = lo; b < hi; b += 32) {
-        const int i = b + lane;
+    for (uint32_t b = lo; b < hi; b += 32) {
+        const uint32_t i = b + static_cast<uint32_t>(lane);
         const int id = i < hi ? ids[i] : -1;
         const bool held = id >= 0 && id < experts;
         const uint32_t peers = __match_any_sync(0xffffffffu, held ? id : -1);
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
         if (held && rank == 0) mine[id] += __popc(peers);
         __syncwarp();
         if (i < hi) row_of[i] = held ? static_cast<int32_t>(row) : -1;
-        if (held) src_of[row] = i;
+        if (held) src_of[row] = static_cast<int32_t>(i);
     }
     // rows behind the last held assignment have no source
     for (long long r = static_cast<long long>(carry) + cta * static_cast<long long>(blockDim.x) + threadIdx.x; r < n;

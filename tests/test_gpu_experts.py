@@ -488,3 +488,79 @@ def test_refusals(h):
         assert err.value.status == 1, i
     st, dev = pts.gemm_check(h)
     assert st == 0 and dev == 0
+
+
+# ---- the layer of the example, forwards, backwards and in 4 bits ------------------
+
+
+def test_example_layer():
+    """Forward and gradients of examples/expert_layer.py against the same layer written out in 64 bits.
+
+    Each 16-bit tensor between two operators is rounded to 2^-8 of itself and
+    a product of n terms keeps that relative to the root of its sum of squares;
+    4 roundings (6 backwards) in a row are below 2^-5 of the result's norm."""
+    import os
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    import expert_layer as ex
+
+    T, D, H, E, k = 100, 72, 136, 5, 2
+    layer = _layer_without_4_bits(ex, D, H, E, k)
+    gen = torch.Generator().manual_seed(9)
+    x = torch.randn(T, D, generator=gen).to(torch.bfloat16).cuda()
+    ids = torch.randint(-1, E, (T, k), generator=gen, dtype=torch.int32).cuda()
+    w = torch.rand(T, k, generator=gen).cuda()
+    dy = torch.randn(T, D, generator=gen).to(torch.bfloat16).cuda()
+    y, saved = layer.forward(x, ids, w)
+    got = layer.backward(dy, saved)
+
+    x64, w64 = x.double().requires_grad_(), w.double().requires_grad_()
+    up, down = layer.up.double().requires_grad_(), layer.down.double().requires_grad_()
+    y64 = torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if e >= 0:
+                y64[t] = y64[t] + w64[t, j] * (down[e] @ (up[e] @ x64[t]).relu().square())
+    want = torch.autograd.grad((y64 * dy.double()).sum(), (x64, w64, up, down))
+    for a, b in zip((y, *got), (y64.detach(), *want)):
+        assert float((a.double() - b).norm()) <= 2.0 ** -5 * float(b.norm())
+    st, dev = pts.gemm_check(layer.h)
+    layer.close()
+    assert st == 0, f"device status {dev:#x}"
+
+
+def _layer_without_4_bits(ex, D, H, E, k):
+    quantise, ex.quantise = ex.quantise, lambda w, group: None   # (sizes that are no multiple of a group)
+    try:
+        return ex.ExpertLayer(D, H, E, k)
+    finally:
+        ex.quantise = quantise
+
+
+def test_example_decode():
+    """The 4-bit forward equals the 16-bit one with the matrices that the codes stand for."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import expert_layer as ex
+    T, D, H, E, k = 5, 128, 256, 6, 3
+    layer = ex.ExpertLayer(D, H, E, k, seed=2)
+    for name in ("up", "down"):
+        q, s = getattr(layer, name + "4")
+        code = torch.stack([q & 15, q >> 4], -1).flatten(-2).double() - 8.0
+        setattr(layer, name, (code * s.double().repeat_interleave(128, -1)))
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(T, D, generator=gen).to(torch.bfloat16).cuda()
+    ids = torch.randint(0, E + 1, (T, k), generator=gen, dtype=torch.int32).cuda()
+    w = torch.rand(T, k, generator=gen).cuda()
+    y = layer.decode(x, ids, w)
+    want = torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if e < E:
+                want[t] += w[t, j].double() * (layer.down[e] @ (layer.up[e] @ x[t].double()).relu().square())
+    layer.close()
+    assert float((y.double() - want).norm()) <= 2.0 ** -5 * float(want.norm())
