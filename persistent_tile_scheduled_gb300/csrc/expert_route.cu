@@ -15,9 +15,13 @@ namespace {
 // A stable counting sort in one launch: one cluster of up to 8 CTAs, CTA c and
 // in it warp w taking consecutive stretches of the assignments.  A warp counts
 // its stretch per expert (a histogram of its own in shared memory, so the order
-// of the counts is that of the assignments and no atomics are needed), the
-// counts are summed over warps, CTAs (through distributed shared memory) and
-// experts, and the warp walks its stretch again handing out rows.
+// of the counts is that of the assignments and no atomics are needed) and notes
+// every assignment's place among the stretch's of its expert in row_of; the
+// counts are summed over warps (a warp per expert), CTAs (through distributed
+// shared memory) and experts; then the places become rows.  Latency bounds it
+// (0.8 MB in and out for 65536 assignments): 8 loads are on their way at a time.
+// (One load at a time, the places found a second time, and a thread per expert
+// for the sums over warps: 19 us for 65536 over 32 experts, this 10.)
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortMaxCtas = 8;
 
@@ -28,21 +32,24 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr)
     return v;
 }
 
+// BATCH: assignments per lane at a time
+template <int BATCH>
 __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
     expert_sort_kernel(const int32_t *__restrict__ ids, int n, int experts, int32_t *__restrict__ offsets,
                        int32_t *__restrict__ row_of, int32_t *__restrict__ src_of)
 {
     extern __shared__ uint32_t sm[];
     const int warps = static_cast<int>(blockDim.x >> 5);
-    uint32_t *hist = sm;                        // [warps][experts]
-    uint32_t *total = sm + warps * experts;     // [experts], this CTA's counts
+    const int pitch = experts | 1;              // (odd: a warp's lanes read one expert's counts without conflicts)
+    uint32_t *hist = sm;                        // [warps][pitch]
+    uint32_t *total = sm + warps * pitch;       // [experts], this CTA's counts; then its first row of each expert
     uint32_t *scan = total + experts;           // [warps]
     const int warp = static_cast<int>(threadIdx.x >> 5);
     const int lane = static_cast<int>(lane_id());
     const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-    uint32_t *mine = hist + warp * experts;
+    uint32_t *mine = hist + warp * pitch;
 
-    for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) hist[i] = 0u;
+    for (int i = threadIdx.x; i < warps * pitch; i += blockDim.x) hist[i] = 0u;
     // (unsigned: a stretch may end within 32 of 2^31)
     const uint32_t count = static_cast<uint32_t>(n), all_warps = static_cast<uint32_t>(ctas * warps);
     const uint32_t per_warp = ((count + all_warps - 1) / all_warps + 31) / 32 * 32;
@@ -53,25 +60,55 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
     pdl_launch_dependents();
     pdl_wait();
 
-    // count
-    for (uint32_t b = lo; b < hi; b += 32) {
-        const uint32_t i = b + static_cast<uint32_t>(lane);
-        const int id = i < hi ? ids[i] : -1;
-        const bool held = id >= 0 && id < experts;
-        const uint32_t peers = __match_any_sync(0xffffffffu, held ? id : -1);
-        if (held && (peers & ((1u << lane) - 1u)) == 0) mine[id] += __popc(peers);
-        __syncwarp();
+    // count, and note each assignment's place (in registers if they hold the
+    // whole stretch, else in row_of)
+    const bool one_batch = per_warp <= 32 * BATCH;
+    int id[BATCH];
+    int32_t place[BATCH];
+    for (uint32_t b = lo; b < hi; b += 32 * BATCH) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const uint32_t i = b + 32 * k + static_cast<uint32_t>(lane);
+            id[k] = i < hi ? __ldg(ids + i) : -1;
+            if (id[k] >= experts) id[k] = -1;
+        }
+        // lanes with the same expert: bit by bit of its number (match.any would
+        // say so at once, but takes some 100 cycles of the SM per warp)
+        uint32_t peers[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) peers[k] = __ballot_sync(0xffffffffu, id[k] >= 0);
+        for (int bit = 1; bit < experts; bit <<= 1)
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const uint32_t set = __ballot_sync(0xffffffffu, id[k] & bit);
+                peers[k] &= id[k] & bit ? set : ~set;
+            }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            place[k] = -1;
+            if (b + 32 * k >= hi) continue;
+            const bool held = id[k] >= 0;
+            const uint32_t rank = __popc(peers[k] & ((1u << lane) - 1u));
+            if (held) place[k] = static_cast<int32_t>(mine[id[k]] + rank);
+            __syncwarp();
+            if (held && rank == 0) mine[id[k]] = static_cast<uint32_t>(place[k]) + __popc(peers[k]);
+            __syncwarp();
+            const uint32_t i = b + 32 * k + static_cast<uint32_t>(lane);
+            if (i < hi && (!one_batch || !held)) row_of[i] = place[k];
+        }
     }
     __syncthreads();
-    // exclusive over the warps, per expert
-    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
-        uint32_t s = 0;
-        for (int w = 0; w < warps; ++w) {
-            const uint32_t c = hist[w * experts + e];
-            hist[w * experts + e] = s;
-            s += c;
+    // exclusive over the warps: a warp per expert, a lane per warp
+    for (int e = warp; e < experts; e += warps) {
+        const uint32_t c = lane < warps ? hist[lane * pitch + e] : 0u;
+        uint32_t incl = c;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, s);
+            if (lane >= s) incl += o;
         }
-        total[e] = s;
+        if (lane < warps) hist[lane * pitch + e] = incl - c;
+        if (lane == 31) total[e] = incl;
     }
     if (ctas > 1) cluster_sync();
     else __syncthreads();
@@ -83,10 +120,14 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
         uint32_t all = 0, below = 0;
         if (e < experts) {
             if (ctas > 1) {
-                for (int c = 0; c < ctas; ++c) {
-                    const uint32_t v = ld_cluster_u32(mapa(smem_u32(total + e), static_cast<uint32_t>(c)));
-                    all += v;
-                    if (c < cta) below += v;
+                uint32_t v[kSortMaxCtas];
+#pragma unroll
+                for (int c = 0; c < kSortMaxCtas; ++c)
+                    v[c] = c < ctas ? ld_cluster_u32(mapa(smem_u32(total + e), static_cast<uint32_t>(c))) : 0u;
+#pragma unroll
+                for (int c = 0; c < kSortMaxCtas; ++c) {
+                    all += v[c];
+                    if (c < cta) below += v[c];
                 }
             } else {
                 all = total[e];
@@ -99,7 +140,9 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
             if (lane >= s) incl += o;
         }
         if (lane == 31) scan[warp] = incl;
-        __syncthreads();
+        // (the counts are read by the whole cluster before they are replaced)
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
         uint32_t before = carry, block = 0;
         for (int w = 0; w < warps; ++w) {
             const uint32_t v = scan[w];
@@ -109,33 +152,36 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
         const uint32_t start = before + incl - all;
         if (e < experts) {
             if (cta == 0) offsets[e] = static_cast<int32_t>(start);
-            for (int w = 0; w < warps; ++w) hist[w * experts + e] += start + below;
+            total[e] = start + below;
         }
         carry += block;
         __syncthreads();
     }
     if (cta == 0 && threadIdx.x == 0) offsets[experts] = static_cast<int32_t>(carry);
 
-    // hand out rows
-    for (uint32_t b = lo; b < hi; b += 32) {
-        const uint32_t i = b + static_cast<uint32_t>(lane);
-        const int id = i < hi ? ids[i] : -1;
-        const bool held = id >= 0 && id < experts;
-        const uint32_t peers = __match_any_sync(0xffffffffu, held ? id : -1);
-        const uint32_t rank = __popc(peers & ((1u << lane) - 1u));
-        uint32_t row = 0;
-        if (held) row = mine[id] + rank;
-        __syncwarp();
-        if (held && rank == 0) mine[id] += __popc(peers);
-        __syncwarp();
-        if (i < hi) row_of[i] = held ? static_cast<int32_t>(row) : -1;
-        if (held) src_of[row] = static_cast<int32_t>(i);
+    // places to rows
+    for (uint32_t b = lo; b < hi; b += 32 * BATCH) {
+        if (!one_batch) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const uint32_t i = b + 32 * k + static_cast<uint32_t>(lane);
+                id[k] = i < hi ? __ldg(ids + i) : -1;
+                place[k] = i < hi ? row_of[i] : -1;   // (as this lane wrote it)
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            if (place[k] >= 0) {
+                const uint32_t i = b + 32 * k + static_cast<uint32_t>(lane);
+                const uint32_t row = static_cast<uint32_t>(place[k]) + mine[id[k]] + total[id[k]];
+                row_of[i] = static_cast<int32_t>(row);
+                src_of[row] = static_cast<int32_t>(i);
+            }
     }
     // rows behind the last held assignment have no source
     for (long long r = static_cast<long long>(carry) + cta * static_cast<long long>(blockDim.x) + threadIdx.x; r < n;
          r += static_cast<long long>(ctas) * blockDim.x)
         src_of[r] = -1;
-    if (ctas > 1) cluster_sync();   // no CTA leaves while another may read its counts
 }
 
 // ---- rows ----------------------------------------------------------------------
@@ -369,18 +415,21 @@ int row_threads(int chunks) { return chunks >= 256 ? 256 : (chunks + 31) / 32 * 
 cudaError_t launch_expert_sort(const int32_t *ids, int64_t n, int experts, int32_t *offsets, int32_t *row_of,
                                int32_t *src_of, cudaStream_t stream, bool overlap)
 {
-    int warps = static_cast<int>((n + 127) / 128);
-    warps = warps < 1 ? 1 : (warps > kSortMaxWarps ? kSortMaxWarps : warps);
-    int ctas = 1;
-    while (ctas < kSortMaxCtas && n > 8192ll * ctas) ctas *= 2;
-    const size_t smem = (static_cast<size_t>(warps + 1) * experts + warps) * sizeof(uint32_t);
+    // Up to 1024: a warp per 32, the shortest chain of steps (32 over 8 experts 2.6
+    // us, with 8 per lane 2.9).  Above 2048 8 CTAs, since a warp's scattered stores
+    // to src_of keep its SM busy (8192 over 64: 4.7 us, on one SM 10.0).
+    const bool few = n <= 32 * kSortMaxWarps;
+    const int ctas = n > 2048 ? kSortMaxCtas : 1, each = few ? 32 : 128;
+    const int64_t wanted = (n + each * ctas - 1) / (each * ctas);
+    const int warps = wanted < 1 ? 1 : (wanted > kSortMaxWarps ? kSortMaxWarps : static_cast<int>(wanted));
+    const size_t smem = (static_cast<size_t>(warps) * (experts | 1) + experts + warps) * sizeof(uint32_t);
+    const auto kernel = few ? expert_sort_kernel<1> : expert_sort_kernel<8>;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    return go(expert_sort_kernel, ctas, warps * 32, smem, ctas, stream, overlap, ids, static_cast<int>(n), experts,
-              offsets, row_of, src_of);
+    return go(kernel, ctas, warps * 32, smem, ctas, stream, overlap, ids, static_cast<int>(n), experts, offsets, row_of,
+              src_of);
 }
 
 cudaError_t launch_expert_gather(const void *x, const int32_t *row_of, void *xs, int tokens, int top_k, int chunks,
