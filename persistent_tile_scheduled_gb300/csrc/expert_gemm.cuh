@@ -18,14 +18,27 @@
 // the user holds them, without a transposed copy:
 //   contraction contiguous (K-major): FWD's X and W, DGRAD's X.
 //   contraction strided (MN-major): DGRAD's W, WGRAD's X and W.  A box of
-//     64 features x 64 contraction rows is one block; blocks of 64 features
-//     follow one another (leading byte offset), groups of 8 contraction rows
-//     are 1024 bytes apart (stride byte offset).
+//     64 features x a ring stage's contraction rows (128 for a pair) is one
+//     block; blocks of 64 features follow one another (leading byte offset),
+//     groups of 8 contraction rows are 1024 bytes apart (stride byte offset).
+//     One box per 64 rows instead, twice the TMA instructions, took 371 us for
+//     16384 rows over 8 experts of 4096 x 4096 where this takes 325.
 // An operand row that belongs to another expert (a box that runs past the
 // expert's last row) only feeds accumulator columns that are not stored.  In
 // WGRAD the rows are the contraction, so there the last 16-row step is cleared
 // in shared memory behind the expert's last row, in both operands (a NaN or
 // infinity there times zero would not be zero), before the MMA reads it.
+//
+// What bounds it (GB300, bf16).  Many rows: the tensor pipe, 85 % busy over 16384
+// rows spread unevenly over 8 experts of 8192 x 4096 (580 us alone; back to back
+// under the power cap 684 us, spread evenly 648, one dense gemm_run of that size
+// 647).  An expert whose rows do not fill its tiles costs the weights' loads of a
+// full one: a pair's stage is 64 KB per SM for 1024 cycles of MMA, the most an SM
+// takes in, so a tile of 200 rows runs hardly faster than one of 256 (8192 rows
+// over 16 experts: 232 us uneven, 213 even).  Few rows: the weights' bytes, 5.8
+// TB/s, with tiles of 64 rows and 8 stages.  The weights' gradient loses about
+// 1 us per tile to the cleared step where rows are no multiple of 16 (2047 and
+// 2049 per expert 343 us, 2048 312).
 //
 // Warp roles as in gemm_kernel.cuh: producer, MMA, 4 epilogue warps, scheduler
 // (a static stride over the tiles of all experts, which it counts from the
@@ -238,8 +251,10 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 const uint32_t fb = (fix ? fix0 : full0) + 8 * stage;
                 const bool pair = CG == 2 && !fix;
                 const uint32_t fbc = pair ? mapa(fb, 0u) : fb;
-                // a pair's leader announces both CTAs' bytes; a stage that is cleared first
-                // is announced by each CTA to itself
+                // a pair's leader announces both CTAs' bytes (each announcing its own, the
+                // peer through a remote arrival, took 862 us for 16384 rows of 8192 x 4096
+                // where this takes 607); a stage that is cleared first is announced by
+                // each CTA to itself
                 if (!pair || leader) mbar_arrive_expect_tx_if(one, fb, pair ? CG * tx : tx);
                 auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
                     if (pair)
