@@ -564,3 +564,38 @@ def test_example_decode():
                 want[t] += w[t, j].double() * (layer.down[e] @ (layer.up[e] @ x[t].double()).relu().square())
     layer.close()
     assert float((y.double() - want).norm()) <= 2.0 ** -5 * float(want.norm())
+
+
+@pytest.mark.parametrize("tokens,dim", [(8, 64), (64, 128), (700, 256)])
+def test_back_to_back_layers_see_their_own_routing(h, tokens, dim):
+    """Layers queued one after another on the same buffers, each with other ids, its kernels started while the ones
+    before still run: every one must follow its own offsets and rows.  Expert e multiplies by e + 1, exactly."""
+    E, k, n = 6, 2, 60
+    gen = torch.Generator().manual_seed(tokens)
+    x = ints((tokens, dim), F16, 61, 3)
+    B = torch.stack([torch.eye(dim) * (e + 1) for e in range(E)]).half().cuda()
+    q = torch.zeros(E, dim, dim, dtype=torch.uint8)
+    for e in range(E):
+        q[e] = 8 + torch.eye(dim, dtype=torch.uint8) * (e + 1)
+    q = q.view(E, dim, dim // 2, 2)
+    B4, s4 = (q[..., 0] | (q[..., 1] << 4)).contiguous().cuda(), torch.ones(E, dim, dim // 32).half().cuda()
+    ids = torch.randint(-1, E, (n, tokens, k), generator=gen, dtype=torch.int32).cuda()
+    w = torch.ones(tokens, k, device="cuda")
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    off, row_of, src = i32(E + 1), i32(tokens, k), i32(tokens * k)
+    xs, c = (torch.zeros(tokens * k, dim, dtype=torch.float16, device="cuda") for _ in range(2))
+    y = torch.zeros(n, 2, tokens, dim, dtype=torch.float16, device="cuda")
+    dw = torch.zeros(n, tokens, k, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(n):
+        pts.gemm_expert_sort(h, tokens, k, E, ids[i], off, row_of, src)
+        pts.gemm_expert_gather(h, tokens, k, dim, x, row_of, xs, F16)
+        pts.gemm_run_experts(h, tokens * k, E, dim, dim, xs, B, off, c, F16)
+        pts.gemm_expert_combine(h, tokens, k, dim, c, row_of, w, y[i, 0], F16)
+        pts.gemm_run_nibble(h, tokens * k, E, dim, dim, 32, xs, B4, s4, None, off, c, F16)
+        pts.gemm_expert_combine(h, tokens, k, dim, c, row_of, w, y[i, 1], F16)
+        pts.gemm_expert_combine_grad(h, tokens, k, dim, x, c, row_of, w, xs, dw[i], F16)
+    torch.cuda.synchronize()
+    factor = torch.where(ids >= 0, ids + 1, 0)
+    assert torch.equal(y.double(), (factor.sum(2).double()[..., None] * x.double())[:, None].expand_as(y))
+    assert torch.equal(dw.double(), factor.double() * (x.double() ** 2).sum(1)[None, :, None])
