@@ -410,8 +410,8 @@ long long piece_blocks(long long tokens, long long chunks, int pieces)
     return (tokens * chunks + kRowThreads * pieces - 1) / (kRowThreads * pieces);
 }
 
-// threads of a block per token: one 16-byte chunk each, up to 256
-int row_threads(int chunks) { return chunks >= 256 ? 256 : (chunks + 31) / 32 * 32; }
+// threads of a block per token: one 16-byte chunk each, up to 256 (a warp where rows are empty: dweights is written)
+int row_threads(int chunks) { return chunks >= 256 ? 256 : (chunks < 1 ? 32 : (chunks + 31) / 32 * 32); }
 
 }  // namespace
 

@@ -165,6 +165,13 @@ def test_combine_grad(h, tokens, top_k, dim, dtype):
     assert (dw[row_of < 0] == 0).all()
 
 
+def test_combine_grad_of_empty_rows(h):
+    row_of = torch.tensor([[0, -1], [1, 2]], dtype=torch.int32, device="cuda")
+    w, dw = torch.ones(2, 2, device="cuda"), torch.full((2, 2), float("nan"), device="cuda")
+    pts.gemm_expert_combine_grad(h, 2, 2, 0, None, None, row_of, w, None, dw, F16)
+    assert (dw == 0).all()
+
+
 def test_row_of_outside_the_rows_counts_as_none(h):
     tokens, top_k, dim = 4, 2, 64
     row_of = torch.tensor([[0, 8], [1 << 30, -7], [2, 3], [-1 << 31, 7]], dtype=torch.int32, device="cuda")
