@@ -376,7 +376,9 @@ gemm_status_t gemm_expert_combine_grad(gemm_handle_t h, int64_t tokens, int64_t 
 /* C[r] = A[r] . B_e for every row r of every expert e, one launch.
  * A: rows x K; B: experts x N x K (each expert's matrix as gemm_run's B);
  * C: rows x N.  dtypes, scales, size rules and K == 0 as in gemm_run (rows
- * takes the place of M; experts < 2^31). */
+ * takes the place of M), but of all calls on experts rows, experts, N and K are
+ * at most GEMM_EXPERT_MAX_SIZE (2^31 - 1024). */
+#define GEMM_EXPERT_MAX_SIZE 2147482624
 gemm_status_t gemm_run_experts(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *A,
                                const void *B, const int32_t *offsets, void *C, gemm_dtype_t dtype, float scale_a,
                                float scale_b, void *stream);
@@ -402,7 +404,8 @@ gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t expe
  *   scales: experts x N x ceil(K / group), of A's type;
  *   zeros: uint8 in 0..15, same shape as scales, or NULL for 8 everywhere;
  *   offsets: as above, or NULL with experts == 1 (every row uses that matrix).
- * group: 32, 64 or 128 (the last group may be short); K % 32 == 0, N % 8 == 0.
+ * group: 32, 64 or 128 (the last group may be short); K % 32 == 0, N % 8 == 0;
+ * experts * N at most GEMM_EXPERT_MAX_SIZE too.
  * Products are exact and sums fp32.  Made for a few rows per expert: the cost is
  * the weights' bytes, read once for every 8 rows of an expert. */
 gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,

@@ -13,6 +13,8 @@ using namespace pts;
 namespace {
 
 constexpr int64_t kLim = (int64_t(1) << 31) - 1;
+// Sizes of the products: the kernels count in 32 bits, and go up to a tile or a stage past the end.
+constexpr int64_t kMaxSize = GEMM_EXPERT_MAX_SIZE;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -127,7 +129,7 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
 gemm_status_t check_product(gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, const int32_t *offsets)
 {
     if (h == nullptr || rows < 0 || experts < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
-    if (rows > kLim || experts > kLim || N > kLim || K > kLim) return GEMM_ERR_INVALID_ARG;
+    if (rows > kMaxSize || experts > kMaxSize || N > kMaxSize || K > kMaxSize) return GEMM_ERR_INVALID_ARG;
     if (experts > 0 && (offsets == nullptr || !aligned4(offsets))) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
 }
@@ -263,12 +265,12 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
                               const int32_t *offsets, void *C, gemm_dtype_t dtype, void *stream)
 {
     if (!is16(dtype) || h == nullptr || rows < 0 || experts < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
-    if (rows > kLim || experts > kLim || N > kLim || K > kLim) return GEMM_ERR_INVALID_ARG;
+    if (rows > kMaxSize || experts > kMaxSize || N > kMaxSize || K > kMaxSize) return GEMM_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return GEMM_ERR_INVALID_ARG;
     if (K % 32 != 0 || N % 8 != 0) return GEMM_ERR_INVALID_ARG;
     if (rows == 0 || experts == 0 || N == 0) return GEMM_OK;
     if ((offsets == nullptr && experts != 1) || !aligned4(offsets)) return GEMM_ERR_INVALID_ARG;
-    if (experts > kLim / N) return GEMM_ERR_INVALID_ARG;   // rows of the weights
+    if (experts > kMaxSize / N) return GEMM_ERR_INVALID_ARG;   // rows of the weights
     // the kernel counts its pieces of work in 32 bits
     const double blocks = double(rows) / 8 + double(rows < experts ? rows : experts);
     if (blocks * (double(N) / 16 + 1) > 2e9) return GEMM_ERR_INVALID_ARG;

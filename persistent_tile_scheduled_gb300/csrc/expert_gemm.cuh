@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                         int it, itf;
                         tile_of(local, etn, tiles_f, p.group_m, it, itf);
                         // equal tiles: ecnt rows in etn tiles, each a multiple of the MMA's granularity
-                        const int size = ((ecnt + etn - 1) / etn + kGran - 1) / kGran * kGran;
+                        const int size = ((ecnt - 1) / etn + kGran) / kGran * kGran;
                         ExpertItem t;
                         t.e = e0 + src;
                         t.f0 = itf * (kRowsPerCta * CG);

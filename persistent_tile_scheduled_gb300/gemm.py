@@ -29,6 +29,7 @@ EXPORTED = ("gemm_create", "gemm_run", "gemm_run_host", "gemm_query", "gemm_chec
 GEMM_NOALLOC_MAX_WORK_ITEMS = 16384
 GEMM_GROUPED_MAX_PROBLEMS = 65536
 GEMM_EXPERT_SORT_MAX_EXPERTS = 1024
+GEMM_EXPERT_MAX_SIZE = 2 ** 31 - 1024
 
 
 class gemm_opts_t(ctypes.Structure):

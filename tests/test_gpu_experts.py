@@ -497,6 +497,19 @@ def test_refusals(h):
     assert st == 0 and dev == 0
 
 
+@pytest.mark.parametrize("which", range(4), ids=["rows", "experts", "N", "K"])
+def test_sizes_whose_counts_would_pass_32_bits_are_refused(h, which):
+    size = [16, 2, 16, 32]
+    size[which] = (1 << 31) - 32   # (a multiple of 32, above the limit)
+    for call in (lambda: pts.gemm_run_experts(h, *size, 1024, 1024, 1024, 1024, BF16),
+                 lambda: pts.gemm_run_experts_dgrad(h, *size, 1024, 1024, 1024, 1024, BF16),
+                 lambda: pts.gemm_run_experts_wgrad(h, *size, 1024, 1024, 1024, 1024, BF16),
+                 lambda: pts.gemm_run_nibble(h, *size, 32, 1024, 1024, 1024, None, 1024, 1024, BF16)):
+        with pytest.raises(pts.GemmError) as err:
+            call()
+        assert err.value.status == 1
+
+
 # ---- the layer of the example, forwards, backwards and in 4 bits ------------------
 
 
