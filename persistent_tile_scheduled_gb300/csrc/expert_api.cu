@@ -272,8 +272,8 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     if ((offsets == nullptr && experts != 1) || !aligned4(offsets)) return GEMM_ERR_INVALID_ARG;
     if (experts > kMaxSize / N) return GEMM_ERR_INVALID_ARG;   // rows of the weights
     // the kernel counts its pieces of work in 32 bits
-    const double blocks = double(rows) / 8 + double(rows < experts ? rows : experts);
-    if (blocks * (double(N) / 16 + 1) > 2e9) return GEMM_ERR_INVALID_ARG;
+    const int64_t max_blocks = rows / 8 + (rows < experts ? rows : experts);
+    if (max_blocks * (N / 16 + 1) > 2000000000) return GEMM_ERR_INVALID_ARG;
     if (C == nullptr || !aligned16(C)) return GEMM_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || B == nullptr || scales == nullptr)) return GEMM_ERR_INVALID_ARG;
     if (!aligned16(A) || !aligned16(B) || !aligned16(scales) || !aligned16(zeros)) return GEMM_ERR_INVALID_ARG;
@@ -292,6 +292,7 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     p.zeros = zeros;
     p.offsets = offsets;
     p.c = C;
+    p.max_blocks = static_cast<int32_t>(max_blocks);
     p.ctas = h->sm_count;
     p.timeout_ns = h->opts.timeout_ns;
     p.status = h->d_status;

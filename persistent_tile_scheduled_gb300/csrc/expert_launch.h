@@ -82,6 +82,7 @@ struct NibbleParams {
     const uint8_t *zeros;     // experts x N x groups, or null (8)
     const int32_t *offsets;   // experts + 1, or null (one expert has every row)
     void *c;                  // rows x N, 16-bit
+    int32_t max_blocks;       // blocks of 8 rows that ascending offsets can make
     int32_t ctas;             // SMs
     int32_t cluster, k_warps; // set by the launch: CTAs and warps of a CTA that share a contraction
     uint64_t timeout_ns;

@@ -251,26 +251,33 @@ struct NibTile {
     int n0, features, r0, cnt;
 };
 
-// Row blocks of all experts.  Called by a whole warp.
+// Row blocks of all experts, at most as many as rows in that order make: offsets
+// that go back and forth claim more, and are not followed that far.  Called by a
+// whole warp.
 __device__ __forceinline__ int nib_blocks(const NibbleParams &p)
 {
     if (!p.offsets) return (p.rows + kNibRows - 1) / kNibRows;
-    int n = 0;
+    uint32_t n = 0;
+    const uint32_t most = static_cast<uint32_t>(p.max_blocks);
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
         const int i = e0 + static_cast<int>(lane_id());
         if (i < p.experts) {
             const int a = max(0, min(__ldg(p.offsets + i), p.rows)), b = max(a, min(__ldg(p.offsets + i + 1), p.rows));
-            n += (b - a + kNibRows - 1) / kNibRows;
+            n = min(n + static_cast<uint32_t>((b - a + kNibRows - 1) / kNibRows), most);
         }
     }
-    return __reduce_add_sync(0xffffffffu, n);
+    // (in two halves: 32 lanes' counts may pass 32 bits)
+    const uint32_t low = __reduce_add_sync(0xffffffffu, n & 0xffffu), high = __reduce_add_sync(0xffffffffu, n >> 16);
+    const unsigned long long all = (static_cast<unsigned long long>(high) << 16) + low;
+    return static_cast<int>(all < most ? all : most);
 }
 
 // Expert and rows of a row block.  Called by a whole warp.
 __device__ __forceinline__ NibBlock nib_block(int block, const NibbleParams &p)
 {
     const int lane = static_cast<int>(lane_id());
-    int e = 0, lo = 0, hi = p.rows, before = 0;
+    int e = 0, lo = 0, hi = p.rows;
+    uint32_t before = 0;   // row blocks before this one's expert, at most `block`
     if (p.offsets) {
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             const int i = e0 + lane;
@@ -279,26 +286,26 @@ __device__ __forceinline__ NibBlock nib_block(int block, const NibbleParams &p)
                 a = max(0, min(__ldg(p.offsets + i), p.rows));
                 b = max(a, min(__ldg(p.offsets + i + 1), p.rows));
             }
-            const int n = (b - a + kNibRows - 1) / kNibRows;
-            int incl = n;
+            // (saturating, for the offsets that claim too many)
+            uint32_t incl = static_cast<uint32_t>((b - a + kNibRows - 1) / kNibRows);
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, s);
-                if (lane >= s) incl += o;
+                const uint32_t o = __shfl_up_sync(0xffffffffu, incl, s);
+                if (lane >= s) incl = min(incl + o, 0x7fffffffu);
             }
-            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > block);
+            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > static_cast<uint32_t>(block));
+            const int src = past ? __ffs(past) - 1 : 32;
+            const uint32_t skipped = __shfl_sync(0xffffffffu, incl, (src - 1) & 31);
+            if (src > 0) before += skipped;
             if (past) {
-                const int src = __ffs(past) - 1;
                 e = e0 + src;
                 lo = __shfl_sync(0xffffffffu, a, src);
                 hi = __shfl_sync(0xffffffffu, b, src);
-                before += __shfl_sync(0xffffffffu, incl - n, src);
                 break;
             }
-            before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
-    const int r0 = lo + (block - before) * kNibRows;
+    const int r0 = lo + (block - static_cast<int>(before)) * kNibRows;
     return NibBlock{e, r0, min(hi - r0, kNibRows)};
 }
 

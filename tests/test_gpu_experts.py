@@ -408,6 +408,20 @@ def test_nibble_rows_keep_their_infinities(h):
     assert torch.isfinite(C[[0, 1, 3, 4]]).all() and not torch.isfinite(C[2][w[0, :, 7] != 0]).any()
 
 
+@pytest.mark.parametrize("rows,E,N", [(64, 64, 40), (1 << 15, 1024, 16400)])
+def test_nibble_offsets_that_go_back_and_forth_stay_inside(h, rows, E, N):
+    """Every other expert claims all rows (in the larger case more pieces of work than 32 bits count); every expert's
+    weights are ones, so that each row is its sum whoever multiplies it."""
+    K = 32
+    A = ints((rows, K), F16, 47)
+    B, s = torch.full((E, N, K // 2), 0x99, dtype=torch.uint8, device="cuda"), torch.ones(E, N, 1).half().cuda()
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    C = torch.full((rows + 8, N), 7.0, dtype=torch.float16, device="cuda")
+    pts.gemm_run_nibble(h, rows, E, N, K, 32, A, B, s, None, off, C, F16)
+    assert (C[:rows] == A.sum(1, dtype=torch.float32).half()[:, None]).all() and (C[rows:] == 7).all()
+
+
 # ---- streams, graphs, refusals -------------------------------------------------
 
 
