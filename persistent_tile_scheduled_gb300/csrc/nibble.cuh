@@ -198,8 +198,7 @@ struct NibScales {
     uint32_t s[kGroups / 2], z[(kGroups + 3) / 4];
 };
 
-// VEC: whole units of them, aligned.  Else one at a time, the last one again
-// behind the end.  (No branches around the loads: a value that meets another
+// VEC: whole units of them, aligned.  Else one at a time, zeros behind the end.  (No branches around the loads: a value that meets another
 // at the end of a branch would be waited for there.)
 template <int GC, bool VEC, bool ZEROS>
 __device__ __forceinline__ NibScales<GC> ld_scales(const uint16_t *sp, const uint8_t *zp, int first, int groups)
@@ -226,6 +225,7 @@ __device__ __forceinline__ NibScales<GC> ld_scales(const uint16_t *sp, const uin
         for (int j = 0; j < kGroups; ++j) {
             const int i = min(first + j, groups - 1);
             s[j] = __ldg(sp + i);
+            if (first + j >= groups) s[j] = 0;   // (an infinite scale times the sum of nothing would be NaN)
             z[j] = ZEROS ? __ldg(zp + i) : 0;
         }
 #pragma unroll

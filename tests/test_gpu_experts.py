@@ -408,6 +408,20 @@ def test_nibble_rows_keep_their_infinities(h):
     assert torch.isfinite(C[[0, 1, 3, 4]]).all() and not torch.isfinite(C[2][w[0, :, 7] != 0]).any()
 
 
+@pytest.mark.parametrize("K,group", [(32, 32), (96, 64), (256, 128), (320, 32)])
+def test_nibble_scales_keep_their_infinities(h, K, group):
+    """An infinite scale of the last group, which a unit of the contraction may not be full of, gives infinities (all
+    its products are positive) and reaches its feature alone."""
+    A, B = torch.ones(2, K).half().cuda(), torch.full((1, 16, K // 2), 0x99, dtype=torch.uint8, device="cuda")
+    s = torch.ones(1, 16, -(-K // group)).half()
+    s[0, 5, -1] = float("inf")
+    C = torch.empty(2, 16, dtype=torch.float16, device="cuda")
+    pts.gemm_run_nibble(h, 2, 1, 16, K, group, A, B, s.cuda(), None, None, C, F16)
+    want = torch.full((2, 16), float(K)).half().cuda()
+    want[:, 5] = float("inf")
+    assert torch.equal(C, want)
+
+
 @pytest.mark.parametrize("rows,E,N", [(64, 64, 40), (1 << 15, 1024, 16400)])
 def test_nibble_offsets_that_go_back_and_forth_stay_inside(h, rows, E, N):
     """Every other expert claims all rows (in the larger case more pieces of work than 32 bits count); every expert's
