@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             bool ok = true;
             int i = 0;
             auto offset = [&](int e) -> int {   // clamped, so that no offsets lead outside the arrays
-                const int v = __ldg(p.offsets + e);
+                const int v = ld_global(p.offsets + e);
                 return v < 0 ? 0 : (v > p.rows ? p.rows : v);
             };
             if constexpr (MODE == EXPERT_WGRAD) {

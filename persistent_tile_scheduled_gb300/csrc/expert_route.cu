@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const uint32_t i = b + 32 * k + static_cast<uint32_t>(lane);
-            id[k] = i < hi ? __ldg(ids + i) : -1;
+            id[k] = i < hi ? ld_global(ids + i) : -1;
             if (id[k] >= experts) id[k] = -1;
         }
         // lanes with the same expert: bit by bit of its number (match.any would
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(32 * kSortMaxWarps, 1)
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const uint32_t i = b + 32 * k + static_cast<uint32_t>(lane);
-                id[k] = i < hi ? __ldg(ids + i) : -1;
+                id[k] = i < hi ? ld_global(ids + i) : -1;
                 place[k] = i < hi ? row_of[i] : -1;   // (as this lane wrote it)
             }
         }
@@ -262,14 +262,14 @@ __global__ void __launch_bounds__(kRowThreads)
     uint4 v[kGatherPieces];
 #pragma unroll
     for (int i = 0; i < kGatherPieces; ++i)
-        if (there[i]) v[i] = __ldcs(x + q[i].token * chunks + q[i].at);
+        if (there[i]) v[i] = ld_global_streamed(x + q[i].token * chunks + q[i].at);
     for (int j0 = 0; j0 < top_k; j0 += 4) {
         int32_t r[kGatherPieces][4];
 #pragma unroll
         for (int i = 0; i < kGatherPieces; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                r[i][j] = there[i] && j0 + j < top_k ? __ldg(row_of + q[i].token * top_k + j0 + j) : -1;
+                r[i][j] = there[i] && j0 + j < top_k ? ld_global(row_of + q[i].token * top_k + j0 + j) : -1;
 #pragma unroll
         for (int i = 0; i < kGatherPieces; ++i)
 #pragma unroll
@@ -300,16 +300,16 @@ __global__ void __launch_bounds__(kRowThreads)
             uint4 v[2][S];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                r[i] = j + i < top_k ? __ldg(row_of + t * top_k + j + i) : -1;
+                r[i] = j + i < top_k ? ld_global(row_of + t * top_k + j + i) : -1;
                 if (r[i] >= n) r[i] = -1;
-                if (w && j + i < top_k) f[i] = __ldg(w + t * top_k + j + i);
+                if (w && j + i < top_k) f[i] = ld_global(w + t * top_k + j + i);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     const int c = c0 + s * static_cast<int>(blockDim.x);
-                    if (r[i] >= 0 && c < chunks) v[i][s] = __ldcs(ys + static_cast<long long>(r[i]) * chunks + c);
+                    if (r[i] >= 0 && c < chunks) v[i][s] = ld_global_streamed(ys + static_cast<long long>(r[i]) * chunks + c);
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -347,14 +347,14 @@ __global__ void __launch_bounds__(256)
     const long long t = blockIdx.x;
     const long long n = static_cast<long long>(tokens) * top_k;
     for (int j = 0; j < top_k; ++j) {
-        const int32_t r = row_of[t * top_k + j];
+        const int32_t r = ld_global(row_of + t * top_k + j);
         float dot = 0.0f;
         if (r >= 0 && r < n) {
-            const float s = w[t * top_k + j];
+            const float s = ld_global(w + t * top_k + j);
             for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
                 float d[8], f[8];
-                unpack8<KIND>(dy[t * chunks + c], d);
-                unpack8<KIND>(ys[static_cast<long long>(r) * chunks + c], f);
+                unpack8<KIND>(ld_global(dy + t * chunks + c), d);
+                unpack8<KIND>(ld_global(ys + static_cast<long long>(r) * chunks + c), f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     dot = fmaf(d[i], f[i], dot);

@@ -189,7 +189,7 @@ __device__ __forceinline__ void nib_store(const NibbleParams &p, long long row, 
     else static_cast<__nv_bfloat16 *>(p.c)[row * p.N + n] = __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ uint4 ld_row(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+__device__ __forceinline__ uint4 ld_row(const uint16_t *p) { return ld_global(reinterpret_cast<const uint4 *>(p)); }
 
 // Scales (pairs) and zeros (fours) of a unit's groups for one feature.
 template <int GC>
@@ -206,27 +206,27 @@ __device__ __forceinline__ NibScales<GC> ld_scales(const uint16_t *sp, const uin
     constexpr int kGroups = NibScales<GC>::kGroups;
     NibScales<GC> r;
     if constexpr (VEC && kGroups == 8) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(sp + first));
+        const uint4 v = ld_global(reinterpret_cast<const uint4 *>(sp + first));
         r.s[0] = v.x, r.s[1] = v.y, r.s[2] = v.z, r.s[3] = v.w;
         if constexpr (ZEROS) {
-            const uint2 z = __ldg(reinterpret_cast<const uint2 *>(zp + first));
+            const uint2 z = ld_global(reinterpret_cast<const uint2 *>(zp + first));
             r.z[0] = z.x, r.z[1] = z.y;
         }
     } else if constexpr (VEC && kGroups == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(sp + first));
+        const uint2 v = ld_global(reinterpret_cast<const uint2 *>(sp + first));
         r.s[0] = v.x, r.s[1] = v.y;
-        if constexpr (ZEROS) r.z[0] = __ldg(reinterpret_cast<const uint32_t *>(zp + first));
+        if constexpr (ZEROS) r.z[0] = ld_global(reinterpret_cast<const uint32_t *>(zp + first));
     } else if constexpr (VEC) {
-        r.s[0] = __ldg(reinterpret_cast<const uint32_t *>(sp + first));
-        if constexpr (ZEROS) r.z[0] = __ldg(reinterpret_cast<const uint16_t *>(zp + first));
+        r.s[0] = ld_global(reinterpret_cast<const uint32_t *>(sp + first));
+        if constexpr (ZEROS) r.z[0] = ld_global(reinterpret_cast<const uint16_t *>(zp + first));
     } else {
         uint32_t s[kGroups], z[kGroups];
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
             const int i = min(first + j, groups - 1);
-            s[j] = __ldg(sp + i);
+            s[j] = ld_global(sp + i);
             if (first + j >= groups) s[j] = 0;   // (an infinite scale times the sum of nothing would be NaN)
-            z[j] = ZEROS ? __ldg(zp + i) : 0;
+            z[j] = ZEROS ? ld_global(zp + i) : 0;
         }
 #pragma unroll
         for (int j = 0; j < kGroups / 2; ++j) r.s[j] = s[2 * j] | s[2 * j + 1] << 16;
@@ -262,7 +262,7 @@ __device__ __forceinline__ int nib_blocks(const NibbleParams &p)
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
         const int i = e0 + static_cast<int>(lane_id());
         if (i < p.experts) {
-            const int a = max(0, min(__ldg(p.offsets + i), p.rows)), b = max(a, min(__ldg(p.offsets + i + 1), p.rows));
+            const int a = max(0, min(ld_global(p.offsets + i), p.rows)), b = max(a, min(ld_global(p.offsets + i + 1), p.rows));
             n = min(n + static_cast<uint32_t>((b - a + kNibRows - 1) / kNibRows), most);
         }
     }
@@ -283,8 +283,8 @@ __device__ __forceinline__ NibBlock nib_block(int block, const NibbleParams &p)
             const int i = e0 + lane;
             int a = 0, b = 0;
             if (i < p.experts) {
-                a = max(0, min(__ldg(p.offsets + i), p.rows));
-                b = max(a, min(__ldg(p.offsets + i + 1), p.rows));
+                a = max(0, min(ld_global(p.offsets + i), p.rows));
+                b = max(a, min(ld_global(p.offsets + i + 1), p.rows));
             }
             // (saturating, for the offsets that claim too many)
             uint32_t incl = static_cast<uint32_t>((b - a + kNibRows - 1) / kNibRows);

@@ -647,3 +647,53 @@ def test_back_to_back_layers_see_their_own_routing(h, tokens, dim):
     factor = torch.where(ids >= 0, ids + 1, 0)
     assert torch.equal(y.double(), (factor.sum(2).double()[..., None] * x.double())[:, None].expand_as(y))
     assert torch.equal(dw.double(), factor.double() * (x.double() ** 2).sum(1)[None, :, None])
+
+
+@pytest.mark.parametrize("tokens,dim", [(8, 64), (64, 256), (1000, 128)])
+def test_a_reader_sees_what_the_call_before_it_wrote(h, tokens, dim):
+    """Pairs of calls queued over and over, the first writing what the second reads, on the same addresses and with
+    other values each time: a call may start while the one before the previous still reads the old values."""
+    E, k, n = 5, 2, 40
+    rows = tokens * k
+    gen = torch.Generator().manual_seed(dim)
+    zeros = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ids = torch.randint(0, E, (n, tokens, k), generator=gen, dtype=torch.int32).cuda()
+    x = torch.randint(-3, 4, (n, tokens, dim), generator=gen).half().cuda()
+    w = torch.ones(tokens, k, device="cuda")
+    eye = torch.eye(dim, dtype=torch.uint8)
+    B = torch.stack([eye * (e + 1) for e in range(E)]).half().cuda()                     # expert e: times e + 1
+    q = torch.stack([8 + eye * 2 * (i + 1) for i in range(3)]).view(3, dim, dim // 2, 2)   # i: times 2 (i + 1)
+    B4, s4 = (q[..., 0] | (q[..., 1] << 4)).contiguous().cuda(), torch.ones(1, dim, dim // 32).half().cuda()
+    off, row_of, src = i32(E + 1), i32(tokens, k), i32(rows)
+    xs, c, out = zeros(rows, dim), zeros(rows, dim), zeros(n, tokens, dim)
+    torch.cuda.synchronize()
+    # routing: sort writes row_of, gather and combine read it
+    for i in range(n):
+        pts.gemm_expert_sort(h, tokens, k, E, ids[i], off, row_of, src)
+        pts.gemm_expert_gather(h, tokens, k, dim, x[i], row_of, xs, F16)
+        pts.gemm_expert_combine(h, tokens, k, dim, xs, row_of, w, out[i], F16)
+    torch.cuda.synchronize()
+    assert torch.equal(out, 2 * x)
+    # rows: gather writes them, the 4-bit product reads them
+    got = zeros(n, rows, dim)
+    for i in range(n):
+        pts.gemm_expert_gather(h, tokens, k, dim, x[i], row_of, xs, F16)
+        pts.gemm_run_nibble(h, rows, 1, dim, dim, 32, xs, B4[0], s4, None, None, got[i], F16)
+    torch.cuda.synchronize()
+    assert torch.equal(got[:, row_of.long()], 2 * x[:, :, None].expand(-1, -1, k, -1))
+    # sums: the 4-bit product, with other weights each time, writes the rows, combine reads them
+    for i in range(n):
+        pts.gemm_run_nibble(h, rows, 1, dim, dim, 32, xs, B4[i % 3], s4, None, None, c, F16)
+        pts.gemm_expert_combine(h, tokens, k, dim, c, row_of, w, out[i], F16)
+    torch.cuda.synchronize()
+    factor = 4.0 * (1 + torch.arange(n, device="cuda") % 3)
+    assert torch.equal(out.float(), factor[:, None, None] * x[-1].float())
+    # offsets: sort writes them, the products read them (the row's factor tells whose it was)
+    for i in range(n):
+        pts.gemm_expert_sort(h, tokens, k, E, ids[i], off, row_of, src)
+        pts.gemm_run_experts(h, rows, E, dim, dim, xs, B, off, got[i], F16)
+    torch.cuda.synchronize()
+    for i in range(n):
+        e = ids[i].flatten().sort()[0]
+        assert torch.equal(got[i].float(), (e + 1).float()[:, None] * xs.float()), i
