@@ -4,8 +4,9 @@ The translation units (the wide-tile 1-SM kernels, the 2-SM kernels, the
 narrow-tile 1-SM and 2-SM kernels, the C ABI, the allocation-free entry point,
 the tensor-pipe peak probe, and the expert layer's products, row kernels,
 4-bit product and C ABI) are compiled in parallel, then linked with the static
-CUDA runtime.  Nothing is rebuilt when the library is newer than every source
-file.
+CUDA runtime.  The expert layer's Python calls (pts_experts.so, a CPython
+extension that links to the library) are built after it.  Nothing is rebuilt
+when both are newer than every source file.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libpts_gemm.so")
+EXPERTS = os.path.join(LIBDIR, "pts_experts.so")
 UNITS = ["gemm_cg1.cu", "gemm_cg2.cu", "gemm_narrow.cu", "gemm_narrow_cg2.cu", "gemm_api.cu", "gemm_noalloc.cu",
          "peak_probe.cu", "expert_fwd.cu", "expert_dgrad.cu", "expert_wgrad.cu", "expert_route.cu", "nibble_f16.cu",
          "nibble_bf16.cu",
@@ -42,9 +45,9 @@ def _sources():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXPERTS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXPERTS))
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
@@ -73,6 +76,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = EXPERTS + ".tmp"
+    r = subprocess.run([cc, *FLAGS, "-shared", "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
+                        os.path.join(CSRC, "expert_binding.cpp"), "-cudart", "none", "-L" + LIBDIR, "-lpts_gemm",
+                        "-Xlinker", "-rpath,$ORIGIN", "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"expert_binding.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXPERTS)
     return LIB
 
 
