@@ -37,8 +37,8 @@
 // takes in, so a tile of 200 rows runs hardly faster than one of 256 (8192 rows
 // over 16 experts: 232 us uneven, 213 even).  Few rows: the weights' bytes, 5.8
 // TB/s, with tiles of 64 rows and 8 stages.  The weights' gradient loses about
-// 1 us per tile to the cleared step where rows are no multiple of 16 (2047 and
-// 2049 per expert 343 us, 2048 312).
+// 0.5 us per tile to the cleared step where rows are no multiple of 16 (2047 and
+// 2049 per expert 325 us, 2048 312).
 //
 // Warp roles as in gemm_kernel.cuh: producer, MMA, 4 epilogue warps, scheduler
 // (a static stride over the tiles of all experts, which it counts from the
@@ -99,8 +99,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     const uint32_t full0 = bar0;                             // + 8*s
     const uint32_t empty0 = bar0 + 8 * kMaxStages;           // + 8*s
     const uint32_t fix0 = bar0 + 16 * kMaxStages;            // + 8*s (WGRAD)
-    const uint32_t peer0 = bar0 + 24 * kMaxStages;           // + 8*s (WGRAD, leader)
-    const uint32_t acc_full0 = bar0 + 32 * kMaxStages;       // + 8*b
+    const uint32_t acc_full0 = bar0 + 24 * kMaxStages;       // + 8*b
     const uint32_t acc_empty0 = acc_full0 + 16;              // + 8*b
     const uint32_t ring_full0 = acc_empty0 + 16;             // + 8*r
     const uint32_t ring_empty0 = ring_full0 + 8 * kRing;     // + 8*r
@@ -123,12 +122,10 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, 1);
+            // (of a pair in WGRAD: both CTAs' clearing warps, or the leader's producer twice)
+            mbar_init(full0 + 8 * s, MODE == EXPERT_WGRAD ? CG : 1);
             mbar_init(empty0 + 8 * s, 1);
-            if (MODE == EXPERT_WGRAD) {
-                mbar_init(fix0 + 8 * s, 1);
-                mbar_init(peer0 + 8 * s, 1);
-            }
+            if (MODE == EXPERT_WGRAD) mbar_init(fix0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
@@ -256,6 +253,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 // where this takes 607); a stage that is cleared first is announced by
                 // each CTA to itself
                 if (!pair || leader) mbar_arrive_expect_tx_if(one, fb, pair ? CG * tx : tx);
+                if (MODE == EXPERT_WGRAD && pair && leader) mbar_arrive_if(one, fb);
                 auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
                     if (pair)
                         tma_load_3d_pair(one, dst, m, fbc, x, y, z);
@@ -537,7 +535,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
         // for this CTA's loads of it, clear the rows behind the end in both
         // operands, and hand the stage to the MMA warp.
         int stage = 0;
-        uint32_t phases = 0;   // bit s: the parity of fix (and peer) barrier s that comes next
+        uint32_t phases = 0;   // bit s: the parity of fix barrier s that comes next
         for (int i = 0;; ++i) {
             ExpertItem t;
             if (ring_read(i, t) <= 0) break;
@@ -561,12 +559,8 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (CG == 2 && !leader) {
-                mbar_arrive_cluster_if(one, mapa(peer0 + 8 * s, 0u));
-            } else {   // the stage is whole when the peer's part is cleared too
-                if (CG == 2 && !ctl.wait_all(peer0 + 8 * s, (phases >> s) & 1u, WHERE_FULL)) break;
-                mbar_arrive_if(one, full0 + 8 * s);
-            }
+            if (CG == 2 && !leader) mbar_arrive_cluster_if(one, mapa(full0 + 8 * s, 0u));
+            else mbar_arrive_if(one, full0 + 8 * s);
             phases ^= 1u << s;
             stage = (stage + stages_used) % S;
         }

@@ -37,7 +37,7 @@ __host__ __device__ constexpr int expert_threads(int mode) { return kThreads + (
 __host__ __device__ constexpr int expert_smem_bytes(int cg, int bn, int stages)
 {
     return 1024 + stages * kb_per_stage(cg) * (kRowsPerCta + bn / cg) * kKBlockBytes + epi_bytes()
-           + 8 * (4 * kMaxStages + 4 + 2 * kRing) + 16   // mbarriers, alignment
+           + 8 * (3 * kMaxStages + 4 + 2 * kRing) + 16   // mbarriers, alignment
            + 4 * kRingWords * kRing + 16;                // ring payload, TMEM base, abort flag
 }
 

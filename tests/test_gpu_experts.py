@@ -382,6 +382,46 @@ def test_nibble(h, counts, N, K, group, zeros, dtype):
     assert (C[off:] == 7.0).all()
 
 
+NIBBLE_MORE = [  # above 8 rows per expert
+    ([9], 8, 32, 32), ([16], 264, 4096, 128), ([17], 24, 96, 64), ([12], 1000, 544, 32), ([31], 40, 1056, 128),
+    ([20, 0, 9, 40], 72, 224, 64), ([33, 1, 16, 17, 0], 136, 352, 32), ([18] * 33, 48, 160, 128), ([24], 4096, 8224, 64),
+    ([11], 2432, 16384, 32), ([25, 8], 520, 12320, 128), ([15], 8, 128, 128), ([10, 10, 10], 16, 8192, 32),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=ids16)
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("counts,N,K,group", NIBBLE_MORE)
+def test_nibble_of_more_rows(h, counts, N, K, group, zeros, dtype):
+    test_nibble(h, counts, N, K, group, zeros, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=ids16)
+def test_nibble_of_more_rows_exact(h, dtype):
+    """Every code, every position, rows on both sides of the eighth."""
+    rows, N, K, group = 11, 16, 128, 32
+    B, s, z, w = packed(1, N, K, group, dtype, True, 43, scale=0.5)
+    A = torch.zeros(rows, K, dtype=TORCH[dtype], device="cuda")
+    C = torch.empty(rows, N, dtype=TORCH[dtype], device="cuda")
+    for k in range(K):
+        A.zero_()
+        A[2, k], A[9, k] = 2.0, -1.0
+        pts.gemm_run_nibble(h, rows, 1, N, K, group, A, B, s, z, None, C, dtype)
+        want = torch.zeros(rows, N, dtype=torch.float64, device="cuda")
+        want[2], want[9] = 2.0 * w[0, :, k], -w[0, :, k]
+        assert torch.equal(C.double(), want), k
+
+
+def test_nibble_rows_keep_their_infinities_above_eight(h):
+    B, s, z, w = packed(1, 24, 64, 32, F16, False, 44)
+    A = rand((21, 64), F16, 45)
+    A[10, 7] = float("inf")
+    C = torch.empty(21, 24, dtype=torch.float16, device="cuda")
+    pts.gemm_run_nibble(h, 21, 1, 24, 64, 32, A, B, s, z, None, C, F16)
+    others = [i for i in range(21) if i != 10]
+    assert torch.isfinite(C[others]).all() and not torch.isfinite(C[10][w[0, :, 7] != 0]).any()
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=ids16)
 def test_nibble_exact(h, dtype):
     """Every code, every position: small integers and a power of two are exact."""
