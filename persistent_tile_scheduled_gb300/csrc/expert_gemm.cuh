@@ -252,30 +252,33 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 // peer through a remote arrival, took 862 us for 16384 rows of 8192 x 4096
                 // where this takes 607); a stage that is cleared first is announced by
                 // each CTA to itself
-                if (!pair || leader) mbar_arrive_expect_tx_if(one, fb, pair ? CG * tx : tx);
-                if (MODE == EXPERT_WGRAD && pair && leader) mbar_arrive_if(one, fb);
-                auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
-                    if (pair)
-                        tma_load_3d_pair(one, dst, m, fbc, x, y, z);
-                    else
-                        tma_load_3d(one, dst, m, fbc, x, y, z);
-                };
-                const uint32_t da = sA + stage * SA, db = sB + stage * SB;
-                const int c = kb * KELEMS;
-                if constexpr (kWmn) {
+                if (elect_one()) {
+                    if (!pair || leader) mbar_arrive_expect_tx_if(1u, fb, pair ? CG * tx : tx);
+                    if (MODE == EXPERT_WGRAD && pair && leader) mbar_arrive_if(1u, fb);
+                    auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
+                        if (pair)
+                            tma_load_3d_pair(1u, dst, m, fbc, x, y, z);
+                        else
+                            tma_load_3d(1u, dst, m, fbc, x, y, z);
+                    };
+                    const uint32_t da = sA + stage * SA, db = sB + stage * SB;
+                    const int c = kb * KELEMS;
+                    if constexpr (kWmn) {
 #pragma unroll
-                    for (int b = 0; b < kRowsPerCta / 64; ++b)
-                        load(da + b * kBlock, &tmW, wf + 64 * b, t.c0 + c, MODE == EXPERT_DGRAD ? t.e : 0);
-                } else {
-                    for (int j = 0; j < nk; ++j) load(da + j * (SA / KBS), &tmW, c + j * KELEMS, wf, t.e);
+                        for (int b = 0; b < kRowsPerCta / 64; ++b)
+                            load(da + b * kBlock, &tmW, wf + 64 * b, t.c0 + c, MODE == EXPERT_DGRAD ? t.e : 0);
+                    } else {
+                        for (int j = 0; j < nk; ++j) load(da + j * (SA / KBS), &tmW, c + j * KELEMS, wf, t.e);
+                    }
+                    if constexpr (kXmn) {
+                        for (int b = 0; b < xloads; ++b) load(db + b * kBlock, mx, xrow + 64 * b, t.c0 + c, 0);
+                    } else {
+                        for (int j = 0; j < nk; ++j)
+                            for (int b = 0; b < xloads; ++b)
+                                load(db + j * (SB / KBS) + b * xbox, mx, c + j * KELEMS, xrow + 16 * b, 0);
+                    }
                 }
-                if constexpr (kXmn) {
-                    for (int b = 0; b < xloads; ++b) load(db + b * kBlock, mx, xrow + 64 * b, t.c0 + c, 0);
-                } else {
-                    for (int j = 0; j < nk; ++j)
-                        for (int b = 0; b < xloads; ++b)
-                            load(db + j * (SB / KBS) + b * xbox, mx, c + j * KELEMS, xrow + 16 * b, 0);
-                }
+                __syncwarp();
                 ++issued;
                 if (++stage == S) {
                     stage = 0;
@@ -327,27 +330,30 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                     }
                     tc_fence_after();
                     const int nk = t.nkb - kb < KBS ? t.nkb - kb : KBS;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < KBS; ++j) {
-                        if (j >= nk) break;
-                        // (the next k-block of an MN-major stage: 64 rows on in every block)
-                        const uint32_t aa = sA + stage * SA + j * (kWmn ? 64 * 128 : SA / KBS);
-                        const uint32_t ab = sB + stage * SB + j * (kXmn ? 64 * 128 : SB / KBS);
-                        const uint64_t ad = kWmn ? smem_desc_mn_sw128<64 * KBS>(aa) : smem_desc_sw128(aa);
-                        const uint64_t bd = kXmn ? smem_desc_mn_sw128<64 * KBS>(ab) : smem_desc_sw128(ab);
-                        // an instruction takes 32 bytes of a K-major row, or 16 contraction rows of 128 bytes
-                        constexpr uint64_t da = kWmn ? 128 : 2, db = kXmn ? 128 : 2;
-                        int steps = 4;
-                        if constexpr (kXmn) {
-                            const int left = t.c_rows - (kb + j) * KELEMS;
-                            steps = left >= KELEMS ? 4 : (left + 15) / 16;
+                        for (int j = 0; j < KBS; ++j) {
+                            if (j >= nk) break;
+                            // (the next k-block of an MN-major stage: 64 rows on in every block)
+                            const uint32_t aa = sA + stage * SA + j * (kWmn ? 64 * 128 : SA / KBS);
+                            const uint32_t ab = sB + stage * SB + j * (kXmn ? 64 * 128 : SB / KBS);
+                            const uint64_t ad = kWmn ? smem_desc_mn_sw128<64 * KBS>(aa) : smem_desc_sw128(aa);
+                            const uint64_t bd = kXmn ? smem_desc_mn_sw128<64 * KBS>(ab) : smem_desc_sw128(ab);
+                            // an instruction takes 32 bytes of a K-major row, or 16 contraction rows of 128 bytes
+                            constexpr uint64_t da = kWmn ? 128 : 2, db = kXmn ? 128 : 2;
+                            int steps = 4;
+                            if constexpr (kXmn) {
+                                const int left = t.c_rows - (kb + j) * KELEMS;
+                                steps = left >= KELEMS ? 4 : (left + 15) / 16;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < steps) umma<KIND, CG>(1u, d, ad + da * k, bd + db * k, idesc,
+                                               (kb + j != 0 || k != 0) ? 1u : 0u);
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma<KIND, CG>(k < steps ? one : 0u, d, ad + da * k, bd + db * k, idesc,
-                                           (kb + j != 0 || k != 0) ? 1u : 0u);
+                        umma_commit<CG>(1u, empty0 + 8 * stage, 0x3);
                     }
-                    umma_commit<CG>(one, empty0 + 8 * stage, 0x3);
+                    __syncwarp();
                     last_stage = stage;
                     last_phase = phase;
                     if (++stage == S) {
@@ -356,7 +362,8 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                     }
                 }
                 if (!ok) break;
-                umma_commit<CG>(one, acc_full0 + 8 * acc, 0x3);
+                if (elect_one()) umma_commit<CG>(1u, acc_full0 + 8 * acc, 0x3);
+                __syncwarp();
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;

@@ -13,6 +13,20 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 
+// True in one lane of a converged warp, always the same.  What one lane issues
+// (MMAs, commits) stands in a branch on this: the compiler then knows that
+// there is one lane, and keeps addresses and descriptors in uniform registers;
+// under a predicate of its own each instruction takes some 200 cycles to issue.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(yes));
+    return yes != 0;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns()
 {
     uint64_t t;
