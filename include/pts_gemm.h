@@ -406,8 +406,9 @@ gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t expe
  *   offsets: as above, or NULL with experts == 1 (every row uses that matrix).
  * group: 32, 64 or 128 (the last group may be short); K % 32 == 0, N % 8 == 0;
  * experts * N at most GEMM_EXPERT_MAX_SIZE too.
- * Products are exact and sums fp32.  Made for a few rows per expert: the cost is
- * the weights' bytes, read once for every 8 rows of an expert. */
+ * Products are exact and sums fp32.  Made for a few to some hundred rows per
+ * expert: the weights are read and expanded once for every 8, 32 or 64 rows of
+ * an expert, whichever is reckoned to be faster for the sizes. */
 gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,
                               const void *A, const void *B, const void *scales, const uint8_t *zeros,
                               const int32_t *offsets, void *C, gemm_dtype_t dtype, void *stream);

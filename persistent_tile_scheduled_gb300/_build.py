@@ -3,7 +3,7 @@
 The translation units (the wide-tile 1-SM kernels, the 2-SM kernels, the
 narrow-tile 1-SM and 2-SM kernels, the C ABI, the allocation-free entry point,
 the tensor-pipe peak probe, and the expert layer's products, row kernels,
-4-bit product and C ABI) are compiled in parallel, then linked with the static
+4-bit products and C ABI) are compiled in parallel, then linked with the static
 CUDA runtime.  The expert layer's Python calls (pts_experts.so, a CPython
 extension that links to the library) are built after it.  Nothing is rebuilt
 when both are newer than every source file.
@@ -26,8 +26,7 @@ LIB = os.path.join(LIBDIR, "libpts_gemm.so")
 EXPERTS = os.path.join(LIBDIR, "pts_experts.so")
 UNITS = ["gemm_cg1.cu", "gemm_cg2.cu", "gemm_narrow.cu", "gemm_narrow_cg2.cu", "gemm_api.cu", "gemm_noalloc.cu",
          "peak_probe.cu", "expert_fwd.cu", "expert_dgrad.cu", "expert_wgrad.cu", "expert_route.cu", "nibble_f16.cu",
-         "nibble_bf16.cu",
-         "expert_api.cu"]
+         "nibble_bf16.cu", "nibble_rows_f16.cu", "nibble_rows_bf16.cu", "expert_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

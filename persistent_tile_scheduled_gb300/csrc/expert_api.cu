@@ -126,6 +126,42 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     return launched(ops.launch(mw, mx, mxs, mo, p, static_cast<int>(clusters) * cg, smem, stream, overlap(h)));
 }
 
+// How the product with 4-bit weights is done: rows of a block (8: nibble.cuh, 32
+// or 64: nibble_rows.cuh, there with `cluster` CTAs to a tile's contraction).
+struct NibbleForm {
+    int block_rows, cluster;
+};
+
+// The form that should take the least time, each by what it takes (GB300, us; the
+// groups' size and the zeros change it little).  By 8: 3.4 and 1 per 8.2 million
+// weights of each row block.  By 32 or 64: 5.2 and, of a CTA, 0.95 or 1.5 per 256
+// of the contraction of a tile of 128 features.  Measured / so reckoned:
+//   rows of 8192^2         8: 13.8 / 11.6    16: 20.4 / 19.8, by 32 20.5 / 20.4
+//                          24: 31.4 / 28, by 32 20.6 / 20.4    64: 69 / 69, by 64 30.5 / 29
+//   16 rows of 1000 x 2048 4.1 / 3.9, by 32 7.6 / 7.1
+//   32 experts, 2048 x 4096, 10 rows each in the mean 57 / 59, by 32 63 / 66; 16 experts,
+//   24 rows each 59 / 58, by 32 34 / 36
+// The rows of each expert are device data: an expert's last block is taken as 0.45 full.
+NibbleForm nibble_form(const gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, bool spread)
+{
+    auto blocks = [&](int of) -> double {
+        if (!spread) return static_cast<double>((rows + of - 1) / of);
+        const double n = static_cast<double>(rows) / of + 0.45 * static_cast<double>(experts), used = static_cast<double>(rows < experts ? rows : experts);
+        return n > used ? n : used;
+    };
+    NibbleForm best{8, 1};
+    double least = 3.4 + blocks(8) * static_cast<double>(N) * static_cast<double>(K) / 8.2e6;
+    const double features = static_cast<double>((N + kNibWideFeatures - 1) / kNibWideFeatures);
+    const double stages = static_cast<double>((K + kNibStageK - 1) / kNibStageK);
+    for (int of = 32; of <= 64; of += 32)
+        for (int c = 1; c <= kNibMaxCtas; c *= 2) {
+            const double rounds = std::ceil(blocks(of) * features * c / h->sm_count), each = std::ceil(stages / c);
+            const double time = (c == 1 ? 5.2 : 5.2 * rounds) + rounds * each * (of == 32 ? 0.95 : 1.5);
+            if (time < least) least = time, best = NibbleForm{of, c};
+        }
+    return best;
+}
+
 gemm_status_t check_product(gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, const int32_t *offsets)
 {
     if (h == nullptr || rows < 0 || experts < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
@@ -272,7 +308,9 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     if ((offsets == nullptr && experts != 1) || !aligned4(offsets)) return GEMM_ERR_INVALID_ARG;
     if (experts > kMaxSize / N) return GEMM_ERR_INVALID_ARG;   // rows of the weights
     // the kernel counts its pieces of work in 32 bits
-    const int64_t max_blocks = rows / 8 + (rows < experts ? rows : experts);
+    const NibbleForm form = nibble_form(h, rows, experts, N, K, offsets != nullptr);
+    const int64_t used = rows < experts ? rows : experts;
+    const int64_t max_blocks = (rows + (form.block_rows - 1) * used) / form.block_rows;
     if (max_blocks * (N / 16 + 1) > 2000000000) return GEMM_ERR_INVALID_ARG;
     if (C == nullptr || !aligned16(C)) return GEMM_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || B == nullptr || scales == nullptr)) return GEMM_ERR_INVALID_ARG;
@@ -292,14 +330,23 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     p.zeros = zeros;
     p.offsets = offsets;
     p.c = C;
+    p.block_rows = form.block_rows;
+    p.cluster = form.cluster;
     p.max_blocks = static_cast<int32_t>(max_blocks);
     p.ctas = h->sm_count;
     p.timeout_ns = h->opts.timeout_ns;
     p.status = h->d_status;
-    CUtensorMap mb;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    NibPrepared *prepared = &h->nibble[dtype];
+    CUtensorMap mb, mx;
     std::memset(&mb, 0, sizeof(mb));
-    if (K > 0 && !encode_map3(h, &mb, B, 1, experts * N, K / 2, GEMM_E4M3, kNibFeatures, 128)) return GEMM_ERR_INVALID_ARG;
-    return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, &h->nibble[dtype], static_cast<cudaStream_t>(stream), overlap(h)));
+    mx = mb;
+    const uint32_t features = form.block_rows == 8 ? kNibFeatures : kNibWideFeatures;
+    if (K > 0 && !encode_map3(h, &mb, B, 1, experts * N, K / 2, GEMM_E4M3, features, kNibStageK / 2)) return GEMM_ERR_INVALID_ARG;
+    if (form.block_rows == 8)
+        return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, prepared, s, overlap(h)));
+    if (K > 0 && !encode_map3(h, &mx, A, 1, rows, K, dtype, static_cast<uint32_t>(form.block_rows), 64)) return GEMM_ERR_INVALID_ARG;
+    return launched((dtype == GEMM_F16 ? launch_nibble_rows_f16 : launch_nibble_rows_bf16)(mb, mx, p, prepared, s, overlap(h)));
 }
 
 }  // extern "C"

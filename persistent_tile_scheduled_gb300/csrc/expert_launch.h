@@ -72,7 +72,7 @@ cudaError_t launch_expert_combine_grad(int kind, const void *dy, const void *ys,
                                        void *dys, float *dw, int tokens, int top_k, int chunks, cudaStream_t stream,
                                        bool overlap);
 
-// ---- few rows times 4-bit weights (nibble.cuh) ---------------------------------
+// ---- rows times 4-bit weights (nibble.cuh: a few, nibble_rows.cuh: more) ---------------------------------
 
 struct NibbleParams {
     int32_t rows, experts, N, K, group, groups;
@@ -82,9 +82,10 @@ struct NibbleParams {
     const uint8_t *zeros;     // experts x N x groups, or null (8)
     const int32_t *offsets;   // experts + 1, or null (one expert has every row)
     void *c;                  // rows x N, 16-bit
-    int32_t max_blocks;       // blocks of 8 rows that ascending offsets can make
+    int32_t block_rows;       // rows of a block: 8 (nibble.cuh), 32 or 64 (nibble_rows.cuh)
+    int32_t max_blocks;       // blocks that ascending offsets can make
     int32_t ctas;             // SMs
-    int32_t cluster, k_warps; // set by the launch: CTAs and warps of a CTA that share a contraction
+    int32_t cluster, k_warps; // CTAs and warps of a CTA that share a contraction (nibble.cuh: set by the launch)
     uint64_t timeout_ns;
     int32_t *status;
 };
@@ -92,6 +93,7 @@ struct NibbleParams {
 constexpr int kNibFeatures = 32;   // features of a tile, rows of the weights' TMA box (128 bytes wide)
 constexpr int kNibStageK = 256;    // contraction per unit of work
 constexpr int kNibMaxCtas = 4;     // CTAs of a cluster
+constexpr int kNibWideFeatures = 128;   // features of a tile where rows are more
 
 // What a handle keeps per dtype: the kernels whose shared-memory limit is
 // raised (a bit each), and the clusters of 2 and 4 CTAs the device holds.
@@ -104,5 +106,9 @@ cudaError_t launch_nibble_f16(const CUtensorMap &b, const NibbleParams &p, NibPr
                               bool overlap);
 cudaError_t launch_nibble_bf16(const CUtensorMap &b, const NibbleParams &p, NibPrepared *prepared, cudaStream_t stream,
                                bool overlap);
+cudaError_t launch_nibble_rows_f16(const CUtensorMap &b, const CUtensorMap &x, const NibbleParams &p, NibPrepared *prepared,
+                                   cudaStream_t stream, bool overlap);
+cudaError_t launch_nibble_rows_bf16(const CUtensorMap &b, const CUtensorMap &x, const NibbleParams &p, NibPrepared *prepared,
+                                    cudaStream_t stream, bool overlap);
 
 }  // namespace pts

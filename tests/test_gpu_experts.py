@@ -396,6 +396,50 @@ def test_nibble_of_more_rows(h, counts, N, K, group, zeros, dtype):
     test_nibble(h, counts, N, K, group, zeros, dtype)
 
 
+NIBBLE_MANY = [  # enough rows that the weights are expanded for 32 or 64 of them at a time; odd sizes on both sides
+    ([33], 4104, 4128, 32), ([64], 4096, 8192, 64), ([24], 8200, 8224, 128), ([129], 1000, 4064, 64), ([250], 136, 8160, 32),
+    ([500], 520, 2080, 128), ([140, 0, 77, 164, 33], 1032, 2080, 32), ([65, 66, 1, 0, 200], 2056, 1056, 64),
+    ([40] * 33, 264, 1184, 128), ([70, 3] * 20, 1096, 544, 32), ([400, 30], 2048, 96, 64), ([31, 33] * 16, 1032, 1536, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=ids16)
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("counts,N,K,group", NIBBLE_MANY)
+def test_nibble_of_many_rows(h, counts, N, K, group, zeros, dtype):
+    test_nibble(h, counts, N, K, group, zeros, dtype)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_nibble_of_many_rows_exact(h, group):
+    """Every code: row r takes weight r of its 512, times a power of two, so each result is one weight, exactly."""
+    rows, N, K = 512, 2056, 512
+    B, s, z, w = packed(1, N, K, group, BF16, True, 43, scale=0.5)
+    A = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    A[torch.arange(rows), torch.arange(rows)] = 2.0
+    C = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    pts.gemm_run_nibble(h, rows, 1, N, K, group, A, B, s, z, None, C, BF16)
+    assert torch.equal(C.double(), 2.0 * w[0].T)
+
+
+def test_nibble_of_many_rows_keeps_infinities(h):
+    """An infinity in one row reaches that row alone, an infinite scale its feature alone."""
+    rows, N, K = 300, 1032, 1056
+    B, s, z, w = packed(1, N, K, 64, F16, False, 44)
+    A = rand((rows, K), F16, 45)
+    A[10, 7] = float("inf")
+    C = torch.empty(rows, N, dtype=torch.float16, device="cuda")
+    pts.gemm_run_nibble(h, rows, 1, N, K, 64, A, B, s, z, None, C, F16)
+    others = [i for i in range(rows) if i != 10]
+    assert torch.isfinite(C[others]).all() and not torch.isfinite(C[10][w[0, :, 7] != 0]).any()
+    A, B, s = torch.ones(rows, K).half().cuda(), torch.full_like(B, 0x99), torch.ones_like(s)
+    s[0, 5, -1] = float("inf")
+    pts.gemm_run_nibble(h, rows, 1, N, K, 64, A, B, s, z, None, C, F16)
+    want = torch.full_like(C, float(K))
+    want[:, 5] = float("inf")
+    assert torch.equal(C, want)
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=ids16)
 def test_nibble_of_more_rows_exact(h, dtype):
     """Every code, every position, rows on both sides of the eighth."""
