@@ -53,12 +53,12 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     const int kelems = dtype == GEMM_E4M3 ? 128 : 64;
     // Variant (cta_group 0).  Few rows per expert: the weights' bytes count, and
     // tiles of 64 rows leave room for 8 stages of them (us on GB300, this / pairs:
-    // 64 rows over 8 experts of 4096^2 45.3 / 46.7, 256 45.7 / 47.5, 2048 over 64 of
-    // 2048^2 84.5 / 88.8; but 512 over 8 56.8 / 49.1, an expert's rows then being
+    // 64 rows over 8 experts of 4096^2 44.9 / 47.6, 256 45.5 / 48.4, 2048 over 64 of
+    // 2048^2 85.3 / 90.3; but 512 over 8 53.1 / 49.9, an expert's rows then being
     // several tiles).  Else pairs from 14 k-blocks per tile, as in gemm_run: 16384
-    // over 32, K = 1024, 103 / 112 for singles, 300 over 19, K = 560, 6.6 / 5.7.  The
+    // over 32, K = 1024, 103 / 111 for singles, 300 over 19, K = 560, 6.6 / 5.5.  The
     // weights' gradient counts the k-blocks of an average expert's rows: 4096 over
-    // 4 34.7 / 35.6, 6000 over 24 42.7 / 37.2, 64 over 8 89 / 45.
+    // 4 33.5 / 33.1, 6000 over 24 42.2 / 36.7, 64 over 8 86 / 43.
     int cg = h->opts.cta_group;
     int bn = kExpertTileN;
     const int64_t length = mode == EXPERT_WGRAD ? rows / experts : contraction;

@@ -31,12 +31,12 @@
 //
 // What bounds it (GB300, bf16).  Many rows: the tensor pipe, 85 % busy over 16384
 // rows spread unevenly over 8 experts of 8192 x 4096 (580 us alone; back to back
-// under the power cap 684 us, spread evenly 648, one dense gemm_run of that size
-// 647).  An expert whose rows do not fill its tiles costs the weights' loads of a
+// under the power cap 656 to 670 us, one dense gemm_run of that size 647).  An expert whose rows do not fill its tiles costs the weights' loads of a
 // full one: a pair's stage is 64 KB per SM for 1024 cycles of MMA, the most an SM
 // takes in, so a tile of 200 rows runs hardly faster than one of 256 (8192 rows
-// over 16 experts: 232 us uneven, 213 even).  Few rows: the weights' bytes, 5.8
-// TB/s, with tiles of 64 rows and 8 stages.  The weights' gradient loses about
+// over 16 experts: 232 us uneven, 213 even).  Few rows: the weights' bytes, 6.2
+// TB/s, with tiles of 64 rows and 8 stages (45.1 us for 40 rows over 8 experts of
+// 4096^2 when each MMA was issued under a predicate, 43.3 by one elected lane).  The weights' gradient loses about
 // 0.5 us per tile to the cleared step where rows are no multiple of 16 (2047 and
 // 2049 per expert 325 us, 2048 312).
 //
