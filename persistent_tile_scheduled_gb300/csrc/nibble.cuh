@@ -113,7 +113,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Nibble
 {
     uint64_t t0 = 0;   // (the timer is slow to read: first after some tries)
     for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait_cta(bar, parity)) return true;
         if ((n & 255u) != 0) continue;
         if (t0 == 0) t0 = globaltimer_ns();
         if (globaltimer_ns() - t0 > p.timeout_ns) {
