@@ -28,7 +28,7 @@
 // every tile cost as many bytes from L2 as the weights.  A taker is a cluster
 // of 1, 2 or 4 CTAs, so that K up to 16384 has a warp per unit; for K below 4096
 // a CTA holds several takers.  (A CTA per 32 features and 8 warps, with the
-// rows loaded as they are needed: 35.2 us where this takes 26.6; 8 rows, 16384 x
+// rows loaded as they are needed: 35.2 us where this takes 25.8; 8 rows, 16384 x
 // 8192, groups of 32 with zeros, bf16.)
 // Weights arrive by TMA, 32 features x 128 contiguous bytes per unit: the MMA
 // wants thread t of a quad to hold the 8 weights that are word t of a 16-byte
