@@ -88,6 +88,18 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     if (tiles > (int64_t(1) << 30)) return GEMM_ERR_INVALID_ARG;
     int64_t clusters = h->opts.max_clusters > 0 && h->opts.max_clusters < resident ? h->opts.max_clusters : resident;
     if (clusters > tiles) clusters = tiles;
+    // Tiles for less than half the SMs: CTAs share a tile's contraction, 0.2 us per
+    // k-block saved for 2.8 us of joining (us, this / one CTA per tile: one row of 1024 x
+    // 8192 10.0 / 32.7, of 2048^2 8.4 / 10.8, of 8192^2, 2 CTAs, 27.6 / 34.1; but of 512 x
+    // 1024 7.2 / 6.8 and of 8192 x 1024 8.5 / 7.1).  Few clusters of 8 find room at once:
+    // 16 tiles of that contraction take 20.7 by 8 CTAs each, 14.6 by 4.
+    int split = 1;
+    const int64_t length_kb = (contraction + kelems - 1) / kelems;
+    if (mode == EXPERT_FWD && bn == kExpertTileNFew && h->opts.cta_group == 0 && h->opts.max_clusters == 0 && length_kb >= 24) {
+        while (split < 4 && tiles * split * 2 <= h->sm_count) split *= 2;
+        if (split == 4 && length_kb >= 64 && tiles * 16 <= h->sm_count) split = 8;
+        if (split == 2 && length_kb < 32) split = 1;
+    }
 
     CUtensorMap mw, mx, mxs, mo;
     std::memset(&mw, 0, sizeof(mw));
@@ -118,12 +130,13 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     p.out_rows = static_cast<int32_t>(N);
     p.stages = stages;
     p.group_m = h->opts.group_size_m;
+    p.split = split;
     p.out_scale = out_scale;
     p.offsets = offsets;
     p.out = out;
     p.timeout_ns = h->opts.timeout_ns;
     p.status = h->d_status;
-    return launched(ops.launch(mw, mx, mxs, mo, p, static_cast<int>(clusters) * cg, smem, stream, overlap(h)));
+    return launched(ops.launch(mw, mx, mxs, mo, p, static_cast<int>(clusters) * cg * split, smem, stream, overlap(h)));
 }
 
 // How the product with 4-bit weights is done: rows of a block (8: nibble.cuh, 32

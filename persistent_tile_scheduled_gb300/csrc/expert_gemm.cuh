@@ -39,6 +39,9 @@
 // 4096^2 when each MMA was issued under a predicate, 43.3 by one elected lane).  The weights' gradient loses about
 // 0.5 us per tile to the cleared step where rows are no multiple of 16 (2047 and
 // 2049 per expert 325 us, 2048 312).
+// Tiles for less than half the SMs (one token): 2, 4 or 8 CTAs share a tile's
+// contraction and add up through distributed shared memory, each its part of the
+// rows, in order (one row of 4096^2 11.3 us instead of 18.6).
 //
 // Warp roles as in gemm_kernel.cuh: producer, MMA, 4 epilogue warps, scheduler
 // (a static stride over the tiles of all experts, which it counts from the
@@ -111,8 +114,12 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     const uint32_t lane = lane_id();
     const uint32_t rank = (CG == 2) ? cluster_ctarank() : 0u;
     const bool leader = rank == 0;
-    const int cluster_id = static_cast<int>(blockIdx.x) / CG;
-    const int num_clusters = static_cast<int>(gridDim.x) / CG;
+    // few tiles: `split` CTAs share one's contraction, and have no other
+    constexpr bool kSplit = MODE == EXPERT_FWD && CG == 1 && BN == kExpertTileNFew;
+    const int split = kSplit ? p.split : 1;
+    const int share = kSplit && split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cluster_id = static_cast<int>(blockIdx.x) / (CG * split);
+    const int num_clusters = static_cast<int>(gridDim.x) / (CG * split);
 
     WaitCtl ctl;
     ctl.abort_addr = abort_flag;
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                             tma_load_3d(1u, dst, m, fbc, x, y, z);
                     };
                     const uint32_t da = sA + stage * SA, db = sB + stage * SB;
-                    const int c = kb * KELEMS;
+                    const int c = (kSplit ? t.c0 + kb : kb) * KELEMS;
                     if constexpr (kWmn) {
 #pragma unroll
                         for (int b = 0; b < kRowsPerCta / 64; ++b)
@@ -393,6 +400,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             const bool empty_sum = t.nkb == 0;
             if (!ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL)) break;
             tc_fence_after();
+            if (kSplit && split > 1) break;   // (the only tile; added up below)
             const uint32_t tbase = tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN);
             const int chunks = (t.n_len + 63) / 64;
             const int f = t.f0 + static_cast<int>(rank) * kRowsPerCta + static_cast<int>(q) * 32;
@@ -523,12 +531,14 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                         t.row_end = elo + ((it + 1) * size < ecnt ? (it + 1) * size : ecnt);
                         const int rows = t.row_end - t.row0;
                         t.n_len = (rows + kGran - 1) / kGran * kGran;
-                        t.nkb = nkb;
-                        t.c0 = t.c_rows = 0;
+                        t.c0 = kSplit ? nkb * share / split : 0;
+                        t.nkb = (kSplit ? nkb * (share + 1) / split : nkb) - t.c0;
+                        t.c_rows = 0;
                         if (rows > 0) {   // (rounding the tile size up may leave the last tile nothing)
                             ok = publish(i, true, t);
                             ++i;
                         }
+                        if (kSplit && split > 1) w = 1ll << 62;   // (the one tile; offsets that go back and forth claim more)
                     }
                     before += total;
                 }
@@ -574,6 +584,50 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
         __syncwarp();
     }
 
+    // ---- a tile whose contraction is shared ------------------------------------
+    if (kSplit && split > 1) {
+        // CTA j of the cluster adds up rows j * part ..: [CTA][row][feature], where the
+        // stages were; the tile is the ring's first item
+        const int part = BN / split, shift = __ffs(part) - 1;   // (split is 2, 4 or 8)
+        __syncthreads();
+        cluster_sync();   // (every CTA is through with its stages)
+        const bool published = mbar_try_wait(ring_full0, 0);
+        const uint4 v0 = ld_shared_v4(ring0), v1 = ld_shared_v4(ring0 + 16);
+        const bool there = published && v0.x != 0;
+        if (there && warp >= 2 && warp < 2 + kEpiWarps) {
+            const uint32_t q = warp & 3u;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem_base + ((q * 32u) << 16) + 32 * c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int row = 32 * c + i, to = row >> shift;
+                    st_cluster_u32(mapa(base + ((share * part + (row & (part - 1))) * kRowsPerCta + q * 32 + lane) * 4,
+                                        static_cast<uint32_t>(to)), v[i]);
+                }
+            }
+        }
+        cluster_sync();
+        if (there)
+            for (int i = static_cast<int>(threadIdx.x); i < part * kRowsPerCta / 2; i += static_cast<int>(blockDim.x)) {
+                const int row = i / (kRowsPerCta / 2), n = 2 * (i % (kRowsPerCta / 2));
+                float lo = 0.0f, hi = 0.0f;
+                for (int c = 0; c < split; ++c) {
+                    const uint32_t from = base + ((c * part + row) * kRowsPerCta + n) * 4;
+                    lo += __uint_as_float(ld_shared_u32(from));
+                    hi += __uint_as_float(ld_shared_u32(from + 4));
+                }
+                const long long out_row = static_cast<long long>(v0.w) + share * part + row;
+                const int f = static_cast<int>(v0.z) + n;
+                if (out_row < static_cast<int>(v1.x) && f < p.features)
+                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + out_row * p.features + f) =
+                        pack2<KIND>(__float_as_uint(lo), __float_as_uint(hi), p.out_scale);
+            }
+    }
+
     // ---- teardown ------------------------------------------------------------
     tc_fence_before();
     __syncthreads();
@@ -586,8 +640,8 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
 
 template <int KIND, int MODE, int CG, int BN>
 struct ExpertInst {
-    static void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, int smem, cudaStream_t stream,
-                       bool overlap)
+    static void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, int cluster, int smem,
+                       cudaStream_t stream, bool overlap)
     {
         cfg = cudaLaunchConfig_t{};
         cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -601,9 +655,9 @@ struct ExpertInst {
             attr[n].val.programmaticStreamSerializationAllowed = 1;
             ++n;
         }
-        if (CG == 2) {
+        if (cluster > 1) {
             attr[n].id = cudaLaunchAttributeClusterDimension;
-            attr[n].val.clusterDim.x = 2;
+            attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
             attr[n].val.clusterDim.y = 1;
             attr[n].val.clusterDim.z = 1;
             ++n;
@@ -623,7 +677,7 @@ struct ExpertInst {
         if (CG == 1) return cudaSuccess;
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
-        config(cfg, attr, 2, smem, nullptr, false);
+        config(cfg, attr, 2, CG, smem, nullptr, false);
         return cudaOccupancyMaxActiveClusters(clusters, expert_kernel<KIND, MODE, CG, BN>, &cfg);
     }
 
@@ -632,7 +686,7 @@ struct ExpertInst {
     {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
-        config(cfg, attr, grid, smem, stream, overlap);
+        config(cfg, attr, grid, CG * p.split, smem, stream, overlap);
         return cudaLaunchKernelEx(&cfg, expert_kernel<KIND, MODE, CG, BN>, w, x, xs, o, p);
     }
 

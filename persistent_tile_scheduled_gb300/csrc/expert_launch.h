@@ -21,6 +21,7 @@ struct ExpertParams {
     int32_t contraction;   // K (FWD), N (DGRAD); unused in WGRAD, where it is an expert's rows
     int32_t out_rows;      // WGRAD: output rows per expert
     int32_t stages;
+    int32_t split;                    // CTAs that share a tile's contraction
     int32_t group_m;       // row tiles per group of the tile order
     float out_scale;
     const int32_t *offsets;   // experts + 1, device

@@ -20,8 +20,8 @@
 // contraction and adds up through distributed shared memory, every CTA its part
 // of the rows, in order.
 //
-// What bounds it (bf16, groups of 64): 32 rows of 8192^2 take 20.7 us, 8 at a time
-// 37; 64 rows 30.5 and 69; 512 rows of 4096^2 49.5 and 121.  A CTA spends 0.95 us on
+// What bounds it (bf16, groups of 64): 32 rows of 8192^2 take 20.2 us, 8 at a time
+// 37; 64 rows 29.9 and 69; 512 rows of 4096^2 49.5 and 121.  A CTA spends 0.95 us on
 // 256 of its contraction (1.5 for 64 rows), mostly in the expanding warps: loads,
 // barriers and scales alone 0.45, the MMAs 0.3, the expanding 0.5; start and end
 // take 5 us, so that few weights are better off in nibble.cuh.  One elected lane
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(NibRowsShape<RB>::kThreads, 1)
     // ---- a cluster's sums ------------------------------------------------------
     if (ctas > 1) {
         // CTA j adds up rows j * part ..: [CTA][row][feature], where the stages were
-        const int part = RB / ctas;
+        const int part = RB / ctas, shift = __ffs(part) - 1;   // (2 or 4 CTAs)
         const bool there = tile0 < tiles;
         const Tile t = there ? tile_at(tile0) : Tile{};
         __syncthreads();
@@ -402,8 +402,8 @@ __global__ void __launch_bounds__(NibRowsShape<RB>::kThreads, 1)
             const int f = ((warp & 3) << 5) + lane, row0 = ((warp - kNrScaleWarp0) >> 2) * 32;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const int r = row0 + i, to = r / part;
-                st_cluster_f32(mapa(base + ((rank * part + r - to * part) * kNibWideFeatures + f) * 4, static_cast<uint32_t>(to)), acc[i]);
+                const int r = row0 + i, to = r >> shift;
+                st_cluster_f32(mapa(base + ((rank * part + (r & (part - 1))) * kNibWideFeatures + f) * 4, static_cast<uint32_t>(to)), acc[i]);
             }
         }
         cluster_sync();

@@ -221,6 +221,36 @@ def test_forward(hv, counts, spare, N, K, dtype):
     assert (C[off:] == 7.0).all()   # rows of no expert are not written
 
 
+# few tiles and a long contraction: CTAs that share it
+FEW = [([1], 0, 128, 1024), ([1], 0, 8, 4112), ([0, 0, 1, 0], 0, 2056, 2064), ([3, 0, 0, 2], 4, 136, 8208), ([0, 1], 1, 8192, 1536),
+       ([32], 0, 264, 1040), ([20, 9, 0], 3, 1000, 2000), ([0, 0, 64], 0, 512, 1104), ([0, 0, 65], 31, 72, 1504),
+       ([0] * 40 + [1, 0, 2], 0, 520, 1072), ([7, 1, 1, 7], 0, 1024, 4096), ([0, 0], 4, 256, 2048)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, E4M3], ids=ids16)
+@pytest.mark.parametrize("counts,spare,N,K", FEW)
+def test_forward_of_few_tiles(hv, counts, spare, N, K, dtype):
+    test_forward(hv, counts, spare, N, K, dtype)
+
+
+def test_few_tiles_exact_and_their_values_stay(h):
+    """Small integers are exact however the contraction is shared; an infinity stays with its row and feature."""
+    A, B = ints((6, 4096), F16, 4, 1), ints((5, 264, 4096), F16, 5, 1)
+    off = offsets_of([2, 0, 3, 0, 1])
+    C = torch.full((6, 264), 7.0, dtype=torch.float16, device="cuda")
+    pts.gemm_run_experts(h, 6, 5, 264, 4096, A, B, off, C, F16)
+    want = torch.cat([A[:2].double() @ B[0].double().T, A[2:5].double() @ B[2].double().T, A[5:].double() @ B[4].double().T])
+    assert torch.equal(C.double(), want)
+    A[3, 4000], B[1] = float("inf"), float("nan")
+    B[4, 17, 3] = float("nan")
+    pts.gemm_run_experts(h, 6, 5, 264, 4096, A, B, off, C, F16)
+    bad = ~torch.isfinite(C)
+    bad[3] &= B[2, :, 4000] == 0   # inf * 0 is NaN there, infinite elsewhere: all of row 3 may be
+    keep = torch.ones_like(bad)
+    keep[3], keep[5, 17] = False, False
+    assert not bad[keep].any() and torch.equal(C.double()[keep], want[keep]) and torch.isnan(C[5, 17])
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=ids16)
 @pytest.mark.parametrize("counts,spare,N,K", SHAPES)
 def test_dgrad(hv, counts, spare, N, K, dtype):
