@@ -199,7 +199,7 @@ gemm_status_t gemm_expert_sort(gemm_handle_t h, int64_t tokens, int64_t top_k, i
     if (!aligned4(expert_ids) || !aligned4(row_of) || !aligned4(src_of)) return GEMM_ERR_INVALID_ARG;
     if ((st = on_device(h)) != GEMM_OK) return st;
     return launched(launch_expert_sort(expert_ids, n, static_cast<int>(experts), offsets, row_of, src_of,
-                                       static_cast<cudaStream_t>(stream), overlap(h)));
+                                       h->sort_smem, static_cast<cudaStream_t>(stream), overlap(h)));
 }
 
 gemm_status_t gemm_expert_gather(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t dim, const void *X,

@@ -62,9 +62,9 @@ ExpertOps expert_ops_wgrad(int kind, int cg);
 
 constexpr int kMaxExpertsSorted = 1024;   // the sort keeps a count per warp and expert in shared memory
 
-// chunks: 16-byte pieces of a row
+// chunks: 16-byte pieces of a row; prepared: whether the handle has raised the sort's shared-memory limit (its two kernels)
 cudaError_t launch_expert_sort(const int32_t *ids, int64_t n, int experts, int32_t *offsets, int32_t *row_of,
-                               int32_t *src_of, cudaStream_t stream, bool overlap);
+                               int32_t *src_of, bool *prepared, cudaStream_t stream, bool overlap);
 cudaError_t launch_expert_gather(const void *x, const int32_t *row_of, void *xs, int tokens, int top_k, int chunks,
                                  cudaStream_t stream, bool overlap);
 cudaError_t launch_expert_combine(int kind, const void *ys, const int32_t *row_of, const float *w, void *y, int tokens,

@@ -410,13 +410,19 @@ long long piece_blocks(long long tokens, long long chunks, int pieces)
     return (tokens * chunks + kRowThreads * pieces - 1) / (kRowThreads * pieces);
 }
 
+// counts per warp and expert (an odd pitch), a row per expert, a sum per warp
+size_t sort_smem_bytes(int warps, int experts)
+{
+    return (static_cast<size_t>(warps) * (experts | 1) + experts + warps) * sizeof(uint32_t);
+}
+
 // threads of a block per token: one 16-byte chunk each, up to 256 (a warp where rows are empty: dweights is written)
 int row_threads(int chunks) { return chunks >= 256 ? 256 : (chunks < 1 ? 32 : (chunks + 31) / 32 * 32); }
 
 }  // namespace
 
 cudaError_t launch_expert_sort(const int32_t *ids, int64_t n, int experts, int32_t *offsets, int32_t *row_of,
-                               int32_t *src_of, cudaStream_t stream, bool overlap)
+                               int32_t *src_of, bool *prepared, cudaStream_t stream, bool overlap)
 {
     // Up to 1024: a warp per 32, the shortest chain of steps (32 over 8 experts 2.6
     // us, with 8 per lane 2.9).  Above 2048 8 CTAs, since a warp's scattered stores
@@ -425,11 +431,14 @@ cudaError_t launch_expert_sort(const int32_t *ids, int64_t n, int experts, int32
     const int ctas = n > 2048 ? kSortMaxCtas : 1, each = few ? 32 : 128;
     const int64_t wanted = (n + each * ctas - 1) / (each * ctas);
     const int warps = wanted < 1 ? 1 : (wanted > kSortMaxWarps ? kSortMaxWarps : static_cast<int>(wanted));
-    const size_t smem = (static_cast<size_t>(warps) * (experts | 1) + experts + warps) * sizeof(uint32_t);
+    const size_t smem = sort_smem_bytes(warps, experts);
     const auto kernel = few ? expert_sort_kernel<1> : expert_sort_kernel<8>;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // (the limit is the function's, on this device, whichever handle or thread launches it: always the most that any call needs)
+    if (smem > 48 * 1024 && !prepared[few]) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(sort_smem_bytes(kSortMaxWarps, kMaxExpertsSorted)));
         if (e != cudaSuccess) return e;
+        prepared[few] = true;
     }
     return go(kernel, ctas, warps * 32, smem, ctas, stream, overlap, ids, static_cast<int>(n), experts, offsets, row_of,
               src_of);

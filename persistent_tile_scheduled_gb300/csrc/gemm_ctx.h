@@ -74,6 +74,7 @@ struct gemm_ctx {
     // experts' products: resident clusters per dtype, mode and variant (0: single CTAs, 1: pairs,
     // 2: single CTAs with the short row tile); 0 = not asked yet
     int expert_clusters[3][3][3] = {};
+    bool sort_smem[2] = {};                   // gemm_expert_sort: limits raised, per kernel
     pts::NibPrepared nibble[2] = {};          // gemm_run_nibble, per dtype
 };
 
