@@ -73,7 +73,10 @@ typedef enum {
  * stage load (0-based) but does not issue it, so the MMA warp's wait on that
  * stage runs past timeout_ns.  The kernel records the time-out, stops every
  * role, frees its resources and returns; gemm_check then reports
- * GEMM_ERR_TIMEOUT and C is unspecified.  The context stays usable. */
+ * GEMM_ERR_TIMEOUT and C is unspecified.  The context stays usable.
+ * gemm_run_experts, its gradients and gemm_run_nibble issue that load but
+ * announce more bytes than it brings (with blocks of 8 rows gemm_run_nibble
+ * does so for every load), to the same effect. */
 
 typedef struct gemm_opts {
     int cta_group;                  /* 1 (128x256 tile per CTA) or 2 (256x256 per CTA pair);
@@ -339,8 +342,9 @@ gemm_status_t gemm_query_grouped(gemm_handle_t h, const gemm_group_problem_t *pr
  * rows counts as -1); an expert whose offsets decrease has no rows.
  * All arrays are contiguous, rows of a multiple of 16 bytes, 16-byte aligned
  * (int32 and fp32 arrays: 4-byte), and outputs do not overlap inputs.  Of the
- * handle's options these calls use cta_group, max_clusters, group_size_m,
- * timeout_ns (gemm_run_experts and its gradients) and overlap_launch. */
+ * handle's options these calls use overlap_launch; gemm_run_experts and its
+ * gradients cta_group, max_clusters and group_size_m too; and these and
+ * gemm_run_nibble timeout_ns and GEMM_DEBUG_FAULT_SKIP_TMA. */
 
 /* Sort tokens * top_k assignments by expert, stably: rows of one expert are in
  * the order of t * top_k + j.  An id outside [0, experts) marks an assignment

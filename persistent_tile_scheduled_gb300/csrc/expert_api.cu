@@ -31,6 +31,9 @@ gemm_status_t on_device(const gemm_ctx *h)
     return cudaSetDevice(h->device) == cudaSuccess ? GEMM_OK : cuda_fail(cudaErrorInvalidDevice);
 }
 
+// The stage load that announces too many bytes (GEMM_DEBUG_FAULT_SKIP_TMA), or -1.
+int32_t fault_load(const gemm_ctx *h) { return h->opts.debug_flags & GEMM_DEBUG_FAULT_SKIP_TMA ? h->opts.fault_arg : -1; }
+
 bool overlap(const gemm_ctx *h) { return h->opts.overlap_launch >= 0; }
 
 // Common checks of the row kernels: tokens x top_k assignments, rows of dim elements.
@@ -134,6 +137,7 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     p.out_scale = out_scale;
     p.offsets = offsets;
     p.out = out;
+    p.fault_load = fault_load(h);
     p.timeout_ns = h->opts.timeout_ns;
     p.status = h->d_status;
     return launched(ops.launch(mw, mx, mxs, mo, p, static_cast<int>(clusters) * cg * split, smem, stream, overlap(h)));
@@ -347,6 +351,7 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     p.cluster = form.cluster;
     p.max_blocks = static_cast<int32_t>(max_blocks);
     p.ctas = h->sm_count;
+    p.fault_load = fault_load(h);
     p.timeout_ns = h->opts.timeout_ns;
     p.status = h->d_status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -354,7 +359,8 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
     CUtensorMap mb, mx;
     std::memset(&mb, 0, sizeof(mb));
     mx = mb;
-    const uint32_t features = form.block_rows == 8 ? kNibFeatures : kNibWideFeatures;
+    // (by 8 the test hook is a box that is a row short of what every load announces)
+    const uint32_t features = form.block_rows == 8 ? kNibFeatures - (p.fault_load >= 0 ? 1 : 0) : kNibWideFeatures;
     if (K > 0 && !encode_map3(h, &mb, B, 1, experts * N, K / 2, GEMM_E4M3, features, kNibStageK / 2)) return GEMM_ERR_INVALID_ARG;
     if (form.block_rows == 8)
         return launched((dtype == GEMM_F16 ? launch_nibble_f16 : launch_nibble_bf16)(mb, p, prepared, s, overlap(h)));

@@ -228,11 +228,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
         bool ok = true;
         for (int i = 0;; ++i) {
             ExpertItem t;
-            const int got = ring_read(i, t);
-            if (got <= 0) {
-                ok = got == 0;
-                break;
-            }
+            if (ring_read(i, t) <= 0) break;
             const int xr = t.n_len / CG;   // this CTA's accumulator columns
             const int wf = t.f0 + static_cast<int>(rank) * kRowsPerCta;
             const int xrow = t.row0 + static_cast<int>(rank) * xr;
@@ -255,12 +251,14 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 const uint32_t fb = (fix ? fix0 : full0) + 8 * stage;
                 const bool pair = CG == 2 && !fix;
                 const uint32_t fbc = pair ? mapa(fb, 0u) : fb;
+                // (test hook: more bytes than come, so that the bounded wait on this stage runs out)
+                const uint32_t withheld = issued == p.fault_load ? 16u : 0u;
                 // a pair's leader announces both CTAs' bytes (each announcing its own, the
                 // peer through a remote arrival, took 862 us for 16384 rows of 8192 x 4096
                 // where this takes 607); a stage that is cleared first is announced by
                 // each CTA to itself
                 if (elect_one()) {
-                    if (!pair || leader) mbar_arrive_expect_tx_if(1u, fb, pair ? CG * tx : tx);
+                    if (!pair || leader) mbar_arrive_expect_tx_if(1u, fb, (pair ? CG * tx : tx) + withheld);
                     if (MODE == EXPERT_WGRAD && pair && leader) mbar_arrive_if(1u, fb);
                     auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
                         if (pair)
@@ -294,20 +292,15 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             }
             if (!ok) break;
         }
-        if (!ok) {
-            // Stopped early: let the loads already issued land before the CTA
-            // can exit (bounded; the peer cannot wait for a stage that the
-            // leader gave up on, so it lets 1 ms pass).
-            if (CG == 1 || leader) {
-                const long long n = issued < S ? issued : S;
-                for (long long j = 0; j < n; ++j) {
-                    const long long g = issued - 1 - j;
-                    ctl.drain(full0 + 8 * static_cast<int>(g % S), static_cast<uint32_t>((g / S) & 1), 10000000ull);
-                }
-            } else if (issued > 0) {
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 1000000ull) {
-                }
+        // Every load that was issued lands before the CTA can exit (bounded), also
+        // where another warp gave up on a stage after the last load was issued.  A
+        // leader's barriers count both CTAs' bytes; a load of its peer's that it did
+        // not announce is given time at the teardown.
+        if (CG == 1 || leader) {
+            const long long n = issued < S ? issued : S;
+            for (long long j = 0; j < n; ++j) {
+                const long long g = issued - 1 - j;
+                ctl.drain(full0 + 8 * static_cast<int>(g % S), static_cast<uint32_t>((g / S) & 1), 10000000ull);
             }
         }
         __syncwarp();
@@ -631,7 +624,18 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     // ---- teardown ------------------------------------------------------------
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();
+    if constexpr (CG == 2) {
+        // stopped early: a load of this CTA that the leader did not announce
+        // completes on a phase that cannot finish; let 1 ms pass, far longer than
+        // any load takes
+        if (!leader && warp == 0 && ld_shared_u32(abort_flag)) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000ull) {
+            }
+            __syncwarp();
+        }
+        cluster_sync();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc<CG>(tmem_base, kAccCols);

@@ -26,6 +26,7 @@ struct ExpertParams {
     float out_scale;
     const int32_t *offsets;   // experts + 1, device
     void *out;
+    int32_t fault_load;       // test hook: the stage load of a producer that announces too many bytes (-1: none)
     uint64_t timeout_ns;
     int32_t *status;
 };
@@ -87,6 +88,7 @@ struct NibbleParams {
     int32_t max_blocks;       // blocks that ascending offsets can make
     int32_t ctas;             // SMs
     int32_t cluster, k_warps; // CTAs and warps of a CTA that share a contraction (nibble.cuh: set by the launch)
+    int32_t fault_load;       // as above (nibble_rows.cuh)
     uint64_t timeout_ns;
     int32_t *status;
 };

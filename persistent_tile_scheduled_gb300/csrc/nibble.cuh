@@ -47,8 +47,8 @@ namespace {
 constexpr int kNibWarps = 16;
 constexpr int kNibRing = 2;             // units in flight per warp
 constexpr int kNibRows = 8;             // rows at a time: one MMA's
-constexpr int kNibSlots = 8;            // tiles whose sums a cluster gathers before they are stored
 constexpr int kNibStageBytes = kNibFeatures * kNibStageK / 2;
+constexpr int kNibSlots = 8;            // tiles whose sums a cluster gathers before they are stored
 constexpr int kNibPitch = kNibFeatures + 4;           // floats between rows of a tile's sums: no bank conflicts
 constexpr int kNibSums = kNibRows * kNibPitch;
 

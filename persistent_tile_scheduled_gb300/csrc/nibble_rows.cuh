@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(NibRowsShape<RB>::kThreads, 1)
                 const uint32_t at = base + s * Shape::kStageBytes;
                 const int k0 = st * kNibStageK;
                 if (elect_one()) {   // (a box behind the end of the contraction is zeros)
-                    mbar_arrive_expect_tx_if(1u, full0 + 8 * s, kNrPackedBytes + 4 * (RB * 128));
+                    // (test hook: more bytes than come, so that a bounded wait on this stage runs out)
+                    mbar_arrive_expect_tx_if(1u, full0 + 8 * s, kNrPackedBytes + 4 * (RB * 128) + (issued == p.fault_load ? 16u : 0u));
                     tma_load_3d(1u, at, &tmB, full0 + 8 * s, k0 / 2, t.row_b + t.n0, 0);
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
@@ -245,8 +246,9 @@ __global__ void __launch_bounds__(NibRowsShape<RB>::kThreads, 1)
                 if (++s == S) s = 0, phase ^= 1u;
             }
         }
-        if (!ok)   // let the loads already issued land before the CTA can exit (bounded)
-            for (int j = max(0, issued - S); j < issued; ++j) ctl.drain(full0 + 8 * (j % S), (j / S) & 1, 10000000ull);
+        // Every load that was issued lands before the CTA can exit (bounded), also where
+        // another warp gave up on a stage after the last load was issued.
+        for (int j = max(0, issued - S); j < issued; ++j) ctl.drain(full0 + 8 * (j % S), (j / S) & 1, 10000000ull);
     } else if (warp == 1) {
         // ================================ MMA ==================================
         constexpr uint32_t idesc = make_idesc<KIND, 1>(RB);
