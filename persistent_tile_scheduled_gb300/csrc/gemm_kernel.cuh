@@ -544,7 +544,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CG, BN))
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
-        bool ok = true;
         int maps_of = -1;   // grouped launch: the problem whose A and B maps this thread last acquired
         // Load k-blocks [kb_from, kb_to) of work item t (kb_from is the
         // item's first k-block or a stage boundary after it).
@@ -601,41 +600,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CG, BN))
         for (int i = 0;; ++i) {
             int w;
             WorkTile t;
-            if (!ring_read(i, w, t, true)) {
-                ok = false;
-                break;
-            }
-            if (w < 0) break;
+            if (!ring_read(i, w, t, true) || w < 0) break;
             if (leader) {
                 mbar_arrive_if(one, started_bar);
                 if (lane == 0) st_shared_u32(started_cnt, static_cast<uint32_t>(i + 1));
             }
-            if (!load_tile(t, t.kb_begin, t.kb_end)) {
-                ok = false;
-                break;
-            }
+            if (!load_tile(t, t.kb_begin, t.kb_end)) break;
         }
-        if (!ok) {
-            // Stopped early: let the loads already issued land before the
-            // CTA can exit (bounded).  The leader drains the full barriers of
-            // its last stages, on which both CTAs' loads of those stages
-            // complete.  The peer may have issued a stage the leader never
-            // armed (the leader stopped first): that load completes on a
-            // leader barrier whose phase can no longer finish, so nothing can
-            // be waited on for it, and the peer instead lets a bounded 1 ms
-            // pass, far longer than any load takes, before it goes on to the
-            // teardown barrier.
-            if (CG == 1 || leader) {
-                const long long n = issued < S ? issued : S;
-                for (long long j = 0; j < n; ++j) {
-                    const long long g = issued - 1 - j;
-                    ctl.drain(full0 + 8 * static_cast<int>(g % S), static_cast<uint32_t>((g / S) & 1),
-                              10000000ull);
-                }
-            } else if (issued > 0) {
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 1000000ull) {
-                }
+        // Every load that was issued lands before the CTA can exit (bounded),
+        // also where another warp gave up on a stage after the last load was
+        // issued.  The leader drains the full barriers of its last stages, on
+        // which both CTAs' loads of those stages complete.  The peer may have
+        // issued a stage the leader never armed (the leader stopped first):
+        // that load completes on a leader barrier whose phase can no longer
+        // finish, so nothing can be waited on for it; see the teardown.
+        if (CG == 1 || leader) {
+            const long long n = issued < S ? issued : S;
+            for (long long j = 0; j < n; ++j) {
+                const long long g = issued - 1 - j;
+                ctl.drain(full0 + 8 * static_cast<int>(g % S), static_cast<uint32_t>((g / S) & 1), 10000000ull);
             }
         }
         __syncwarp();
@@ -1106,7 +1089,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CG, BN))
     // ---- teardown ------------------------------------------------------------
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();
+    if constexpr (CG == 2) {
+        // stopped early: a load of this CTA's that the leader never armed gets a
+        // bounded 1 ms to land, far longer than any load takes
+        if (!leader && warp == 0 && ld_shared_u32(abort_flag)) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000ull) {
+            }
+            __syncwarp();
+        }
+        cluster_sync();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc<CG>(tmem_base, kAccCols);

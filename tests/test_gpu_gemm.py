@@ -829,6 +829,31 @@ def test_wait_time_out_is_reported_and_the_context_survives(shape, sched):
         pts.gemm_destroy(h)
 
 
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("sched", [pts.GEMM_SCHED_NONPERSISTENT, pts.GEMM_SCHED_STATIC, pts.GEMM_SCHED_CLC])
+@pytest.mark.parametrize("K,load", [(64, 0), (256, 0)])
+def test_wait_time_out_after_the_last_load_was_issued(shape, sched, K, load):
+    """The same where the whole contraction fits the ring: the producer has
+    issued all its loads, and ends without an error of its own, when the MMA
+    warp gives up; the CTA still lets them land before it exits."""
+    x = wl.custom(300, 520, K, wl.BF16, "uniform", 3)
+    h = pts.gemm_create(0, pts.make_opts(debug_flags=pts.GEMM_DEBUG_FAULT_SKIP_TMA, fault_arg=load,
+                                         timeout_ns=20_000_000, **SHAPES[shape]))
+    try:
+        run_device(h, x, sched)
+        st, dev = pts.gemm_check(h)
+        assert st == pts.gemm.GEMM_ERR_TIMEOUT and dev >> 24 == 1
+    finally:
+        pts.gemm_destroy(h)
+    h = pts.gemm_create(0, pts.make_opts(**SHAPES[shape]))
+    try:
+        C = run_device(h, x, sched)
+        assert pts.gemm_check(h)[0] == 0
+        assert compare_full(x, C) <= TOL[wl.BF16]
+    finally:
+        pts.gemm_destroy(h)
+
+
 @pytest.mark.parametrize("sched", [pts.GEMM_SCHED_STATIC, pts.GEMM_SCHED_CLC])
 def test_stream_k_state_is_cleared_after_a_device_error(sched):
     """A stream-K launch that stops on a wait time-out leaves some cut tiles
