@@ -11,13 +11,13 @@
 #include <cstdint>
 #include <initializer_list>
 
-#include "pts_gemm.h"
+#include "gemm_ctx.h"
 
 namespace {
 
 // torch.Tensor and its accessors, the dtypes, and what a refused tensor calls
 // (it raises); set once by setup().
-PyObject *g_tensor, *g_dtype, *g_is_cuda, *g_contiguous, *g_numel, *g_data_ptr, *g_refuse, *g_cuda_stream;
+PyObject *g_tensor, *g_dtype, *g_device, *g_contiguous, *g_numel, *g_data_ptr, *g_refuse, *g_cuda_stream;
 PyObject *g_elements[3], *g_i32, *g_f32, *g_u8;
 
 PyObject *get(PyObject *accessor, PyObject *x)
@@ -76,7 +76,14 @@ public:
         return static_cast<gemm_dtype_t>(ok_ ? d : 0);
     }
 
-    void *raw()   // a handle or an address
+    gemm_handle_t handle()
+    {
+        const auto h = static_cast<gemm_handle_t>(raw());
+        if (h) device_ = h->device;
+        return h;
+    }
+
+    void *raw()   // an address
     {
         if (!ok_) return nullptr;
         PyObject *x = *v_++;
@@ -86,7 +93,7 @@ public:
         return p;
     }
 
-    // a tensor's address; it must be contiguous, on a GPU, of `dtype` and hold `count` elements
+    // a tensor's address; it must be contiguous, on the handle's GPU, of `dtype` and hold `count` elements
     void *array(PyObject *dtype, int64_t count, const char *what)
     {
         if (!ok_) return nullptr;
@@ -94,11 +101,13 @@ public:
         if (x == Py_None || PyLong_CheckExact(x)) return raw();
         ++v_;
         if (!PyObject_TypeCheck(x, reinterpret_cast<PyTypeObject *>(g_tensor))) return refuse(what, x, dtype, count);
-        PyObject *type = get(g_dtype, x), *cuda = type ? get(g_is_cuda, x) : nullptr;
-        PyObject *contiguous = cuda ? call(g_contiguous, x) : nullptr, *numel = contiguous ? call(g_numel, x) : nullptr;
-        const bool fits = numel && type == dtype && cuda == Py_True && contiguous == Py_True && PyLong_AsLongLong(numel) >= count;
+        PyObject *type = get(g_dtype, x), *device = type ? call(g_device, x) : nullptr;
+        PyObject *contiguous = device ? call(g_contiguous, x) : nullptr, *numel = contiguous ? call(g_numel, x) : nullptr;
+        const int64_t at_device = numel ? PyLong_AsLongLong(device) : -1;   // (-1: on no GPU)
+        const bool fits = numel && type == dtype && at_device >= 0 && (device_ < 0 || at_device == device_) && contiguous == Py_True
+                          && PyLong_AsLongLong(numel) >= count;
         Py_XDECREF(type);
-        Py_XDECREF(cuda);
+        Py_XDECREF(device);
         Py_XDECREF(contiguous);
         Py_XDECREF(numel);
         if (PyErr_Occurred()) return fail();
@@ -131,7 +140,7 @@ private:
     }
     void *refuse(const char *what, PyObject *x, PyObject *dtype, int64_t count)
     {
-        PyObject *r = PyObject_CallFunction(g_refuse, "sOOL", what, x, dtype, static_cast<long long>(count));
+        PyObject *r = PyObject_CallFunction(g_refuse, "sOOLi", what, x, dtype, static_cast<long long>(count), device_);
         Py_XDECREF(r);   // (it raises)
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, what);
         return fail();
@@ -139,6 +148,7 @@ private:
 
     PyObject *const *v_;
     bool ok_;
+    int device_ = -1;   // the handle's
 };
 
 // Make the call without the interpreter's lock; its status as an int.
@@ -162,7 +172,7 @@ PyObject *run(const Args &a, F f)
         Args a(v, n, count_);
 
 PTS_CALL(expert_sort, 9)
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t tokens = a.integer(), top_k = a.integer(), experts = a.integer(), m = product({tokens, top_k});
     const auto ids = static_cast<const int32_t *>(a.array(g_i32, m, "expert_ids"));
     const auto offsets = static_cast<int32_t *>(a.array(g_i32, offsets_of(experts), "offsets"));
@@ -175,7 +185,7 @@ PTS_CALL(expert_sort, 9)
 PTS_CALL(expert_gather, 9)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_expert_gather", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t tokens = a.integer(), top_k = a.integer(), dim = a.integer(), m = product({tokens, top_k});
     const void *X = a.array(t, product({tokens, dim}), "X");
     const auto row_of = static_cast<const int32_t *>(a.array(g_i32, m, "row_of"));
@@ -187,7 +197,7 @@ PTS_CALL(expert_gather, 9)
 PTS_CALL(expert_combine, 10)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_expert_combine", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t tokens = a.integer(), top_k = a.integer(), dim = a.integer(), m = product({tokens, top_k});
     const void *Ys = a.array(t, product({m, dim}), "Ys");
     const auto row_of = static_cast<const int32_t *>(a.array(g_i32, m, "row_of"));
@@ -200,7 +210,7 @@ PTS_CALL(expert_combine, 10)
 PTS_CALL(expert_combine_grad, 12)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_expert_combine_grad", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t tokens = a.integer(), top_k = a.integer(), dim = a.integer(), m = product({tokens, top_k});
     const void *dY = a.array(t, product({tokens, dim}), "dY"), *Ys = a.array(t, product({m, dim}), "Ys");
     const auto row_of = static_cast<const int32_t *>(a.array(g_i32, m, "row_of"));
@@ -216,7 +226,7 @@ PTS_CALL(expert_combine_grad, 12)
 PTS_CALL(run_experts, 13)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_run_experts", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t rows = a.integer(), experts = a.integer(), N = a.integer(), K = a.integer();
     const void *A = a.array(t, product({rows, K}), "A"), *B = a.array(t, product({experts, N, K}), "B");
     const auto offsets = static_cast<const int32_t *>(a.array(g_i32, offsets_of(experts), "offsets"));
@@ -231,7 +241,7 @@ PTS_CALL(run_experts, 13)
 PTS_CALL(run_experts_dgrad, 11)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_run_experts_dgrad", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t rows = a.integer(), experts = a.integer(), N = a.integer(), K = a.integer();
     const void *dC = a.array(t, product({rows, N}), "dC"), *B = a.array(t, product({experts, N, K}), "B");
     const auto offsets = static_cast<const int32_t *>(a.array(g_i32, offsets_of(experts), "offsets"));
@@ -243,7 +253,7 @@ PTS_CALL(run_experts_dgrad, 11)
 PTS_CALL(run_experts_wgrad, 11)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_run_experts_wgrad", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t rows = a.integer(), experts = a.integer(), N = a.integer(), K = a.integer();
     const void *dC = a.array(t, product({rows, N}), "dC"), *A = a.array(t, product({rows, K}), "A");
     const auto offsets = static_cast<const int32_t *>(a.array(g_i32, offsets_of(experts), "offsets"));
@@ -255,7 +265,7 @@ PTS_CALL(run_experts_wgrad, 11)
 PTS_CALL(run_nibble, 14)
     PyObject *t;
     const gemm_dtype_t dtype = a.type("gemm_run_nibble", &t);
-    const auto h = static_cast<gemm_handle_t>(a.raw());
+    const auto h = a.handle();
     const int64_t rows = a.integer(), experts = a.integer(), N = a.integer(), K = a.integer(), group = a.integer();
     const int64_t groups = product({experts, N, group > 0 && K > 0 ? (K - 1) / group + 1 : 0});
     const void *A = a.array(t, product({rows, K}), "A"), *B = a.array(g_u8, product({experts, N, K}) / 2, "B");
@@ -284,13 +294,13 @@ PyObject *setup(PyObject *, PyObject *const *v, Py_ssize_t n)
     g_f32 = v[6];
     g_u8 = v[7];
     g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    const struct { PyObject **to; const char *name; } members[] = {{&g_dtype, "dtype"}, {&g_is_cuda, "is_cuda"},
+    const struct { PyObject **to; const char *name; } members[] = {{&g_dtype, "dtype"}, {&g_device, "get_device"},
         {&g_contiguous, "is_contiguous"}, {&g_numel, "numel"}, {&g_data_ptr, "data_ptr"}};
     for (const auto &m : members) {
         *m.to = PyObject_GetAttrString(g_tensor, m.name);
         if (!*m.to) return nullptr;
     }
-    if (!PyType_Check(g_tensor) || !Py_TYPE(g_dtype)->tp_descr_get || !Py_TYPE(g_is_cuda)->tp_descr_get || !g_cuda_stream) {
+    if (!PyType_Check(g_tensor) || !Py_TYPE(g_dtype)->tp_descr_get || !g_cuda_stream) {
         PyErr_SetString(PyExc_TypeError, "setup: not a tensor type");
         return nullptr;
     }

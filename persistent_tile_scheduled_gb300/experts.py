@@ -1,9 +1,9 @@
 """Python binding of the expert layer's operators in include/pts_gemm.h.
 
 Names and order of arguments are the C functions'.  A tensor passed where the
-C call takes a pointer is checked first (on a GPU, contiguous, of the expected
-type, large enough for the sizes given); a raw device address is passed on as
-it is.  ``stream`` is a torch stream or a raw handle; None is the legacy
+C call takes a pointer is checked first (on the handle's GPU, contiguous, of
+the expected type, large enough for the sizes given); a raw device address is
+passed on as it is.  ``stream`` is a torch stream or a raw handle; None is the legacy
 default stream, so a caller on another torch stream passes that stream.
 """
 from __future__ import annotations
@@ -17,15 +17,21 @@ from . import _build
 from .gemm import GEMM_ERR_INVALID_ARG, GemmError, load
 
 
-def _refuse(what, x, dtype, count):
+def _refuse(what, x, dtype, count, device=-1):
     """Raises for an argument that the extension module does not take: not a dtype (x is None), or not such a tensor."""
     if x is None:
         raise GemmError(GEMM_ERR_INVALID_ARG, f"{what}: unknown dtype {count}")
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{what}: needs a tensor, an address or None, got {type(x).__name__}")
+    where = f" on cuda:{device}" if device >= 0 else ""
     raise GemmError(GEMM_ERR_INVALID_ARG,
-                    f"{what}: needs a contiguous CUDA tensor of {dtype} with at least {count} elements, got "
+                    f"{what}: needs a contiguous CUDA tensor{where} of {dtype} with at least {count} elements, got "
                     f"{tuple(x.shape)} {x.dtype} on {x.device}{'' if x.is_contiguous() else ', not contiguous'}")
+
+
+def _setup(module):
+    module.setup(torch.Tensor, _refuse, torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.float32,
+                 torch.uint8)
 
 
 class _Calls:
@@ -36,8 +42,8 @@ class _Calls:
         loader = importlib.machinery.ExtensionFileLoader("pts_experts", _build.EXPERTS)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pts_experts", loader))
         loader.exec_module(module)
-        module.setup(torch.Tensor, _refuse, torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int32,
-                     torch.float32, torch.uint8)
+        _setup(module)
+        self.module = module
         for f in ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "run_experts",
                   "run_experts_dgrad", "run_experts_wgrad", "run_nibble"):
             setattr(self, f, getattr(module, f))

@@ -77,3 +77,39 @@ def test_sizes_whose_product_passes_64_bits_want_more_than_any_tensor_has():
     with pytest.raises(pts.GemmError) as err:
         pts.gemm_run_experts(None, 4, 1 << 40, 1 << 40, 64, 1 << 20, x, 1 << 20, 1 << 20, g.GEMM_F16)
     assert "contiguous CUDA tensor" in str(err.value) and str((1 << 63) - 1) in str(err.value)
+
+
+class _Elsewhere:
+    """A tensor as the extension module sees one, on a GPU of choice."""
+    def __init__(self, device, dtype):
+        self.where, self.kind = device, dtype
+
+    dtype = property(lambda self: self.kind)
+    is_cuda = property(lambda self: self.where >= 0)
+    get_device = lambda self: self.where  # noqa: E731
+    is_contiguous = lambda self: True  # noqa: E731
+    numel = lambda self: 1 << 20  # noqa: E731
+    data_ptr = lambda self: 1 << 20  # noqa: E731
+
+
+def test_a_tensor_of_another_gpu_than_the_handles_is_refused():
+    from persistent_tile_scheduled_gb300 import experts
+    experts._c.expert_sort   # (loads the module)
+    module, handle = experts._c.module, (ctypes.c_int32 * 64)(1)   # a handle begins with its device
+    h = ctypes.addressof(handle)
+
+    def refuse(what, x, dtype, count, device=None):
+        raise KeyError((what, x.where, device))
+
+    types = (torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.float32, torch.uint8)
+    module.setup(_Elsewhere, refuse, *types)
+    try:
+        for where in ([0, 1, 1, 1], [1, 1, 1, 0], [1, 2, 1, 1], [1, 1, -1, 1]):
+            at, wrong = next((i, w) for i, w in enumerate(where) if w != 1)
+            with pytest.raises(KeyError) as err:
+                module.expert_sort(h, 4, 2, 2000, *[_Elsewhere(w, torch.int32) for w in where], None)
+            assert err.value.args[0] == (("expert_ids", "offsets", "row_of", "src_of")[at], wrong, 1)
+        # all on the handle's: the C call is made, and refuses 2000 experts
+        assert module.expert_sort(h, 4, 2, 2000, *[_Elsewhere(1, torch.int32)] * 4, None) == g.GEMM_ERR_INVALID_ARG
+    finally:
+        experts._setup(module)
