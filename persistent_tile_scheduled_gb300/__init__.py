@@ -12,4 +12,4 @@ from .gemm import (GEMM_BF16, GEMM_DEBUG_CLC_STOP_AT, GEMM_DEBUG_FAULT_SKIP_TMA,
                    make_opts)
 from .experts import (gemm_expert_combine, gemm_expert_combine_grad, gemm_expert_gather, gemm_expert_sort,  # noqa: F401
                       gemm_run_experts, gemm_run_experts_dgrad, gemm_run_experts_wgrad, gemm_run_nibble)
-from ._build import build  # noqa: F401
+from ._build import build, build_experts  # noqa: F401

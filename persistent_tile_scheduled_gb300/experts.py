@@ -34,18 +34,23 @@ def _setup(module):
                  torch.uint8)
 
 
+_FUNCTIONS = ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "run_experts", "run_experts_dgrad",
+              "run_experts_wgrad", "run_nibble")
+
+
 class _Calls:
     """The functions of the extension module, which is loaded (and built, if it has to be) at the first call."""
 
     def __getattr__(self, name):
+        if name != "module" and name not in _FUNCTIONS:
+            raise AttributeError(name)
         load()
-        loader = importlib.machinery.ExtensionFileLoader("pts_experts", _build.EXPERTS)
+        loader = importlib.machinery.ExtensionFileLoader("pts_experts", _build.build_experts())
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pts_experts", loader))
         loader.exec_module(module)
         _setup(module)
         self.module = module
-        for f in ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "run_experts",
-                  "run_experts_dgrad", "run_experts_wgrad", "run_nibble"):
+        for f in _FUNCTIONS:
             setattr(self, f, getattr(module, f))
         return self.__dict__[name]
 

@@ -94,7 +94,6 @@ class _Elsewhere:
 
 def test_a_tensor_of_another_gpu_than_the_handles_is_refused():
     from persistent_tile_scheduled_gb300 import experts
-    experts._c.expert_sort   # (loads the module)
     module, handle = experts._c.module, (ctypes.c_int32 * 64)(1)   # a handle begins with its device
     h = ctypes.addressof(handle)
 
