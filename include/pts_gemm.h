@@ -77,6 +77,10 @@ typedef enum {
  * gemm_run_experts, its gradients and gemm_run_nibble issue that load but
  * announce more bytes than it brings (with blocks of 8 rows gemm_run_nibble
  * does so for every load), to the same effect. */
+#define GEMM_DEBUG_NIBBLE_FORM(rows, ctas) ((unsigned)(rows) << 8 | (unsigned)(ctas) << 16)
+/* gemm_run_nibble expands its weights for blocks of `rows` (8, 32 or 64) rows,
+ * with `ctas` (1; for 32 and 64 also 2 or 4) CTAs to a tile's contraction,
+ * instead of what is reckoned to be fastest for the sizes. */
 
 typedef struct gemm_opts {
     int cta_group;                  /* 1 (128x256 tile per CTA) or 2 (256x256 per CTA pair);

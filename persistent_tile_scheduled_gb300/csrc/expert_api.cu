@@ -161,6 +161,8 @@ struct NibbleForm {
 // The rows of each expert are device data: an expert's last block is taken as 0.45 full.
 NibbleForm nibble_form(const gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, bool spread)
 {
+    if (h->opts.debug_flags & GEMM_DEBUG_NIBBLE_FORM(0xff, 0))
+        return NibbleForm{static_cast<int>(h->opts.debug_flags >> 8 & 0xff), static_cast<int>(h->opts.debug_flags >> 16 & 0xf)};
     auto blocks = [&](int of) -> double {
         if (!spread) return static_cast<double>((rows + of - 1) / of);
         const double n = static_cast<double>(rows) / of + 0.45 * static_cast<double>(experts), used = static_cast<double>(rows < experts ? rows : experts);

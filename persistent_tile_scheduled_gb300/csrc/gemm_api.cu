@@ -547,7 +547,11 @@ gemm_status_t gemm_create(gemm_handle_t *out, int device, const gemm_opts_t *opt
     if (o.clc_depth < 0 || o.clc_depth > 2) return GEMM_ERR_INVALID_ARG;
     if (o.clc_depth == 0) o.clc_depth = pts::kDefaultClcLead;
     if (o.tile_n == pts::kTileNNarrow && (o.split == 4 || o.split_k == 1)) return GEMM_ERR_INVALID_ARG;
-    if (o.debug_flags & ~(GEMM_DEBUG_RECORDS | GEMM_DEBUG_CLC_STOP_AT | GEMM_DEBUG_FAULT_SKIP_TMA))
+    if (o.debug_flags & ~(GEMM_DEBUG_RECORDS | GEMM_DEBUG_CLC_STOP_AT | GEMM_DEBUG_FAULT_SKIP_TMA | GEMM_DEBUG_NIBBLE_FORM(0xff, 0xf)))
+        return GEMM_ERR_INVALID_ARG;
+    const unsigned form_rows = o.debug_flags >> 8 & 0xff, form_ctas = o.debug_flags >> 16 & 0xf;
+    const bool wide = form_rows == 32 || form_rows == 64;
+    if (form_rows == 0 ? form_ctas != 0 : !((form_rows == 8 && form_ctas == 1) || (wide && (form_ctas == 1 || form_ctas == 2 || form_ctas == 4))))
         return GEMM_ERR_INVALID_ARG;
 
     int ndev = 0;

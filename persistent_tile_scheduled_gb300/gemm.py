@@ -21,6 +21,11 @@ GEMM_DEBUG_RECORDS = 0x1
 GEMM_DEBUG_CLC_STOP_AT = 0x2
 GEMM_DEBUG_FAULT_SKIP_TMA = 0x4
 
+
+def GEMM_DEBUG_NIBBLE_FORM(rows: int, ctas: int) -> int:
+    return rows << 8 | ctas << 16
+
+
 EXPORTED = ("gemm_create", "gemm_run", "gemm_run_host", "gemm_query", "gemm_check",
             "gemm_read_debug", "gemm_destroy", "gemm_status_string", "gemm_run_noalloc",
             "gemm_run_host_batch", "gemm_run_grouped", "gemm_query_grouped", "gemm_tensor_peak_probe",

@@ -125,3 +125,26 @@ def test_nibble(counts, N, K, load):
         return C, torch.cat(per_expert(counts, lambda e, r: A[r].double() @ w[e].T))
 
     run_out_then_exact({}, load, call)
+
+
+@pytest.mark.parametrize("rows,ctas", [(8, 1), (32, 1), (32, 2), (32, 4), (64, 1), (64, 2), (64, 4)])
+@pytest.mark.parametrize("counts,N,K,load", [([70], 264, 1024, 0), ([40, 0, 33], 136, 4096, 3), ([300], 1032, 8192, 7)])
+def test_every_form_of_nibble(rows, ctas, counts, N, K, load):
+    """The withheld load: the first, the last but some, one in the middle; every CTA has K / 256 / ctas of them at least."""
+    E, off, R = len(counts), offsets_of(counts), sum(counts)
+    A, form = ints((R, K), 8), pts.GEMM_DEBUG_NIBBLE_FORM(rows, ctas)
+    B, s = torch.full((E, N, K // 2), 0x99, dtype=torch.uint8, device="cuda"), torch.ones(E, N, K // 64).half().cuda()
+    want = A.double().sum(1)[:, None].expand(R, N)
+
+    def call(flags):
+        h = pts.gemm_create(0, pts.make_opts(debug_flags=form | flags, fault_arg=load, timeout_ns=TIMEOUT_NS))
+        C = torch.zeros(R, N, dtype=torch.float16, device="cuda")
+        pts.gemm_run_nibble(h, R, E, N, K, 64, A, B, s, None, None if E == 1 else off, C, F16)
+        st, dev = pts.gemm_check(h)
+        pts.gemm_destroy(h)
+        return C, st, dev
+
+    C, st, dev = call(pts.GEMM_DEBUG_FAULT_SKIP_TMA)
+    assert st == pts.gemm.GEMM_ERR_TIMEOUT and dev >> 24 == 1
+    C, st, dev = call(0)
+    assert st == 0 and torch.equal(C.double(), want)
