@@ -153,11 +153,12 @@ struct NibbleForm {
 // groups' size and the zeros change it little).  By 8: 3.4 and 1 per 8.2 million
 // weights of each row block.  By 32 or 64: 5.2 and, of a CTA, 0.95 or 1.5 per 256
 // of the contraction of a tile of 128 features.  Measured / so reckoned:
-//   rows of 8192^2         8: 13.8 / 11.6    16: 20.4 / 19.8, by 32 20.5 / 20.4
-//                          24: 31.4 / 28, by 32 20.6 / 20.4    64: 69 / 69, by 64 30.5 / 29
-//   16 rows of 1000 x 2048 4.1 / 3.9, by 32 7.6 / 7.1
-//   32 experts, 2048 x 4096, 10 rows each in the mean 57 / 59, by 32 63 / 66; 16 experts,
-//   24 rows each 59 / 58, by 32 34 / 36
+//   rows of 8192^2         8: 13.4 / 11.6    16: 20.3 / 19.8, by 32 19.3 / 20.4
+//                          24: 30.6 / 28, by 32 19.4 / 20.4    64: 69 / 69, by 64 29.2 / 29
+//   64 rows of 20480 x 16384 by 64 with 1, 2, 4 CTAs to a tile 184 / 197, 155 / 160, 147 / 146
+//   16 rows of 1000 x 2048 4.3 / 3.9, by 32 7.4 / 7.1
+//   32 experts, 2048 x 4096, 10 rows each 66 / 59, by 32 63 / 66; 16 experts, 24 rows each
+//   50 / 60, by 32 32.6 / 51
 // The rows of each expert are device data: an expert's last block is taken as 0.45 full.
 NibbleForm nibble_form(const gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, bool spread)
 {

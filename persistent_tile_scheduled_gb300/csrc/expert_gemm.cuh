@@ -31,7 +31,7 @@
 //
 // What bounds it (GB300, bf16).  Many rows: the tensor pipe, 85 % busy over 16384
 // rows spread unevenly over 8 experts of 8192 x 4096 (580 us alone; back to back
-// under the power cap 656 to 670 us, one dense gemm_run of that size 647).  An expert whose rows do not fill its tiles costs the weights' loads of a
+// under the power cap 660 to 690 us, one dense gemm_run of that size 647).  An expert whose rows do not fill its tiles costs the weights' loads of a
 // full one: a pair's stage is 64 KB per SM for 1024 cycles of MMA, the most an SM
 // takes in, so a tile of 200 rows runs hardly faster than one of 256 (8192 rows
 // over 16 experts: 232 us uneven, 213 even).  Few rows: the weights' bytes, 6.2

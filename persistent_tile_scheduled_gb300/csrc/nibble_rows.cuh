@@ -14,14 +14,16 @@
 // of 128 features and the rows), MMA, warps that scale and sum (4 per 32 rows),
 // warps that expand.  They hand on units of 256 or 128 of the contraction, two
 // of each in flight: the expanded weights and the sums of their groups.
-// A tile is 128 features x one row block.  Where there are more than SMs, a CTA
-// takes one after another, the loads and the expanding running ahead into the
-// next; where there are fewer, a cluster of 2 or 4 CTAs shares a tile's
-// contraction and adds up through distributed shared memory, every CTA its part
-// of the rows, in order.
+// A tile is 128 features x one row block.  Either a CTA takes one tile after
+// another, the loads and the expanding running ahead into the next; or a cluster
+// of 2 or 4 CTAs shares a tile's contraction and adds up through distributed
+// shared memory, every CTA its part of the rows, in order.  The latter is for
+// fewer tiles than SMs, but also for a few more, whose last round would leave most
+// SMs idle (64 rows of 20480 x 16384, 160 tiles: 4 CTAs to each, in several
+// rounds, 147 us, 2 CTAs 155, one 184): the caller reckons which.
 //
-// What bounds it (bf16, groups of 64): 32 rows of 8192^2 take 20.2 us, 8 at a time
-// 37; 64 rows 29.9 and 69; 512 rows of 4096^2 49.5 and 121.  A CTA spends 0.95 us on
+// What bounds it (bf16, groups of 64): 32 rows of 8192^2 take 19.4 us, 8 at a time
+// 37; 64 rows 29.3 and 69; 512 rows of 4096^2 49.7 and 121.  A CTA spends 0.95 us on
 // 256 of its contraction (1.5 for 64 rows), mostly in the expanding warps: loads,
 // barriers and scales alone 0.45, the MMAs 0.3, the expanding 0.5; start and end
 // take 5 us, so that few weights are better off in nibble.cuh.  One elected lane
@@ -80,7 +82,7 @@ __device__ __forceinline__ void expand_in_order(uint32_t w, uint32_t zero, uint3
 // their zeros, four to a register, left as they are where `given` is 0.  VEC: all
 // there and aligned, one load; else one by one, the last one again behind the end.
 // A lane has a feature, so every load touches 32 lines: one load per group took a
-// third of the time (31 us where this takes 20.6).  There is no branch around a
+// third of the time (31 us where the rest took 20.6).  There is no branch around a
 // load, since it would be waited for at the branch's end.
 template <int N, bool VEC>
 __device__ __forceinline__ void load_group_scales(const uint16_t *p, int first, int groups, uint32_t (&v)[(N + 1) / 2])
