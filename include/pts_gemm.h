@@ -44,7 +44,8 @@
 extern "C" {
 #endif
 
-typedef enum { GEMM_F16 = 0, GEMM_BF16 = 1, GEMM_E4M3 = 2 } gemm_dtype_t;
+/* GEMM_F32: the logits of gemm_expert_route and its gradient, nothing else. */
+typedef enum { GEMM_F16 = 0, GEMM_BF16 = 1, GEMM_E4M3 = 2, GEMM_F32 = 3 } gemm_dtype_t;
 
 typedef enum {
     GEMM_SCHED_NONPERSISTENT = 0,
@@ -420,6 +421,96 @@ gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t expe
 gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,
                               const void *A, const void *B, const void *scales, const uint8_t *zeros,
                               const int32_t *offsets, void *C, gemm_dtype_t dtype, void *stream);
+
+/* ---- what stands around the products --------------------------------------
+ * The rest of a feed-forward layer, dense or of experts: a router's choice, the
+ * products with bias, activation and residual, and the gradients of both; and a
+ * whole layer of experts for a few tokens.  The rules of "a layer of experts"
+ * hold here too (arrays, alignment, device data that leads nowhere).  Of the
+ * handle's options gemm_run_linear uses those that gemm_run_experts does, the
+ * other calls overlap_launch. */
+
+/* Activations, of the fp32 sum z:
+ *   RELU max(z, 0); RELU2 max(z, 0)^2; GELU z Phi(z) (the normal distribution's
+ *   integral); GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2;
+ *   SILU z / (1 + exp(-z)).
+ * With GEMM_ACT_GATED the matrix holds 2N features, a gate's N and then N that
+ * it multiplies: act(z[n]) * z[N + n]. */
+typedef enum {
+    GEMM_ACT_NONE = 0, GEMM_ACT_RELU = 1, GEMM_ACT_RELU2 = 2, GEMM_ACT_GELU = 3, GEMM_ACT_GELU_TANH = 4, GEMM_ACT_SILU = 5,
+    GEMM_ACT_GATED = 0x10   /* added to one of the others */
+} gemm_act_t;
+
+/* Z[r] = A[r] . B_e + bias_e and C[r] = act(Z[r]) + residual[r] for every row r
+ * of every expert e, one launch.  As gemm_run_experts, and
+ *   offsets   as there, or NULL with experts == 1: every row uses that matrix;
+ *   B         experts x N' x K with N' = N, gated 2N;
+ *   bias      experts x N', of C's type, or NULL;
+ *   residual  rows x N, of C's type, or NULL; it may be C itself;
+ *   Z         rows x N', of C's type, or NULL: what gemm_linear_grad needs;
+ *   act       a gemm_act_t.
+ * Bias, activation and residual are computed on the fp32 sums, each output is
+ * rounded once.  K == 0: Z is the bias. */
+gemm_status_t gemm_run_linear(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *A,
+                              const void *B, const void *bias, const void *residual, const int32_t *offsets, void *C,
+                              void *Z, int act, gemm_dtype_t dtype, float scale_a, float scale_b, void *stream);
+
+/* The backward pass through its epilogue: dZ[r] = dC[r] * act'(Z[r]), gated
+ * dZ[r, n] = dC[r, n] Z[r, N + n] act'(Z[r, n]) and dZ[r, N + n] = dC[r, n]
+ * act(Z[r, n]); dbias_e = the sum of dZ over expert e's rows (fp32, before dZ is
+ * rounded, in a fixed order; zeros for an expert without rows), experts x N', or
+ * NULL for none.  dC: rows x N, Z and dZ: rows x N', fp16 or bf16.  dZ is then
+ * the dC of gemm_run_experts_dgrad and _wgrad over N' (with offsets {0, rows}
+ * where there is one matrix); the residual's gradient is dC. */
+gemm_status_t gemm_linear_grad(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, const void *dC, const void *Z,
+                               const int32_t *offsets, void *dZ, float *dbias, int act, gemm_dtype_t dtype, void *stream);
+
+/* How the weights follow from the logits l of the chosen experts:
+ *   SELECTED  softmax over the chosen;
+ *   ALL       softmax over all experts, its values for the chosen;
+ *   SIGMOID   1 / (1 + exp(-l)), divided by their sum over the chosen. */
+typedef enum { GEMM_ROUTE_SELECTED = 0, GEMM_ROUTE_ALL = 1, GEMM_ROUTE_SIGMOID = 2 } gemm_route_t;
+
+/* A token's experts: the top_k largest of its logits, largest first, equal ones
+ * by the lower index, and their weights (fp32): expert_ids and weights are what
+ * gemm_expert_sort, gemm_expert_combine and gemm_expert_layer take.  A logit of
+ * -infinity, or NaN, is never chosen; where fewer than top_k are left, the
+ * others' ids are -1 and their weights 0 (a padded token: all of them).
+ * +infinity counts as the largest finite value.
+ * logits: tokens x experts, fp32, fp16 or bf16, aligned to its type.  experts in
+ * [1, GEMM_EXPERT_SORT_MAX_EXPERTS], top_k in [1, min(experts,
+ * GEMM_EXPERT_ROUTE_MAX_TOP_K)]; tokens * experts < 2^40. */
+#define GEMM_EXPERT_ROUTE_MAX_TOP_K 32
+gemm_status_t gemm_expert_route(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t experts, const void *logits,
+                                int32_t *expert_ids, float *weights, gemm_route_t mode, gemm_dtype_t dtype, void *stream);
+
+/* Its gradient: dlogits (of the logits' type, all of it written, zeros where
+ * nothing depends on a logit) from dweights, for the expert_ids that it chose.
+ * The choice itself has no gradient.  An id outside [0, experts) has none
+ * either. */
+gemm_status_t gemm_expert_route_grad(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t experts, const void *logits,
+                                     const int32_t *expert_ids, const float *dweights, void *dlogits, gemm_route_t mode,
+                                     gemm_dtype_t dtype, void *stream);
+
+/* A whole layer of experts for a few tokens, in two launches, without sorting:
+ *   Y[t] = residual[t] + sum_j weights[t, j] * (W2_e act(W1_e X[t] + b1_e) + b2_e),
+ * e = expert_ids[t, j]; an id outside [0, experts) contributes nothing.
+ *   X, Y, residual: tokens x dim (residual may be NULL, or Y itself);
+ *   up    experts x hidden' x dim (W1), up_bias experts x hidden' or NULL, with
+ *         hidden' = hidden, gated 2 hidden;
+ *   down  experts x dim x hidden (W2), down_bias experts x dim or NULL;
+ *   Hs    tokens * top_k x hidden: the hidden rows (rounded to the type) pass
+ *         through it, a row per assignment; a token that names an expert twice
+ *         has it computed once.
+ * fp16 or bf16; sums fp32.  dim % 8 == 0, hidden % 8 == 0; tokens at most
+ * GEMM_EXPERT_LAYER_MAX_TOKENS, tokens * top_k GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS,
+ * experts GEMM_EXPERT_SORT_MAX_EXPERTS. */
+#define GEMM_EXPERT_LAYER_MAX_TOKENS 64
+#define GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS 512
+gemm_status_t gemm_expert_layer(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t experts, int64_t dim,
+                                int64_t hidden, const void *X, const int32_t *expert_ids, const float *weights,
+                                const void *up, const void *up_bias, const void *down, const void *down_bias,
+                                const void *residual, void *Hs, void *Y, int act, gemm_dtype_t dtype, void *stream);
 
 /* ---- tensor-pipe peak probe (a measurement aid, not a GEMM) -------------
  * Every SM (cta_group 1) or SM pair (cta_group 2) issues `mmas` back-to-back

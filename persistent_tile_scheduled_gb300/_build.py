@@ -2,8 +2,9 @@
 
 The translation units (the wide-tile 1-SM kernels, the 2-SM kernels, the
 narrow-tile 1-SM and 2-SM kernels, the C ABI, the allocation-free entry point,
-the tensor-pipe peak probe, and the expert layer's products, row kernels,
-4-bit products and C ABI) are compiled in parallel, then linked with the static
+the tensor-pipe peak probe, the expert layer's products, row kernels, 4-bit
+products and C ABI, and what stands around the products: the product with an
+epilogue and its gradient, routing, the layer for a few tokens) are compiled in parallel, then linked with the static
 CUDA runtime.  Nothing is rebuilt when the library is newer than every source
 file.
 
@@ -30,7 +31,8 @@ EXPERTS = os.path.join(LIBDIR, "pts_experts" + sysconfig.get_config_var("EXT_SUF
 BINDING = os.path.join(CSRC, "expert_binding.cpp")
 UNITS = ["gemm_cg1.cu", "gemm_cg2.cu", "gemm_narrow.cu", "gemm_narrow_cg2.cu", "gemm_api.cu", "gemm_noalloc.cu",
          "peak_probe.cu", "expert_fwd.cu", "expert_dgrad.cu", "expert_wgrad.cu", "expert_route.cu", "nibble_f16.cu",
-         "nibble_bf16.cu", "nibble_rows_f16.cu", "nibble_rows_bf16.cu", "expert_api.cu"]
+         "nibble_bf16.cu", "nibble_rows_f16.cu", "nibble_rows_bf16.cu", "expert_api.cu", "linear_f16.cu", "linear_bf16.cu",
+         "linear_e4m3.cu", "linear_grad.cu", "route.cu", "expert_layer_f16.cu", "expert_layer_bf16.cu", "layer_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "expert_check.h"
 #include "expert_launch.h"
 #include "gemm_ctx.h"
 #include "gemm_plan.h"
@@ -12,45 +13,33 @@ using namespace pts;
 
 namespace {
 
-constexpr int64_t kLim = (int64_t(1) << 31) - 1;
-// Sizes of the products: the kernels count in 32 bits, and go up to a tile or a stage past the end.
-constexpr int64_t kMaxSize = GEMM_EXPERT_MAX_SIZE;
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool is16(gemm_dtype_t d) { return d == GEMM_F16 || d == GEMM_BF16; }
-
-gemm_status_t launched(cudaError_t e)
-{
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return e == cudaSuccess ? GEMM_OK : cuda_fail(e);
-}
-
-gemm_status_t on_device(const gemm_ctx *h)
-{
-    return cudaSetDevice(h->device) == cudaSuccess ? GEMM_OK : cuda_fail(cudaErrorInvalidDevice);
-}
-
 // The stage load that announces too many bytes (GEMM_DEBUG_FAULT_SKIP_TMA), or -1.
 int32_t fault_load(const gemm_ctx *h) { return h->opts.debug_flags & GEMM_DEBUG_FAULT_SKIP_TMA ? h->opts.fault_arg : -1; }
-
-bool overlap(const gemm_ctx *h) { return h->opts.overlap_launch >= 0; }
 
 // Common checks of the row kernels: tokens x top_k assignments, rows of dim elements.
 gemm_status_t check_rows(gemm_ctx *h, int64_t tokens, int64_t top_k, int64_t dim, int es)
 {
-    if (h == nullptr || tokens < 0 || top_k < 1 || dim < 0 || dim > kLim) return GEMM_ERR_INVALID_ARG;
-    if (top_k > kLim || tokens > kLim || tokens * top_k > kLim) return GEMM_ERR_INVALID_ARG;
+    if (h == nullptr || tokens < 0 || top_k < 1 || dim < 0 || dim > kIntMax) return GEMM_ERR_INVALID_ARG;
+    if (top_k > kIntMax || tokens > kIntMax || tokens * top_k > kIntMax) return GEMM_ERR_INVALID_ARG;
     if ((dim * es) % 16 != 0) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
 }
+
+// What a product's epilogue adds (gemm_run_linear).
+struct Epilogue {
+    const void *bias, *residual;
+    void *z;
+    int act;
+};
 
 // One product of the experts.  features / contraction / out_rows as in
 // ExpertParams; W and X as in expert_gemm.cuh.
 gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *W,
                           const void *X, const int32_t *offsets, void *out, gemm_dtype_t dtype, float out_scale,
-                          cudaStream_t stream)
+                          cudaStream_t stream, const Epilogue *epi = nullptr)
 {
+    const bool gated = epi && (epi->act & GEMM_ACT_GATED);
+    const int tile_f = gated ? kRowsPerCta / 2 : kRowsPerCta;   // output features of a CTA's tile
     const int64_t features = mode == EXPERT_FWD ? N : K;
     const int64_t contraction = mode == EXPERT_FWD ? K : N;   // (WGRAD: an expert's rows)
     const int kelems = dtype == GEMM_E4M3 ? 128 : 64;
@@ -74,10 +63,12 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     while (stages > 2 && expert_smem_bytes(cg, bn, stages) > h->max_smem_optin) --stages;
     const int smem = expert_smem_bytes(cg, bn, stages);
     const int kind = static_cast<int>(dtype);
-    const ExpertOps ops = mode == EXPERT_FWD ? expert_ops_fwd(kind, cg, bn)
+    const ExpertOps ops = epi                  ? (kind == 0 ? linear_ops_f16 : kind == 1 ? linear_ops_bf16 : linear_ops_e4m3)(gated, cg, bn)
+                          : mode == EXPERT_FWD ? expert_ops_fwd(kind, cg, bn)
                           : mode == EXPERT_DGRAD ? expert_ops_dgrad(kind, cg)
                                                  : expert_ops_wgrad(kind, cg);
-    int &resident = h->expert_clusters[kind][mode][bn == kExpertTileNFew ? 2 : cg - 1];
+    const int variant = bn == kExpertTileNFew ? 2 : cg - 1;
+    int &resident = epi ? h->linear_clusters[kind][gated][variant] : h->expert_clusters[kind][mode][variant];
     if (resident == 0) {
         int n = 0;
         if (ops.prepare(smem, h->sm_count, &n) != cudaSuccess) return cuda_fail(cudaErrorInvalidValue);
@@ -85,7 +76,7 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
         resident = n;
     }
     // tiles: at most one short one per expert on top of the rows' own
-    const int64_t tf = (features + kRowsPerCta * cg - 1) / (kRowsPerCta * cg);
+    const int64_t tf = (features + tile_f * cg - 1) / (tile_f * cg);
     const int64_t used = rows < experts ? rows : experts;
     const int64_t tiles = mode == EXPERT_WGRAD ? experts * tf * ((N + bn - 1) / bn) : (rows / bn + used) * tf;
     if (tiles > (int64_t(1) << 30)) return GEMM_ERR_INVALID_ARG;
@@ -104,24 +95,29 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
         if (split == 2 && length_kb < 32) split = 1;
     }
 
-    CUtensorMap mw, mx, mxs, mo;
-    std::memset(&mw, 0, sizeof(mw));
-    mx = mxs = mo = mw;
+    LinearMaps m;
+    std::memset(&m, 0, sizeof(m));
     bool ok = true;
     const uint32_t stage_rows = static_cast<uint32_t>(64 * kb_per_stage(cg));   // contraction rows of a stage
     if (mode == EXPERT_WGRAD) {
-        ok = encode_map3(h, &mw, W, 1, rows, K, dtype, stage_rows, 64) && encode_map3(h, &mx, X, 1, rows, N, dtype, stage_rows, 64);
-        mxs = mx;
-        ok = ok && encode_map3(h, &mo, out, experts, N, K, dtype, 64, 32);
+        ok = encode_map3(h, &m.w, W, 1, rows, K, dtype, stage_rows, 64) && encode_map3(h, &m.x, X, 1, rows, N, dtype, stage_rows, 64);
+        m.xs = m.x;
+        ok = ok && encode_map3(h, &m.o, out, experts, N, K, dtype, 64, 32);
     } else {
         if (contraction > 0) {
-            ok = mode == EXPERT_FWD ? encode_map3(h, &mw, W, experts, N, K, dtype, kRowsPerCta, kelems)
-                                    : encode_map3(h, &mw, W, experts, N, K, dtype, stage_rows, 64);
-            ok = ok && encode_map3(h, &mx, X, 1, rows, contraction, dtype, static_cast<uint32_t>(bn / cg), kelems)
-                 && encode_map3(h, &mxs, X, 1, rows, contraction, dtype, 16, kelems);
+            ok = gated                ? encode_map_gated(h, &m.w, W, experts, N, K, dtype, kelems)
+                 : mode == EXPERT_FWD ? encode_map3(h, &m.w, W, experts, N, K, dtype, kRowsPerCta, kelems)
+                                      : encode_map3(h, &m.w, W, experts, N, K, dtype, stage_rows, 64);
+            ok = ok && encode_map3(h, &m.x, X, 1, rows, contraction, dtype, static_cast<uint32_t>(bn / cg), kelems)
+                 && encode_map3(h, &m.xs, X, 1, rows, contraction, dtype, 16, kelems);
         }
-        ok = ok
-             && encode_map3(h, &mo, out, 1, rows, features, dtype == GEMM_E4M3 ? GEMM_BF16 : dtype, 64, 32);
+        const gemm_dtype_t to = dtype == GEMM_E4M3 ? GEMM_BF16 : dtype;
+        const uint32_t box_rows = epi ? kLinearChunk : 64, box_cols = gated ? 16 : 32;
+        ok = ok && encode_map3(h, &m.o, out, 1, rows, features, to, box_rows, box_cols);
+        if (epi && epi->residual) ok = ok && encode_map3(h, &m.r, epi->residual, 1, rows, features, to, box_rows, box_cols);
+        if (epi && epi->z)
+            ok = ok && (gated ? encode_map_halves(h, &m.z, epi->z, rows, features, to, box_rows)
+                              : encode_map3(h, &m.z, epi->z, 1, rows, features, to, box_rows, box_cols));
     }
     if (!ok) return GEMM_ERR_INVALID_ARG;
 
@@ -140,7 +136,13 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     p.fault_load = fault_load(h);
     p.timeout_ns = h->opts.timeout_ns;
     p.status = h->d_status;
-    return launched(ops.launch(mw, mx, mxs, mo, p, static_cast<int>(clusters) * cg * split, smem, stream, overlap(h)));
+    if (epi) {
+        p.act = epi->act;
+        p.bias = epi->bias;
+        p.residual = epi->residual;
+        p.z = epi->z;
+    }
+    return launched(ops.launch(m, p, static_cast<int>(clusters) * cg * split, smem, stream, overlap(h)));
 }
 
 // How the product with 4-bit weights is done: rows of a block (8: nibble.cuh, 32
@@ -187,6 +189,17 @@ gemm_status_t check_product(gemm_ctx *h, int64_t rows, int64_t experts, int64_t 
     if (h == nullptr || rows < 0 || experts < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
     if (rows > kMaxSize || experts > kMaxSize || N > kMaxSize || K > kMaxSize) return GEMM_ERR_INVALID_ARG;
     if (experts > 0 && (offsets == nullptr || !aligned4(offsets))) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+constexpr int32_t kNoOffsets = 0;   // stands in the checks for offsets that need not be there
+
+// What e4m3 sums are multiplied by.
+gemm_status_t scale_of(float scale_a, float scale_b, float *scale)
+{
+    if (!(scale_a > 0.0f) || !(scale_b > 0.0f) || !std::isfinite(scale_a) || !std::isfinite(scale_b))
+        return GEMM_ERR_INVALID_ARG;
+    *scale = static_cast<float>(1.0 / (static_cast<double>(scale_a) * static_cast<double>(scale_b)));
     return GEMM_OK;
 }
 
@@ -269,11 +282,7 @@ gemm_status_t gemm_run_experts(gemm_handle_t h, int64_t rows, int64_t experts, i
     if (st != GEMM_OK) return st;
     if ((K * elem_bytes(dtype)) % 16 != 0 || (N * 2) % 16 != 0) return GEMM_ERR_INVALID_ARG;
     float scale = 1.0f;
-    if (dtype == GEMM_E4M3) {
-        if (!(scale_a > 0.0f) || !(scale_b > 0.0f) || !std::isfinite(scale_a) || !std::isfinite(scale_b))
-            return GEMM_ERR_INVALID_ARG;
-        scale = static_cast<float>(1.0 / (static_cast<double>(scale_a) * static_cast<double>(scale_b)));
-    }
+    if (dtype == GEMM_E4M3 && (st = scale_of(scale_a, scale_b, &scale)) != GEMM_OK) return st;
     if (rows == 0 || experts == 0 || N == 0) return GEMM_OK;
     if (C == nullptr || !aligned16(C)) return GEMM_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || B == nullptr || !aligned16(A) || !aligned16(B))) return GEMM_ERR_INVALID_ARG;
@@ -314,6 +323,25 @@ gemm_status_t gemm_run_experts_wgrad(gemm_handle_t h, int64_t rows, int64_t expe
     if (rows == 0)   // every sum is empty
         return launched(cudaMemsetAsync(dB, 0, static_cast<size_t>(experts) * N * K * 2, s));
     return run_product(h, EXPERT_WGRAD, rows, experts, N, K, A, dC, offsets, dB, dtype, 1.0f, s);
+}
+
+gemm_status_t gemm_run_linear(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *A,
+                              const void *B, const void *bias, const void *residual, const int32_t *offsets, void *C,
+                              void *Z, int act, gemm_dtype_t dtype, float scale_a, float scale_b, void *stream)
+{
+    if (dtype < GEMM_F16 || dtype > GEMM_E4M3 || !is_act(act)) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_product(h, rows, experts, N, K, experts == 1 && offsets == nullptr ? &kNoOffsets : offsets);
+    if (st != GEMM_OK) return st;
+    const bool gated = act & GEMM_ACT_GATED;
+    if ((K * elem_bytes(dtype)) % 16 != 0 || N % 8 != 0 || (gated && N > kMaxSize / 2)) return GEMM_ERR_INVALID_ARG;
+    float scale = 1.0f;
+    if (dtype == GEMM_E4M3 && (st = scale_of(scale_a, scale_b, &scale)) != GEMM_OK) return st;
+    if (rows == 0 || experts == 0 || N == 0) return GEMM_OK;
+    if (C == nullptr || !aligned16(C) || !aligned16(bias) || !aligned16(residual) || !aligned16(Z)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (A == nullptr || B == nullptr || !aligned16(A) || !aligned16(B))) return GEMM_ERR_INVALID_ARG;
+    if ((st = on_device(h)) != GEMM_OK) return st;
+    const Epilogue epi{bias, residual, Z, act};
+    return run_product(h, EXPERT_FWD, rows, experts, N, K, B, A, offsets, C, dtype, scale, static_cast<cudaStream_t>(stream), &epi);
 }
 
 gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, int64_t group,

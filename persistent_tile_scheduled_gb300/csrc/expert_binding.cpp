@@ -1,4 +1,5 @@
-// The expert layer's calls from Python, as an extension module.
+// The expert layer's calls, and those around its products, from Python, as an
+// extension module.
 //
 // A decoding step makes several of these calls for a few microseconds of GPU
 // work each, so what a call costs the host counts: with the tensors checked in
@@ -67,13 +68,20 @@ public:
         return static_cast<float>(x);
     }
 
-    // a dtype of the library, and torch's for it
-    gemm_dtype_t type(const char *what, PyObject **torch)
+    // a dtype of the library, up to `last`, and torch's for it
+    gemm_dtype_t type(const char *what, PyObject **torch, gemm_dtype_t last = GEMM_E4M3)
     {
         const int64_t d = integer();
-        if (ok_ && (d < GEMM_F16 || d > GEMM_E4M3)) refuse(what, Py_None, Py_None, d);
-        *torch = ok_ ? g_elements[d] : nullptr;
+        if (ok_ && (d < GEMM_F16 || d > last)) refuse(what, Py_None, Py_None, d);
+        *torch = !ok_ ? nullptr : d == GEMM_F32 ? g_f32 : g_elements[d];
         return static_cast<gemm_dtype_t>(ok_ ? d : 0);
+    }
+
+    // an int argument of the C call; what does not fit in 32 bits is nothing that it takes
+    int choice()
+    {
+        const int64_t x = integer();
+        return x < INT32_MIN || x > INT32_MAX ? -1 : static_cast<int>(x);
     }
 
     gemm_handle_t handle()
@@ -164,7 +172,7 @@ PyObject *run(const Args &a, F f)
 }
 
 // The functions below take every argument of the C call, in its order but for
-// the dtype, which comes first: the arrays' checks need it.
+// the dtype and the activation, which come first: the arrays' checks need them.
 
 #define PTS_CALL(name_, count_)                                                   \
     PyObject *name_(PyObject *, PyObject *const *v, Py_ssize_t n)                 \
@@ -279,6 +287,91 @@ PTS_CALL(run_nibble, 14)
     });
 }
 
+// features of a matrix with N outputs
+int64_t features_of(int act, int64_t N) { return act >= 0 && (act & GEMM_ACT_GATED) && N < INT64_MAX / 2 ? 2 * N : N; }
+
+PTS_CALL(run_linear, 17)
+    PyObject *t;
+    const gemm_dtype_t dtype = a.type("gemm_run_linear", &t);
+    const int act = a.choice();
+    const auto h = a.handle();
+    const int64_t rows = a.integer(), experts = a.integer(), N = a.integer(), K = a.integer(), all = features_of(act, N);
+    PyObject *to = dtype == GEMM_E4M3 ? g_elements[GEMM_BF16] : t;
+    const void *A = a.array(t, product({rows, K}), "A"), *B = a.array(t, product({experts, all, K}), "B");
+    const void *bias = a.array(to, product({experts, all}), "bias"), *residual = a.array(to, product({rows, N}), "residual");
+    const auto offsets = static_cast<const int32_t *>(a.array(g_i32, offsets_of(experts), "offsets"));
+    void *C = a.array(to, product({rows, N}), "C"), *Z = a.array(to, product({rows, all}), "Z");
+    const float scale_a = a.real(), scale_b = a.real();
+    void *stream = a.stream();
+    return run(a, [&] {
+        return gemm_run_linear(h, rows, experts, N, K, A, B, bias, residual, offsets, C, Z, act, dtype, scale_a, scale_b, stream);
+    });
+}
+
+PTS_CALL(linear_grad, 12)
+    PyObject *t;
+    const gemm_dtype_t dtype = a.type("gemm_linear_grad", &t);
+    const int act = a.choice();
+    const auto h = a.handle();
+    const int64_t rows = a.integer(), experts = a.integer(), N = a.integer(), all = features_of(act, N);
+    const void *dC = a.array(t, product({rows, N}), "dC"), *Z = a.array(t, product({rows, all}), "Z");
+    const auto offsets = static_cast<const int32_t *>(a.array(g_i32, offsets_of(experts), "offsets"));
+    void *dZ = a.array(t, product({rows, all}), "dZ");
+    const auto dbias = static_cast<float *>(a.array(g_f32, product({experts, all}), "dbias"));
+    void *stream = a.stream();
+    return run(a, [&] { return gemm_linear_grad(h, rows, experts, N, dC, Z, offsets, dZ, dbias, act, dtype, stream); });
+}
+
+PTS_CALL(expert_route, 10)
+    PyObject *t;
+    const gemm_dtype_t dtype = a.type("gemm_expert_route", &t, GEMM_F32);
+    const auto h = a.handle();
+    const int64_t tokens = a.integer(), top_k = a.integer(), experts = a.integer(), m = product({tokens, top_k});
+    const void *logits = a.array(t, product({tokens, experts}), "logits");
+    const auto ids = static_cast<int32_t *>(a.array(g_i32, m, "expert_ids"));
+    const auto weights = static_cast<float *>(a.array(g_f32, m, "weights"));
+    const auto mode = static_cast<gemm_route_t>(a.choice());
+    void *stream = a.stream();
+    return run(a, [&] { return gemm_expert_route(h, tokens, top_k, experts, logits, ids, weights, mode, dtype, stream); });
+}
+
+PTS_CALL(expert_route_grad, 11)
+    PyObject *t;
+    const gemm_dtype_t dtype = a.type("gemm_expert_route_grad", &t, GEMM_F32);
+    const auto h = a.handle();
+    const int64_t tokens = a.integer(), top_k = a.integer(), experts = a.integer(), m = product({tokens, top_k});
+    const void *logits = a.array(t, product({tokens, experts}), "logits");
+    const auto ids = static_cast<const int32_t *>(a.array(g_i32, m, "expert_ids"));
+    const auto dweights = static_cast<const float *>(a.array(g_f32, m, "dweights"));
+    void *dlogits = a.array(t, product({tokens, experts}), "dlogits");
+    const auto mode = static_cast<gemm_route_t>(a.choice());
+    void *stream = a.stream();
+    return run(a, [&] {
+        return gemm_expert_route_grad(h, tokens, top_k, experts, logits, ids, dweights, dlogits, mode, dtype, stream);
+    });
+}
+
+PTS_CALL(expert_layer, 19)
+    PyObject *t;
+    const gemm_dtype_t dtype = a.type("gemm_expert_layer", &t);
+    const int act = a.choice();
+    const auto h = a.handle();
+    const int64_t tokens = a.integer(), top_k = a.integer(), experts = a.integer(), dim = a.integer(), hidden = a.integer();
+    const int64_t m = product({tokens, top_k}), all = features_of(act, hidden), row = product({tokens, dim});
+    const void *X = a.array(t, row, "X");
+    const auto ids = static_cast<const int32_t *>(a.array(g_i32, m, "expert_ids"));
+    const auto weights = static_cast<const float *>(a.array(g_f32, m, "weights"));
+    const void *up = a.array(t, product({experts, all, dim}), "up"), *up_bias = a.array(t, product({experts, all}), "up_bias");
+    const void *down = a.array(t, product({experts, dim, hidden}), "down"), *down_bias = a.array(t, product({experts, dim}), "down_bias");
+    const void *residual = a.array(t, row, "residual");
+    void *Hs = a.array(t, product({m, hidden}), "Hs"), *Y = a.array(t, row, "Y");
+    void *stream = a.stream();
+    return run(a, [&] {
+        return gemm_expert_layer(h, tokens, top_k, experts, dim, hidden, X, ids, weights, up, up_bias, down, down_bias, residual, Hs, Y,
+                                 act, dtype, stream);
+    });
+}
+
 // setup(Tensor, refuse, float16, bfloat16, float8_e4m3fn, int32, float32, uint8)
 PyObject *setup(PyObject *, PyObject *const *v, Py_ssize_t n)
 {
@@ -310,7 +403,9 @@ PyObject *setup(PyObject *, PyObject *const *v, Py_ssize_t n)
 #define PTS_METHOD(name_) {#name_, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&name_)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {PTS_METHOD(setup), PTS_METHOD(expert_sort), PTS_METHOD(expert_gather), PTS_METHOD(expert_combine),
                            PTS_METHOD(expert_combine_grad), PTS_METHOD(run_experts), PTS_METHOD(run_experts_dgrad),
-                           PTS_METHOD(run_experts_wgrad), PTS_METHOD(run_nibble), {nullptr, nullptr, 0, nullptr}};
+                           PTS_METHOD(run_experts_wgrad), PTS_METHOD(run_nibble), PTS_METHOD(run_linear),
+                           PTS_METHOD(linear_grad), PTS_METHOD(expert_route), PTS_METHOD(expert_route_grad),
+                           PTS_METHOD(expert_layer), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "pts_experts", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -48,6 +48,9 @@
 // offsets as it walks them), and in WGRAD a warp that clears.  Waits are
 // bounded in the same way.
 #pragma once
+#include <type_traits>
+
+#include "activation.cuh"
 #include "expert_launch.h"
 #include "gemm_kernel.cuh"
 
@@ -71,15 +74,21 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr)
            | (1ull << 46) | (2ull << 61);
 }
 
-template <int KIND, int MODE, int CG, int BN>
+template <int EPI>
+using MapsOf = std::conditional_t<EPI == EPI_NONE, ExpertMaps, LinearMaps>;
+
+template <int KIND, int MODE, int CG, int BN, int EPI = EPI_NONE>
 __global__ void __launch_bounds__(expert_threads(MODE), 1)
-    expert_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                  const __grid_constant__ CUtensorMap tmXs, const __grid_constant__ CUtensorMap tmO,
-                  const ExpertParams p)
+    expert_kernel(const __grid_constant__ MapsOf<EPI> maps, const ExpertParams p)
 {
     // tmW: boxes of 128 features x one k-block (MN-major: 64 features x a stage); tmX: boxes
     // of BN / CG rows x one k-block, tmXs: of 16 rows (MN-major: both as tmW);
-    // tmO: the store box, 32 features x 64 rows
+    // tmO: the store box, 32 features x 64 rows.  With an epilogue 32 rows, gated 16
+    // features, and a box of W holds 64 features of a gate and of what it multiplies
+    // (encode_map_gated), so that a lane of the epilogue has both of its sums.
+    static_assert(EPI == EPI_NONE || MODE == EXPERT_FWD, "");
+    const CUtensorMap &tmW = maps.w, &tmX = maps.x, &tmXs = maps.xs, &tmO = maps.o;
+    constexpr int kFeatures = EPI == EPI_GATED ? kRowsPerCta / 2 : kRowsPerCta;   // output features of a CTA's tile
     constexpr bool kWmn = MODE != EXPERT_FWD;     // the operand's features are contiguous, the contraction is not
     constexpr bool kXmn = MODE == EXPERT_WGRAD;
     constexpr int KBS = kb_per_stage(CG);
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     const uint32_t bar0 = sEpi + epi_bytes();
     const uint32_t full0 = bar0;                             // + 8*s
     const uint32_t empty0 = bar0 + 8 * kMaxStages;           // + 8*s
-    const uint32_t fix0 = bar0 + 16 * kMaxStages;            // + 8*s (WGRAD)
+    const uint32_t fix0 = bar0 + 16 * kMaxStages;            // + 8*s (WGRAD; with an epilogue the residual's boxes)
     const uint32_t acc_full0 = bar0 + 24 * kMaxStages;       // + 8*b
     const uint32_t acc_empty0 = acc_full0 + 16;              // + 8*b
     const uint32_t ring_full0 = acc_empty0 + 16;             // + 8*r
@@ -134,6 +143,8 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             mbar_init(empty0 + 8 * s, 1);
             if (MODE == EXPERT_WGRAD) mbar_init(fix0 + 8 * s, 1);
         }
+        if (EPI != EPI_NONE)   // (the residual's boxes, two to an epilogue warp)
+            for (int k = 0; k < 2 * kEpiWarps; ++k) mbar_init(fix0 + 8 * k, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
             mbar_init(acc_empty0 + 8 * b, kEpiWarps * CG);
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             ExpertItem t;
             if (ring_read(i, t) <= 0) break;
             const int xr = t.n_len / CG;   // this CTA's accumulator columns
-            const int wf = t.f0 + static_cast<int>(rank) * kRowsPerCta;
+            const int wf = t.f0 + static_cast<int>(rank) * kFeatures;
             const int xrow = t.row0 + static_cast<int>(rank) * xr;
             // K-major X: one large box when it holds mostly wanted rows, else boxes of 16
             const bool big = 2 * xr > kXRows;
@@ -272,6 +283,11 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
 #pragma unroll
                         for (int b = 0; b < kRowsPerCta / 64; ++b)
                             load(da + b * kBlock, &tmW, wf + 64 * b, t.c0 + c, MODE == EXPERT_DGRAD ? t.e : 0);
+                    } else if constexpr (EPI == EPI_GATED) {
+                        for (int j = 0; j < nk; ++j) {
+                            if (pair) tma_load_5d_pair(da + j * (SA / KBS), &tmW, fbc, c + j * KELEMS, 0, 0, wf / 8, t.e);
+                            else tma_load_5d(da + j * (SA / KBS), &tmW, fbc, c + j * KELEMS, 0, 0, wf / 8, t.e);
+                        }
                     } else {
                         for (int j = 0; j < nk; ++j) load(da + j * (SA / KBS), &tmW, c + j * KELEMS, wf, t.e);
                     }
@@ -374,93 +390,271 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
         __syncwarp();
     } else if (warp < 2 + kEpiWarps) {
         // ============================== epilogue ===============================
-        // A warp owns 32 features (TMEM lanes) of the tile.  Per chunk of 64
-        // output rows it packs the fragments, stores them transposed into a
-        // staging buffer of 64 rows x 64 bytes (64-byte swizzle) and hands
-        // that to one TMA store; a chunk that ends inside an expert's last
-        // rows is copied out 16 bytes at a time instead.
-        const uint32_t q = warp & 3u;
-        const uint32_t stage_base = sEpi + (warp - 2) * (kEpiBufsPerWarp * kEpiBufBytes);
-        // stmatrix: this lane's address is that of row (lane % 8) of the 8 x 8
-        // matrix of features 8 (lane / 8) .. + 7
-        const uint32_t st_row = lane & 7u, st_chunk = lane >> 3;
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        uint32_t nstore = 0;
-        for (int i = 0;; ++i) {
-            ExpertItem t;
-            if (ring_read(i, t) <= 0) break;
-            const bool empty_sum = t.nkb == 0;
-            if (!ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL)) break;
-            tc_fence_after();
-            if (kSplit && split > 1) break;   // (the only tile; added up below)
-            const uint32_t tbase = tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN);
-            const int chunks = (t.n_len + 63) / 64;
-            const int f = t.f0 + static_cast<int>(rank) * kRowsPerCta + static_cast<int>(q) * 32;
-            for (int c = 0; c < chunks; ++c) {
-                uint32_t lo[32], hi[32];
-                tmem_ld_16x256b_x8(tbase + c * 64, lo);
-                tmem_ld_16x256b_x8(tbase + (16u << 16) + c * 64, hi);
-                tmem_wait_ld();
-                if (empty_sum) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) lo[j] = hi[j] = 0u;
+        if constexpr (EPI != EPI_NONE) {
+            // As below, with chunks of 32 rows: a warp's 8 KB are four boxes.  C goes
+            // out through a ring of them, into which the residual's boxes are loaded
+            // ahead, so that each is added in place; Z takes two of the four.
+            constexpr int kF = EPI == EPI_GATED ? 16 : 32;   // output features of a warp
+            constexpr uint32_t kRow = 2 * kF, kBox = kLinearChunk * kRow;
+            constexpr uint32_t kSlot = kEpiBufsPerWarp * kEpiBufBytes / 4;
+            const uint32_t q = warp & 3u;
+            const uint32_t stage_base = sEpi + (warp - 2) * (kEpiBufsPerWarp * kEpiBufBytes);
+            const uint32_t res0 = fix0 + 16 * (warp - 2);   // + 8 * (chunk & 1): the residual's box is there
+            const bool keep = p.z != nullptr, res = p.residual != nullptr;
+            const uint32_t bufs = keep ? 2 : 4;
+            const int lead = static_cast<int>(bufs) / 2;    // chunks that the residual's loads are ahead
+            // stmatrix: this lane's row and 16 bytes of it (32 features: 8 rows at a time; gated 16)
+            const uint32_t st_row = EPI == EPI_GATED ? (lane & 7u) + ((lane >> 4) << 3) : lane & 7u;
+            const uint32_t st_chunk = EPI == EPI_GATED ? (lane >> 3) & 1u : lane >> 3;
+            auto at = [&](uint32_t buf, uint32_t row, uint32_t chunk) -> uint32_t {   // (the store maps' swizzles)
+                return buf + row * kRow + ((chunk ^ (EPI == EPI_GATED ? (row >> 2) & 1u : (row >> 1) & 3u)) << 4);
+            };
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            uint32_t n = 0, loads = 0;   // chunks done, residual boxes asked for
+            for (int i = 0;; ++i) {
+                ExpertItem t;
+                if (ring_read(i, t) <= 0) break;
+                if (kSplit && split > 1) {   // (the only tile; added up below)
+                    ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL);
+                    tc_fence_after();
+                    break;
                 }
-                if (c + 1 == chunks) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (CG == 2 && !leader)
-                        mbar_arrive_cluster_if(one, mapa(acc_empty0 + 8 * acc, 0u));
-                    else
-                        mbar_arrive_if(one, acc_empty0 + 8 * acc);
-                }
-                const uint32_t buf = stage_base + (nstore & 1u) * kEpiBufBytes;
-                bulk_wait_read<1>();   // the store that used this buffer has read it
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t row = 8 * j + st_row;
-                    stmatrix_x4_trans(buf + row * 64 + ((st_chunk ^ ((row >> 1) & 3u)) << 4),
-                                      pack2<KIND>(lo[4 * j], lo[4 * j + 1], p.out_scale),
-                                      pack2<KIND>(lo[4 * j + 2], lo[4 * j + 3], p.out_scale),
-                                      pack2<KIND>(hi[4 * j], hi[4 * j + 1], p.out_scale),
-                                      pack2<KIND>(hi[4 * j + 2], hi[4 * j + 3], p.out_scale));
-                }
-                const int row0 = t.row0 + c * 64;
-                if (MODE == EXPERT_WGRAD || row0 + 64 <= t.row_end) {
+                const bool empty_sum = t.nkb == 0;
+                const int chunks = (t.n_len + kLinearChunk - 1) / kLinearChunk;
+                const int f = t.f0 + static_cast<int>(rank) * kFeatures + static_cast<int>(q) * kF;
+                auto load_residual = [&](int c) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    tma_store_3d_if((f < p.features && row0 < t.row_end) ? one : 0u, &tmO, buf, f, row0,
-                                    MODE == EXPERT_WGRAD ? t.e : 0);
-                } else {
+                    if (elect_one()) {
+                        const uint32_t bar = res0 + 8 * (loads & 1u);
+                        mbar_arrive_expect_tx(bar, kBox);
+                        tma_load_3d(1u, stage_base + loads % bufs * kSlot, &maps.r, bar, f, t.row0 + c * kLinearChunk, 0);
+                    }
                     __syncwarp();
+                    ++loads;
+                };
+                if (res) {
+                    bulk_wait_read<1>();
+                    for (int c = 0; c < lead && c < chunks; ++c) load_residual(c);
+                }
+                // a lane's features are f + lane / 4 + 0, 8, 16, 24; gated 0 of both matrices and 8 of both
+                float bias[4] = {};
+                if (p.bias) {
+                    const uint16_t *b = static_cast<const uint16_t *>(p.bias)
+                                        + static_cast<long long>(t.e) * (EPI == EPI_GATED ? 2ll * p.features : p.features);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t r = 8 * j + (lane >> 2), ch = lane & 3u;
-                        const uint4 v = ld_shared_v4(buf + r * 64 + ((ch ^ ((r >> 1) & 3u)) << 4));
-                        const long long row = row0 + static_cast<long long>(r);
-                        if (row < t.row_end && f + 8 * static_cast<int>(ch) < p.features)
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * p.features + f + 8 * ch) = v;
+                    for (int k = 0; k < 4; ++k) {
+                        const int ff = f + static_cast<int>(lane >> 2) + 8 * (EPI == EPI_GATED ? k >> 1 : k);
+                        if (ff < p.features) bias[k] = unpack1<KIND>(ld_global(b + ff + (EPI == EPI_GATED && (k & 1) ? p.features : 0)));
                     }
                 }
-                bulk_commit();
-                ++nstore;
+                if (!ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL)) break;
+                tc_fence_after();
+                const uint32_t tbase = tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN);
+                bool ok = true;
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t lo[16], hi[16];
+                    tmem_ld_16x256b_x4(tbase + c * kLinearChunk, lo);
+                    tmem_ld_16x256b_x4(tbase + (16u << 16) + c * kLinearChunk, hi);
+                    tmem_wait_ld();
+                    if (c + 1 == chunks) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (CG == 2 && !leader)
+                            mbar_arrive_cluster_if(one, mapa(acc_empty0 + 8 * acc, 0u));
+                        else
+                            mbar_arrive_if(one, acc_empty0 + 8 * acc);
+                    }
+                    float x[16], y[16];   // [rows 8j ..][feature 0, 8; y: 16, 24 (gated 0 of both matrices; y: 8)][2 rows]
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        x[j] = fmaf(empty_sum ? 0.0f : __uint_as_float(lo[j]), p.out_scale, bias[(j >> 1) & 1]);
+                        y[j] = fmaf(empty_sum ? 0.0f : __uint_as_float(hi[j]), p.out_scale, bias[2 + ((j >> 1) & 1)]);
+                    }
+                    const uint32_t buf = stage_base + n % bufs * kSlot, zbuf = stage_base + (2 + (n & 1u)) * kSlot;
+                    bulk_wait_read<1>();   // the stores that used these boxes have read them
+                    __syncwarp();
+                    if (keep) {
+                        if constexpr (EPI == EPI_GATED) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 8)   // 16 rows, of each matrix
+#pragma unroll
+                                for (int k = 0; k < 4; k += 2)
+                                    stmatrix_x4_trans(at(zbuf + k / 2 * kBox, 2 * j + st_row, st_chunk), pack2f<KIND>(x[j + k], x[j + k + 1]),
+                                                      pack2f<KIND>(y[j + k], y[j + k + 1]), pack2f<KIND>(x[j + k + 4], x[j + k + 5]),
+                                                      pack2f<KIND>(y[j + k + 4], y[j + k + 5]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                stmatrix_x4_trans(at(zbuf, 2 * j + st_row, st_chunk), pack2f<KIND>(x[j], x[j + 1]), pack2f<KIND>(x[j + 2], x[j + 3]),
+                                                  pack2f<KIND>(y[j], y[j + 1]), pack2f<KIND>(y[j + 2], y[j + 3]));
+                        }
+                    }
+                    with_act(p.act, [&](auto tag) {
+                        constexpr int A = decltype(tag)::value;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (EPI == EPI_GATED && (j & 2)) continue;
+                            x[j] = act<A>(x[j]);
+                            y[j] = act<A>(y[j]);
+                            if (EPI == EPI_GATED) x[j] *= x[j + 2], y[j] *= y[j + 2];
+                        }
+                    });
+                    if (res) {
+                        ok = ctl.wait_all(res0 + 8 * (n & 1u), (n >> 1) & 1u, WHERE_FULL);
+                        if (!ok) break;
+                        if (c + lead < chunks) {
+                            if (lead == 1) bulk_wait_read<0>();   // (its box is the last chunk's)
+                            load_residual(c + lead);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += EPI == EPI_GATED ? 8 : 4) {
+                        // four matrices of 8 rows x 8 features
+                        float *v[4] = {x + j, EPI == EPI_GATED ? y + j : x + j + 2, EPI == EPI_GATED ? x + j + 4 : y + j, EPI == EPI_GATED ? y + j + 4 : y + j + 2};
+                        const uint32_t to = at(buf, 2 * j + st_row, st_chunk);
+                        if (res) {
+                            uint32_t r[4];
+                            ldmatrix_x4_trans(to, r[0], r[1], r[2], r[3]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 a = unpack2<KIND>(r[k]);
+                                v[k][0] += a.x;
+                                v[k][1] += a.y;
+                            }
+                        }
+                        stmatrix_x4_trans(to, pack2f<KIND>(v[0][0], v[0][1]), pack2f<KIND>(v[1][0], v[1][1]), pack2f<KIND>(v[2][0], v[2][1]),
+                                          pack2f<KIND>(v[3][0], v[3][1]));
+                    }
+                    const int row0 = t.row0 + c * kLinearChunk;
+                    if (row0 + kLinearChunk <= t.row_end) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        const uint32_t go = f < p.features ? one : 0u;
+                        tma_store_3d_if(go, &tmO, buf, f, row0, 0);
+                        if (keep) {
+                            tma_store_3d_if(go, &maps.z, zbuf, f, EPI == EPI_GATED ? 0 : row0, EPI == EPI_GATED ? row0 : 0);
+                            if constexpr (EPI == EPI_GATED) tma_store_3d_if(go, &maps.z, zbuf + kBox, f, 1, row0);
+                        }
+                    } else {
+                        __syncwarp();
+                        constexpr uint32_t kPieces = kF / 8;   // 16-byte pieces of a row
+                        for (uint32_t piece = lane; piece < kLinearChunk * kPieces; piece += 32) {
+                            const uint32_t r = piece / kPieces, ch = piece % kPieces;
+                            const long long row = row0 + static_cast<long long>(r);
+                            const int ff = f + 8 * static_cast<int>(ch);
+                            if (row >= t.row_end || ff >= p.features) continue;
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * p.features + ff) = ld_shared_v4(at(buf, r, ch));
+                            if (!keep) continue;
+                            uint16_t *z = static_cast<uint16_t *>(p.z) + row * p.features * (EPI == EPI_GATED ? 2 : 1) + ff;
+                            *reinterpret_cast<uint4 *>(z) = ld_shared_v4(at(zbuf, r, ch));
+                            if constexpr (EPI == EPI_GATED) *reinterpret_cast<uint4 *>(z + p.features) = ld_shared_v4(at(zbuf + kBox, r, ch));
+                        }
+                        __syncwarp();
+                    }
+                    bulk_commit();
+                    ++n;
+                }
+                if (!ok) break;
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
             }
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1u;
+            for (; n < loads; ++n) ctl.drain(res0 + 8 * (n & 1u), (n >> 1) & 1u, 10000000ull);   // (stopped early)
+            bulk_wait_read<0>();
+            __syncwarp();
+        } else {
+            // A warp owns 32 features (TMEM lanes) of the tile.  Per chunk of 64
+            // output rows it packs the fragments, stores them transposed into a
+            // staging buffer of 64 rows x 64 bytes (64-byte swizzle) and hands
+            // that to one TMA store; a chunk that ends inside an expert's last
+            // rows is copied out 16 bytes at a time instead.
+            const uint32_t q = warp & 3u;
+            const uint32_t stage_base = sEpi + (warp - 2) * (kEpiBufsPerWarp * kEpiBufBytes);
+            // stmatrix: this lane's address is that of row (lane % 8) of the 8 x 8
+            // matrix of features 8 (lane / 8) .. + 7
+            const uint32_t st_row = lane & 7u, st_chunk = lane >> 3;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            uint32_t nstore = 0;
+            for (int i = 0;; ++i) {
+                ExpertItem t;
+                if (ring_read(i, t) <= 0) break;
+                const bool empty_sum = t.nkb == 0;
+                if (!ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL)) break;
+                tc_fence_after();
+                if (kSplit && split > 1) break;   // (the only tile; added up below)
+                const uint32_t tbase = tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN);
+                const int chunks = (t.n_len + 63) / 64;
+                const int f = t.f0 + static_cast<int>(rank) * kRowsPerCta + static_cast<int>(q) * 32;
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t lo[32], hi[32];
+                    tmem_ld_16x256b_x8(tbase + c * 64, lo);
+                    tmem_ld_16x256b_x8(tbase + (16u << 16) + c * 64, hi);
+                    tmem_wait_ld();
+                    if (empty_sum) {
+    #pragma unroll
+                        for (int j = 0; j < 32; ++j) lo[j] = hi[j] = 0u;
+                    }
+                    if (c + 1 == chunks) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (CG == 2 && !leader)
+                            mbar_arrive_cluster_if(one, mapa(acc_empty0 + 8 * acc, 0u));
+                        else
+                            mbar_arrive_if(one, acc_empty0 + 8 * acc);
+                    }
+                    const uint32_t buf = stage_base + (nstore & 1u) * kEpiBufBytes;
+                    bulk_wait_read<1>();   // the store that used this buffer has read it
+                    __syncwarp();
+    #pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t row = 8 * j + st_row;
+                        stmatrix_x4_trans(buf + row * 64 + ((st_chunk ^ ((row >> 1) & 3u)) << 4),
+                                          pack2<KIND>(lo[4 * j], lo[4 * j + 1], p.out_scale),
+                                          pack2<KIND>(lo[4 * j + 2], lo[4 * j + 3], p.out_scale),
+                                          pack2<KIND>(hi[4 * j], hi[4 * j + 1], p.out_scale),
+                                          pack2<KIND>(hi[4 * j + 2], hi[4 * j + 3], p.out_scale));
+                    }
+                    const int row0 = t.row0 + c * 64;
+                    if (MODE == EXPERT_WGRAD || row0 + 64 <= t.row_end) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        tma_store_3d_if((f < p.features && row0 < t.row_end) ? one : 0u, &tmO, buf, f, row0,
+                                        MODE == EXPERT_WGRAD ? t.e : 0);
+                    } else {
+                        __syncwarp();
+    #pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t r = 8 * j + (lane >> 2), ch = lane & 3u;
+                            const uint4 v = ld_shared_v4(buf + r * 64 + ((ch ^ ((r >> 1) & 3u)) << 4));
+                            const long long row = row0 + static_cast<long long>(r);
+                            if (row < t.row_end && f + 8 * static_cast<int>(ch) < p.features)
+                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * p.features + f + 8 * ch) = v;
+                        }
+                    }
+                    bulk_commit();
+                    ++nstore;
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
             }
+            bulk_wait_read<0>();
+            __syncwarp();
         }
-        bulk_wait_read<0>();
-        __syncwarp();
     } else if (warp == kSchedWarp) {
         // ============================== scheduler ==============================
         // Tile w of all experts' tiles in order, w = cluster, cluster + grid, ...
         if (leader) {
-            const int tiles_f = (p.features + kRowsPerCta * CG - 1) / (kRowsPerCta * CG);
+            const int tiles_f = (p.features + kFeatures * CG - 1) / (kFeatures * CG);
             bool ok = true;
             int i = 0;
             auto offset = [&](int e) -> int {   // clamped, so that no offsets lead outside the arrays
+                if (EPI != EPI_NONE && !p.offsets) return e == 0 ? 0 : p.rows;
                 const int v = ld_global(p.offsets + e);
                 return v < 0 ? 0 : (v > p.rows ? p.rows : v);
             };
@@ -519,7 +713,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                         const int size = ((ecnt - 1) / etn + kGran) / kGran * kGran;
                         ExpertItem t;
                         t.e = e0 + src;
-                        t.f0 = itf * (kRowsPerCta * CG);
+                        t.f0 = itf * (kFeatures * CG);
                         t.row0 = elo + it * size;
                         t.row_end = elo + ((it + 1) * size < ecnt ? (it + 1) * size : ecnt);
                         const int rows = t.row_end - t.row0;
@@ -605,19 +799,49 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
         }
         cluster_sync();
         if (there)
-            for (int i = static_cast<int>(threadIdx.x); i < part * kRowsPerCta / 2; i += static_cast<int>(blockDim.x)) {
-                const int row = i / (kRowsPerCta / 2), n = 2 * (i % (kRowsPerCta / 2));
-                float lo = 0.0f, hi = 0.0f;
+            for (int i = static_cast<int>(threadIdx.x); i < part * kFeatures / 2; i += static_cast<int>(blockDim.x)) {
+                const int row = i / (kFeatures / 2), n = 2 * (i % (kFeatures / 2));
+                const int m = EPI == EPI_GATED ? (n / 8) * 16 + n % 8 : n;   // the accumulator's row
+                float lo = 0.0f, hi = 0.0f, lo2 = 0.0f, hi2 = 0.0f;
                 for (int c = 0; c < split; ++c) {
-                    const uint32_t from = base + ((c * part + row) * kRowsPerCta + n) * 4;
+                    const uint32_t from = base + ((c * part + row) * kRowsPerCta + m) * 4;
                     lo += __uint_as_float(ld_shared_u32(from));
                     hi += __uint_as_float(ld_shared_u32(from + 4));
+                    if constexpr (EPI == EPI_GATED) {
+                        lo2 += __uint_as_float(ld_shared_u32(from + 32));
+                        hi2 += __uint_as_float(ld_shared_u32(from + 36));
+                    }
                 }
                 const long long out_row = static_cast<long long>(v0.w) + share * part + row;
                 const int f = static_cast<int>(v0.z) + n;
-                if (out_row < static_cast<int>(v1.x) && f < p.features)
-                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + out_row * p.features + f) =
-                        pack2<KIND>(__float_as_uint(lo), __float_as_uint(hi), p.out_scale);
+                if (out_row >= static_cast<int>(v1.x) || f >= p.features) continue;
+                uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + out_row * p.features + f);
+                if constexpr (EPI == EPI_NONE) {
+                    *out = pack2<KIND>(__float_as_uint(lo), __float_as_uint(hi), p.out_scale);
+                } else {
+                    constexpr int kBoth = EPI == EPI_GATED ? 2 : 1;
+                    float2 b0 = make_float2(0.0f, 0.0f), b1 = b0, r = b0;
+                    if (p.bias) {
+                        const uint16_t *bias = static_cast<const uint16_t *>(p.bias) + static_cast<long long>(v0.y) * kBoth * p.features + f;
+                        b0 = unpack2<KIND>(ld_global(reinterpret_cast<const uint32_t *>(bias)));
+                        if constexpr (EPI == EPI_GATED) b1 = unpack2<KIND>(ld_global(reinterpret_cast<const uint32_t *>(bias + p.features)));
+                    }
+                    if (p.residual)
+                        r = unpack2<KIND>(ld_global(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.residual) + out_row * p.features + f)));
+                    lo = fmaf(lo, p.out_scale, b0.x), hi = fmaf(hi, p.out_scale, b0.y);
+                    lo2 = fmaf(lo2, p.out_scale, b1.x), hi2 = fmaf(hi2, p.out_scale, b1.y);
+                    if (p.z) {
+                        uint16_t *z = static_cast<uint16_t *>(p.z) + out_row * kBoth * p.features + f;
+                        *reinterpret_cast<uint32_t *>(z) = pack2f<KIND>(lo, hi);
+                        if constexpr (EPI == EPI_GATED) *reinterpret_cast<uint32_t *>(z + p.features) = pack2f<KIND>(lo2, hi2);
+                    }
+                    with_act(p.act, [&](auto tag) {
+                        constexpr int A = decltype(tag)::value;
+                        lo = act<A>(lo), hi = act<A>(hi);
+                    });
+                    if constexpr (EPI == EPI_GATED) lo *= lo2, hi *= hi2;
+                    *out = pack2f<KIND>(lo + r.x, hi + r.y);
+                }
             }
     }
 
@@ -642,7 +866,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     }
 }
 
-template <int KIND, int MODE, int CG, int BN>
+template <int KIND, int MODE, int CG, int BN, int EPI = EPI_NONE>
 struct ExpertInst {
     static void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, int cluster, int smem,
                        cudaStream_t stream, bool overlap)
@@ -674,7 +898,7 @@ struct ExpertInst {
     // occupancy query is not asked there).
     static cudaError_t prepare(int smem, int sms, int *clusters)
     {
-        cudaError_t e = cudaFuncSetAttribute(expert_kernel<KIND, MODE, CG, BN>,
+        cudaError_t e = cudaFuncSetAttribute(expert_kernel<KIND, MODE, CG, BN, EPI>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         *clusters = sms;
@@ -682,16 +906,15 @@ struct ExpertInst {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(cfg, attr, 2, CG, smem, nullptr, false);
-        return cudaOccupancyMaxActiveClusters(clusters, expert_kernel<KIND, MODE, CG, BN>, &cfg);
+        return cudaOccupancyMaxActiveClusters(clusters, expert_kernel<KIND, MODE, CG, BN, EPI>, &cfg);
     }
 
-    static cudaError_t launch(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &xs, const CUtensorMap &o,
-                              const ExpertParams &p, int grid, int smem, cudaStream_t stream, bool overlap)
+    static cudaError_t launch(const LinearMaps &maps, const ExpertParams &p, int grid, int smem, cudaStream_t stream, bool overlap)
     {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         config(cfg, attr, grid, CG * p.split, smem, stream, overlap);
-        return cudaLaunchKernelEx(&cfg, expert_kernel<KIND, MODE, CG, BN>, w, x, xs, o, p);
+        return cudaLaunchKernelEx(&cfg, expert_kernel<KIND, MODE, CG, BN, EPI>, static_cast<const MapsOf<EPI> &>(maps), p);
     }
 
     static ExpertOps ops() { return ExpertOps{&prepare, &launch}; }

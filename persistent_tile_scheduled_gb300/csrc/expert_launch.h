@@ -14,6 +14,10 @@ enum : int { EXPERT_FWD = 0, EXPERT_DGRAD = 1, EXPERT_WGRAD = 2 };
 
 // ---- the experts' products (expert_gemm.cuh) --------------------------------
 
+// The epilogue: none; bias, activation and residual (EPI_LINEAR); the same with a
+// gate's features and those it multiplies side by side (EPI_GATED).
+enum : int { EPI_NONE = 0, EPI_LINEAR = 1, EPI_GATED = 2 };
+
 struct ExpertParams {
     int32_t rows;          // rows of X (the offsets are clamped to it)
     int32_t experts;
@@ -29,6 +33,18 @@ struct ExpertParams {
     int32_t fault_load;       // test hook: the stage load of a producer that announces too many bytes (-1: none)
     uint64_t timeout_ns;
     int32_t *status;
+    // of an epilogue (offsets may then be null: one matrix has all rows)
+    int32_t act;              // gemm_act_t
+    const void *bias, *residual;   // experts x N', rows x N, or null
+    void *z;                  // rows x N', or null
+};
+
+// Tensor maps of a product, and of one with an epilogue.
+struct ExpertMaps {
+    CUtensorMap w, x, xs, o;
+};
+struct LinearMaps : ExpertMaps {
+    CUtensorMap r, z;   // residual, Z: boxes as o's
 };
 
 // producer, MMA, 4 epilogue warps, scheduler; WGRAD has a clearing warp too
@@ -49,8 +65,7 @@ constexpr int64_t kExpertFewRows = 32;  // at most so many on average
 
 struct ExpertOps {
     cudaError_t (*prepare)(int smem, int sms, int *clusters);
-    cudaError_t (*launch)(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &xs, const CUtensorMap &o,
-                          const ExpertParams &p, int grid, int smem, cudaStream_t stream, bool overlap);
+    cudaError_t (*launch)(const LinearMaps &maps, const ExpertParams &p, int grid, int smem, cudaStream_t stream, bool overlap);
 };
 
 // kind: 0 fp16, 1 bf16, 2 e4m3 (forward only); bn: kExpertTileN, or
@@ -58,6 +73,11 @@ struct ExpertOps {
 ExpertOps expert_ops_fwd(int kind, int cg, int bn);
 ExpertOps expert_ops_dgrad(int kind, int cg);
 ExpertOps expert_ops_wgrad(int kind, int cg);
+// the forward product with an epilogue
+ExpertOps linear_ops_f16(bool gated, int cg, int bn);
+ExpertOps linear_ops_bf16(bool gated, int cg, int bn);
+ExpertOps linear_ops_e4m3(bool gated, int cg, int bn);
+constexpr int kLinearChunk = 32;   // output rows per store box with an epilogue
 
 // ---- rows to the experts and back (expert_route.cu) ---------------------------
 

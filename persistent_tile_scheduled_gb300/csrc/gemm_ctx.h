@@ -74,6 +74,7 @@ struct gemm_ctx {
     // experts' products: resident clusters per dtype, mode and variant (0: single CTAs, 1: pairs,
     // 2: single CTAs with the short row tile); 0 = not asked yet
     int expert_clusters[3][3][3] = {};
+    int linear_clusters[3][2][3] = {};        // gemm_run_linear: the same per dtype, plain or gated, and variant
     bool sort_smem[2] = {};                   // gemm_expert_sort: limits raised, per kernel
     pts::NibPrepared nibble[2] = {};          // gemm_run_nibble, per dtype
 };
@@ -124,7 +125,7 @@ inline const CUtensorMap *get_map(gemm_ctx *h, const void *ptr, uint64_t rows, u
 
 // Encode the tensor map of a depth x rows x cols array of 2-byte or e4m3
 // elements (cols contiguous), box box_rows x box_cols of one depth slice.
-// box_cols fills the swizzle's width (128 or 64 bytes).
+// box_cols fills the swizzle's width (128, 64 or 32 bytes).
 inline bool encode_map3(const gemm_ctx *h, CUtensorMap *out, const void *ptr, uint64_t depth, uint64_t rows,
                         uint64_t cols, int dtype, uint32_t box_rows, uint32_t box_cols)
 {
@@ -137,8 +138,46 @@ inline bool encode_map3(const gemm_ctx *h, CUtensorMap *out, const void *ptr, ui
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return h->encode(out, t, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     box_cols * es == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                     : box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                           : CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)
+           == CUDA_SUCCESS;
+}
+
+inline CUtensorMapDataType map_type(int dtype)
+{
+    return dtype == GEMM_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+           : dtype == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+}
+
+// The matrices of a gated product, depth x (n gate rows, then n others) x cols, as
+// 8 gate rows, the 8 others of the same features, the next 8 gate rows, ...: a box
+// of 128 rows holds 64 features of both.  n is a multiple of 8.
+inline bool encode_map_gated(const gemm_ctx *h, CUtensorMap *out, const void *ptr, uint64_t depth, uint64_t n, uint64_t cols,
+                             int dtype, uint32_t box_cols)
+{
+    const cuuint64_t row = cols * (dtype == GEMM_E4M3 ? 1 : 2);
+    cuuint64_t dims[5] = {cols, 8, 2, n / 8, depth};
+    cuuint64_t strides[4] = {row, n * row, 8 * row, 2 * n * row};
+    cuuint32_t box[5] = {box_cols, 8, 2, 8, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return h->encode(out, map_type(dtype), 5, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)
+           == CUDA_SUCCESS;
+}
+
+// Rows of n gate values and n others (2-byte) as n x 2 x rows, so that a box of
+// either half ends at its last feature: box_rows x 16 of one half.
+inline bool encode_map_halves(const gemm_ctx *h, CUtensorMap *out, const void *ptr, uint64_t rows, uint64_t n, int dtype, uint32_t box_rows)
+{
+    cuuint64_t dims[3] = {n, 2, rows};
+    cuuint64_t strides[2] = {2 * n, 4 * n};
+    cuuint32_t box[3] = {16, 1, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return h->encode(out, map_type(dtype), 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE)
            == CUDA_SUCCESS;
 }
 

@@ -222,6 +222,23 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t pred, uint32_t dst, co
                  : "memory");
 }
 
+// 5-D forms.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint32_t bar, int x, int y, int z, int u, int v)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const void *tmap, uint32_t cluster_bar, int x, int y, int z, int u, int v)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+                 "l"(tmap), "r"(cluster_bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
+                 : "memory");
+}
+
 // Bring a 2-D box of the tensor into L2 (no shared-memory destination, no
 // completion); out-of-bounds parts are ignored.
 __device__ __forceinline__ void tma_prefetch_2d(uint32_t pred, const void *tmap, int x, int y)
@@ -394,6 +411,17 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
                  : "memory");
 }
 
+// The same for 32 columns.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit elements, each stored transposed: thread t
 // holds elements 2 (t % 4), + 1 of row t / 4 of matrix i in r[i]; column c of
 // matrix i goes to the 16 bytes at the address that thread 8 i + c gives.
@@ -401,6 +429,15 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, ui
 {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0),
                  "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+// The way back: the matrices that stmatrix_x4_trans stored.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
                  : "memory");
 }
 

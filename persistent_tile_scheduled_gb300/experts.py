@@ -1,4 +1,4 @@
-"""Python binding of the expert layer's operators in include/pts_gemm.h.
+"""Python binding of the expert layer's operators in include/pts_gemm.h, and of what stands around the products there.
 
 Names and order of arguments are the C functions'.  A tensor passed where the
 C call takes a pointer is checked first (on the handle's GPU, contiguous, of
@@ -35,7 +35,7 @@ def _setup(module):
 
 
 _FUNCTIONS = ("expert_sort", "expert_gather", "expert_combine", "expert_combine_grad", "run_experts", "run_experts_dgrad",
-              "run_experts_wgrad", "run_nibble")
+              "run_experts_wgrad", "run_nibble", "run_linear", "linear_grad", "expert_route", "expert_route_grad", "expert_layer")
 
 
 class _Calls:
@@ -111,4 +111,41 @@ def gemm_run_nibble(h, rows, experts, N, K, group, A, B, scales, zeros, offsets,
     status = _c.run_nibble(dtype, h, rows, experts, N, K, group, A, B, scales, zeros, offsets, C, stream)
     if status:
         raise GemmError(status, "gemm_run_nibble")
+    return 0
+
+
+def gemm_run_linear(h, rows, experts, N, K, A, B, bias, residual, offsets, C, Z, act, dtype, scale_a=1.0, scale_b=1.0, stream=None) -> int:
+    status = _c.run_linear(dtype, act, h, rows, experts, N, K, A, B, bias, residual, offsets, C, Z, scale_a, scale_b, stream)
+    if status:
+        raise GemmError(status, "gemm_run_linear")
+    return 0
+
+
+def gemm_linear_grad(h, rows, experts, N, dC, Z, offsets, dZ, dbias, act, dtype, stream=None) -> int:
+    status = _c.linear_grad(dtype, act, h, rows, experts, N, dC, Z, offsets, dZ, dbias, stream)
+    if status:
+        raise GemmError(status, "gemm_linear_grad")
+    return 0
+
+
+def gemm_expert_route(h, tokens, top_k, experts, logits, expert_ids, weights, mode, dtype, stream=None) -> int:
+    status = _c.expert_route(dtype, h, tokens, top_k, experts, logits, expert_ids, weights, mode, stream)
+    if status:
+        raise GemmError(status, "gemm_expert_route")
+    return 0
+
+
+def gemm_expert_route_grad(h, tokens, top_k, experts, logits, expert_ids, dweights, dlogits, mode, dtype, stream=None) -> int:
+    status = _c.expert_route_grad(dtype, h, tokens, top_k, experts, logits, expert_ids, dweights, dlogits, mode, stream)
+    if status:
+        raise GemmError(status, "gemm_expert_route_grad")
+    return 0
+
+
+def gemm_expert_layer(h, tokens, top_k, experts, dim, hidden, X, expert_ids, weights, up, up_bias, down, down_bias, residual, Hs, Y, act,
+                      dtype, stream=None) -> int:
+    status = _c.expert_layer(dtype, act, h, tokens, top_k, experts, dim, hidden, X, expert_ids, weights, up, up_bias, down, down_bias,
+                             residual, Hs, Y, stream)
+    if status:
+        raise GemmError(status, "gemm_expert_layer")
     return 0

@@ -13,10 +13,13 @@ from typing import Optional
 
 from . import _build
 
-GEMM_F16, GEMM_BF16, GEMM_E4M3 = 0, 1, 2
+GEMM_F16, GEMM_BF16, GEMM_E4M3, GEMM_F32 = 0, 1, 2, 3
 GEMM_SCHED_NONPERSISTENT, GEMM_SCHED_STATIC, GEMM_SCHED_CLC = 0, 1, 2
 SCHEDS = {"nonpersistent": 0, "static": 1, "clc": 2}
 GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_CUDA, GEMM_ERR_TIMEOUT, GEMM_ERR_COVERAGE = range(6)
+GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_RELU2, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_SILU = range(6)
+GEMM_ACT_GATED = 0x10
+GEMM_ROUTE_SELECTED, GEMM_ROUTE_ALL, GEMM_ROUTE_SIGMOID = range(3)
 GEMM_DEBUG_RECORDS = 0x1
 GEMM_DEBUG_CLC_STOP_AT = 0x2
 GEMM_DEBUG_FAULT_SKIP_TMA = 0x4
@@ -30,11 +33,15 @@ EXPORTED = ("gemm_create", "gemm_run", "gemm_run_host", "gemm_query", "gemm_chec
             "gemm_read_debug", "gemm_destroy", "gemm_status_string", "gemm_run_noalloc",
             "gemm_run_host_batch", "gemm_run_grouped", "gemm_query_grouped", "gemm_tensor_peak_probe",
             "gemm_expert_sort", "gemm_expert_gather", "gemm_expert_combine", "gemm_expert_combine_grad",
-            "gemm_run_experts", "gemm_run_experts_dgrad", "gemm_run_experts_wgrad", "gemm_run_nibble")
+            "gemm_run_experts", "gemm_run_experts_dgrad", "gemm_run_experts_wgrad", "gemm_run_nibble",
+            "gemm_run_linear", "gemm_linear_grad", "gemm_expert_route", "gemm_expert_route_grad", "gemm_expert_layer")
 GEMM_NOALLOC_MAX_WORK_ITEMS = 16384
 GEMM_GROUPED_MAX_PROBLEMS = 65536
 GEMM_EXPERT_SORT_MAX_EXPERTS = 1024
 GEMM_EXPERT_MAX_SIZE = 2 ** 31 - 1024
+GEMM_EXPERT_ROUTE_MAX_TOP_K = 32
+GEMM_EXPERT_LAYER_MAX_TOKENS = 64
+GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS = 512
 
 
 class gemm_opts_t(ctypes.Structure):
@@ -133,7 +140,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                        ("gemm_run_experts", [vp, i64, i64, i64, i64, vp, vp, vp, vp, dt, f32, f32, vp]),
                        ("gemm_run_experts_dgrad", [vp, i64, i64, i64, i64, vp, vp, vp, vp, dt, vp]),
                        ("gemm_run_experts_wgrad", [vp, i64, i64, i64, i64, vp, vp, vp, vp, dt, vp]),
-                       ("gemm_run_nibble", [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, dt, vp])):
+                       ("gemm_run_nibble", [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, dt, vp]),
+                       ("gemm_run_linear", [vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, dt, dt, f32, f32, vp]),
+                       ("gemm_linear_grad", [vp, i64, i64, i64, vp, vp, vp, vp, vp, dt, dt, vp]),
+                       ("gemm_expert_route", [vp, i64, i64, i64, vp, vp, vp, dt, dt, vp]),
+                       ("gemm_expert_route_grad", [vp, i64, i64, i64, vp, vp, vp, vp, dt, dt, vp]),
+                       ("gemm_expert_layer", [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, dt, dt, vp])):
         getattr(lib, name).argtypes, getattr(lib, name).restype = args, st
     lib.gemm_status_string.argtypes = [ctypes.c_int]
     lib.gemm_status_string.restype = ctypes.c_char_p
