@@ -16,9 +16,9 @@ namespace pts {
 
 namespace {
 
-constexpr int kGradThreads = 256;
-constexpr int kGradRows = 4;      // rows of a thread whose loads are on their way together
-constexpr int kGradMaxCtas = 8;   // CTAs that share an expert's rows
+constexpr int kGradThreads = 256;      // of a CTA; twice that where CTAs are few
+constexpr int kGradRows = 2;      // rows of a thread that are loaded together, while those before are computed
+constexpr int kGradMaxCtas = 16;   // CTAs of a cluster: they share an expert's rows
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
 {
@@ -29,13 +29,13 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
 
 // tx: threads side by side (a power of two), ctas: CTAs of a cluster
 template <int KIND, bool GATED>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(2 * kGradThreads)
     linear_grad_kernel(const LinearGradParams p, int tx, int ctas, int blocks)
 {
     extern __shared__ float sums[];   // [GATED + 1][rows at a time][8 tx], then [GATED + 1][8 tx]
     const int rank = static_cast<int>(blockIdx.x) % ctas, unit = static_cast<int>(blockIdx.x) / ctas;
     const int e = unit / blocks, block = unit - e * blocks;
-    const int ty = kGradThreads / tx, my = static_cast<int>(threadIdx.x) / tx, mx = static_cast<int>(threadIdx.x) % tx;
+    const int threads = static_cast<int>(blockDim.x), ty = threads / tx, my = static_cast<int>(threadIdx.x) / tx, mx = static_cast<int>(threadIdx.x) % tx;
     const long long col = (static_cast<long long>(block) * tx + mx) * 8;
     const bool in = col < p.N;
     const long long pitch = static_cast<long long>(p.N) * (GATED ? 2 : 1);
@@ -51,25 +51,35 @@ __global__ void __launch_bounds__(kGradThreads)
     }
     const long long first = lo + (hi - lo) * rank / ctas, end = lo + (hi - lo) * (rank + 1) / ctas;
     float sum[GATED ? 2 : 1][8] = {};
+    struct Rows {
+        uint4 d[kGradRows], g[kGradRows], u[GATED ? kGradRows : 1];
+    };
+    auto load = [&](Rows &v, long long r0) {
+#pragma unroll
+        for (int i = 0; i < kGradRows; ++i) {
+            const long long r = r0 + static_cast<long long>(i) * ty;
+            if (r >= end) break;
+            v.d[i] = ld_global_streamed(reinterpret_cast<const uint4 *>(dc + r * p.N + col));
+            v.g[i] = ld_global_streamed(reinterpret_cast<const uint4 *>(z + r * pitch + col));
+            if constexpr (GATED) v.u[i] = ld_global_streamed(reinterpret_cast<const uint4 *>(z + r * pitch + p.N + col));
+        }
+    };
     with_act(p.act, [&](auto tag) {
         constexpr int A = decltype(tag)::value;
-        for (long long r0 = first + my; in && r0 < end; r0 += static_cast<long long>(ty) * kGradRows) {
-            uint4 d[kGradRows], g[kGradRows], u[kGradRows];
+        const long long step = static_cast<long long>(ty) * kGradRows;
+        Rows v, next;
+        long long r0 = in ? first + my : end;
+        load(v, r0);
+        for (; r0 < end; r0 += step) {
+            load(next, r0 + step);
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
                 const long long r = r0 + static_cast<long long>(i) * ty;
-                if (r >= end) continue;
-                d[i] = ld_global_streamed(reinterpret_cast<const uint4 *>(dc + r * p.N + col));
-                g[i] = ld_global_streamed(reinterpret_cast<const uint4 *>(z + r * pitch + col));
-                if constexpr (GATED) u[i] = ld_global_streamed(reinterpret_cast<const uint4 *>(z + r * pitch + p.N + col));
-            }
-#pragma unroll
-            for (int i = 0; i < kGradRows; ++i) {
-                const long long r = r0 + static_cast<long long>(i) * ty;
-                if (r >= end) continue;
-                const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w}, gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-                uint32_t uw[4] = {}, o[4], o2[4];
-                if constexpr (GATED) uw[0] = u[i].x, uw[1] = u[i].y, uw[2] = u[i].z, uw[3] = u[i].w;
+                if (r >= end) break;
+                const uint32_t dw[4] = {v.d[i].x, v.d[i].y, v.d[i].z, v.d[i].w}, gw[4] = {v.g[i].x, v.g[i].y, v.g[i].z, v.g[i].w};
+                uint32_t o[4];
+                [[maybe_unused]] uint32_t uw[4], o2[4];
+                if constexpr (GATED) uw[0] = v.u[i].x, uw[1] = v.u[i].y, uw[2] = v.u[i].z, uw[3] = v.u[i].w;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float2 c = unpack2<KIND>(dw[q]), x = unpack2<KIND>(gw[q]);
@@ -91,6 +101,7 @@ __global__ void __launch_bounds__(kGradThreads)
                 *reinterpret_cast<uint4 *>(dz + r * pitch + col) = make_uint4(o[0], o[1], o[2], o[3]);
                 if constexpr (GATED) *reinterpret_cast<uint4 *>(dz + r * pitch + p.N + col) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
             }
+            v = next;
         }
     });
     if (!p.dbias) return;
@@ -103,7 +114,7 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
         for (int q = 0; q < 8; ++q) sums[(h * ty + my) * width + mx * 8 + q] = sum[h][q];
     __syncthreads();
-    for (int c = static_cast<int>(threadIdx.x); c < kHalves * width; c += kGradThreads) {
+    for (int c = static_cast<int>(threadIdx.x); c < kHalves * width; c += threads) {
         const float *from = sums + c / width * ty * width + c % width;
         float s = 0.0f;
         for (int y = 0; y < ty; ++y) s += from[y * width];
@@ -111,7 +122,7 @@ __global__ void __launch_bounds__(kGradThreads)
     }
     if (ctas > 1) cluster_sync();
     else __syncthreads();
-    for (int c = static_cast<int>(threadIdx.x) * ctas + rank; c < kHalves * width; c += kGradThreads * ctas) {
+    for (int c = static_cast<int>(threadIdx.x) * ctas + rank; c < kHalves * width; c += threads * ctas) {
         float s = 0.0f;
         for (int k = 0; k < ctas; ++k) s += ctas > 1 ? ld_cluster_f32(mapa(smem_u32(total + c), static_cast<uint32_t>(k))) : total[c];
         const long long at = static_cast<long long>(block) * width + c % width;
@@ -123,16 +134,22 @@ __global__ void __launch_bounds__(kGradThreads)
 template <int KIND, bool GATED>
 cudaError_t go(const LinearGradParams &p, cudaStream_t stream, bool overlap)
 {
-    const int64_t pieces = (p.N + 7) / 8, each = p.rows / p.experts;
-    int tx = 32, ctas = 1;
-    while (tx > 4 && tx / 2 >= pieces) tx /= 2;
-    const auto grid = [&] { return p.experts * ((pieces + tx - 1) / tx) * ctas; };
-    while (grid() < 4 * p.sms && ctas < kGradMaxCtas && each / (2 * ctas) >= kGradThreads / tx * kGradRows) ctas *= 2;
-    while (grid() < 4 * p.sms && ctas == kGradMaxCtas && tx > 8) tx /= 2;
-    if (grid() > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const size_t smem = (GATED ? 2 : 1) * (kGradThreads + tx) * 8 * sizeof(float);
-    return launch_kernel(linear_grad_kernel<KIND, GATED>, dim3(static_cast<unsigned>(grid())), kGradThreads, smem, ctas, stream, overlap, p,
-                         tx, ctas, static_cast<int>((pieces + tx - 1) / tx));
+    // Blocks of 64 columns, and as many CTAs to one as make a single wave (16384 x 8192,
+    // gelu's tanh form: 128 blocks by 4 135 us, by 8 144, by 2 162; blocks of 256 columns
+    // by 8 151).  Clusters need not be whole where nothing is added up.
+    const int64_t pieces = p.N / 8, each = p.rows / p.experts, tx = pieces < 8 ? 4 : 8, blocks = (pieces + tx - 1) / tx;
+    int64_t ctas = 1;
+    while (p.experts * blocks * ctas * 2 <= 4 * p.sms && each >= 128 * ctas && (ctas < kGradMaxCtas || !p.dbias)) ctas *= 2;
+    const int64_t grid = p.experts * blocks * ctas;
+    const int threads = 2 * grid <= 4 * p.sms ? 2 * kGradThreads : kGradThreads;
+    const size_t smem = (GATED ? 2 : 1) * (threads + tx) * 8 * sizeof(float);
+    const auto kernel = linear_grad_kernel<KIND, GATED>;
+    if (p.dbias && ctas > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), threads, smem, p.dbias ? static_cast<int>(ctas) : 1, stream, overlap, p,
+                         static_cast<int>(tx), static_cast<int>(ctas), static_cast<int>(blocks));
 }
 
 }  // namespace
