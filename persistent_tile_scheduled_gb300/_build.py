@@ -32,7 +32,7 @@ BINDING = os.path.join(CSRC, "expert_binding.cpp")
 UNITS = ["gemm_cg1.cu", "gemm_cg2.cu", "gemm_narrow.cu", "gemm_narrow_cg2.cu", "gemm_api.cu", "gemm_noalloc.cu",
          "peak_probe.cu", "expert_fwd.cu", "expert_dgrad.cu", "expert_wgrad.cu", "expert_route.cu", "nibble_f16.cu",
          "nibble_bf16.cu", "nibble_rows_f16.cu", "nibble_rows_bf16.cu", "expert_api.cu", "linear_f16.cu", "linear_bf16.cu",
-         "linear_e4m3.cu", "linear_grad.cu", "route.cu", "expert_layer_f16.cu", "expert_layer_bf16.cu", "layer_api.cu"]
+         "linear_e4m3.cu", "linear_rows.cu", "linear_grad.cu", "route.cu", "expert_layer_f16.cu", "expert_layer_bf16.cu", "layer_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

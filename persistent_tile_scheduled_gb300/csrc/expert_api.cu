@@ -203,6 +203,25 @@ gemm_status_t scale_of(float scale_a, float scale_b, float *scale)
     return GEMM_OK;
 }
 
+// An upper bound of linear_rows.cu's items.
+int64_t rows_items(int64_t rows, int64_t experts, int64_t N, bool gated)
+{
+    return ((rows < experts ? rows : experts) + rows / 8 + 1) * ((N + 15) / (gated ? 8 : 16));
+}
+
+// Whether the product with an epilogue streams its weights into registers.
+bool few_rows(const gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64_t K, bool gated, gemm_dtype_t dtype)
+{
+    // (told which variant of the others to take, or to let a wait run out, it takes one of those)
+    if (!is16(dtype) || h->opts.cta_group != 0 || h->opts.max_clusters != 0 || (h->opts.debug_flags & GEMM_DEBUG_FAULT_SKIP_TMA)) return false;
+    // Up to 8 rows a matrix is read once from memory; of the 9th on a second time, from
+    // L2 (us, this / through shared memory: one row of 4096^2 gated 13.1 / 17.3, 8 13.4 /
+    // 17.5, 9 18.4 / 17.6; 1 of 1024^2 3.1 / 7.6; 16 over 8 experts of 4096^2 38.3 /
+    // 45.3, 40 44.2 / 47.2, 64 50 / 47.7).
+    return K > 0 && rows <= kLinearRowsMax && experts <= kLinearRowsMax && rows <= (experts == 1 ? 8 : 5 * experts)
+           && rows_items(rows, experts, N, gated) <= kIntMax;
+}
+
 }  // namespace
 
 extern "C" {
@@ -340,6 +359,22 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, int64_t rows, int64_t experts, in
     if (C == nullptr || !aligned16(C) || !aligned16(bias) || !aligned16(residual) || !aligned16(Z)) return GEMM_ERR_INVALID_ARG;
     if (K > 0 && (A == nullptr || B == nullptr || !aligned16(A) || !aligned16(B))) return GEMM_ERR_INVALID_ARG;
     if ((st = on_device(h)) != GEMM_OK) return st;
+    if (few_rows(h, rows, experts, N, K, gated, dtype)) {
+        LinearRowsParams p{};
+        p.rows = static_cast<int32_t>(rows);
+        p.experts = static_cast<int32_t>(experts);
+        p.N = static_cast<int32_t>(N);
+        p.K = static_cast<int32_t>(K);
+        p.act = act;
+        p.x = A;
+        p.w = B;
+        p.bias = bias;
+        p.residual = residual;
+        p.offsets = offsets;
+        p.c = C;
+        p.z = Z;
+        return launched(launch_linear_rows(static_cast<int>(dtype), p, h->sm_count, static_cast<cudaStream_t>(stream), overlap(h)));
+    }
     const Epilogue epi{bias, residual, Z, act};
     return run_product(h, EXPERT_FWD, rows, experts, N, K, B, A, offsets, C, dtype, scale, static_cast<cudaStream_t>(stream), &epi);
 }

@@ -79,6 +79,18 @@ ExpertOps linear_ops_bf16(bool gated, int cg, int bn);
 ExpertOps linear_ops_e4m3(bool gated, int cg, int bn);
 constexpr int kLinearChunk = 32;   // output rows per store box with an epilogue
 
+// The same for few rows (linear_rows.cu): fp16 and bf16.
+struct LinearRowsParams {
+    int32_t rows, experts, N, K;
+    int32_t act;                // gemm_act_t
+    const void *x, *w, *bias, *residual;
+    const int32_t *offsets;     // or null (one matrix)
+    void *c, *z;                // z: or null
+};
+constexpr int kLinearRowsMax = 1024;   // rows, and experts: tables in shared memory
+
+cudaError_t launch_linear_rows(int kind, const LinearRowsParams &p, int sms, cudaStream_t stream, bool overlap);
+
 // ---- rows to the experts and back (expert_route.cu) ---------------------------
 
 constexpr int kMaxExpertsSorted = 1024;   // the sort keeps a count per warp and expert in shared memory
