@@ -25,6 +25,9 @@ constexpr float kGeluTanhTwice = 1.5957691f;     // 2 sqrt(2 / pi)
 constexpr float kGeluTanhCube = 0.044715f;
 constexpr float kNormalPeak = 0.39894228f;       // 1 / sqrt(2 pi)
 
+// g = t (kTail[0] + t (kTail[1] + ...))
+__device__ constexpr float kTail[7] = {0.14371697f, 0.14171756f, 0.14001835f, 0.025731557f, 0.18214381f, -0.18064261f, 0.047314238f};
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -45,13 +48,9 @@ __device__ __forceinline__ float normal_exp(float z) { return exp2_fast(-0.5f * 
 __device__ __forceinline__ float normal_tail(float z, float e)
 {
     const float t = rcp_fast(fmaf(0.36f, fabsf(z), 1.0f));
-    float g = 0.047314238f;
-    g = fmaf(g, t, -0.18064261f);
-    g = fmaf(g, t, 0.18214381f);
-    g = fmaf(g, t, 0.025731557f);
-    g = fmaf(g, t, 0.14001835f);
-    g = fmaf(g, t, 0.14171756f);
-    g = fmaf(g, t, 0.14371697f);
+    float g = fmaf(kTail[6], t, kTail[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) g = fmaf(g, t, kTail[i]);
     return g * t * e;
 }
 
@@ -71,29 +70,91 @@ __device__ __forceinline__ float act(float z)
     return z;
 }
 
-// act(z) and its derivative.
-template <int ACT>
-__device__ __forceinline__ float2 act_and_slope(float z)
+// Two values side by side: one instruction computes both (PTX's f32x2 forms).
+struct Pair {
+    unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float x, float y)
 {
-    if constexpr (ACT == ACT_RELU) return make_float2(positive(z), z > 0.0f ? 1.0f : 0.0f);
-    if constexpr (ACT == ACT_RELU2) return make_float2(positive(z) * positive(z), 2.0f * positive(z));
-    if constexpr (ACT == ACT_GELU) {
-        const float e = normal_exp(z), q = normal_tail(z, e), p = z > 0.0f ? 1.0f - q : q;
-        return make_float2(z * p, fmaf(kNormalPeak * z, e, p));
-    }
-    if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ Pair pair(float2 f) { return pair(f.x, f.y); }
+__device__ __forceinline__ Pair both(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 split(Pair p)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b)
+{
+    Pair p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+    return p;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b)
+{
+    Pair p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+    return p;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
+{
+    Pair p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return p;
+}
+template <class F>
+__device__ __forceinline__ Pair each(Pair p, F f)
+{
+    const float2 v = split(p);
+    return pair(f(v.x), f(v.y));
+}
+
+// act(z) and its derivative, of two values.
+template <int ACT>
+__device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
+{
+    if constexpr (ACT == ACT_RELU) {
+        a = each(z, [](float v) { return positive(v); });
+        slope = each(z, [](float v) { return v > 0.0f ? 1.0f : 0.0f; });
+    } else if constexpr (ACT == ACT_RELU2) {
+        const Pair p = each(z, [](float v) { return positive(v); });
+        a = p * p;
+        slope = p + p;
+    } else if constexpr (ACT == ACT_GELU) {
+        // Phi(z) = q below 0, 1 - q above, q = Phi(-|z|) (normal_tail); Phi + z phi(z)
+        const Pair e = each(z * z * both(-0.5f * kLog2E), [](float v) { return exp2_fast(v); });
+        const Pair t = each(fma(both(0.36f), each(z, [](float v) { return fabsf(v); }), both(1.0f)), [](float v) { return rcp_fast(v); });
+        Pair g = fma(both(kTail[6]), t, both(kTail[5]));
+#pragma unroll
+        for (int i = 4; i >= 0; --i) g = fma(g, t, both(kTail[i]));
+        const float2 q = split(g * t * e), v = split(z);
+        const Pair p = pair(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y);
+        a = z * p;
+        slope = fma(z * both(kNormalPeak), e, p);
+    } else if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
         // z s(y), s = 1 / (1 + exp(-y)): s + z s (1 - s) y', with 1 - s = exp(-y) s
-        float y = -kLog2E * z, dy = 1.0f;   // (y: the exponent of 2)
+        Pair y, dy;   // (y: the exponent of 2)
         if constexpr (ACT == ACT_GELU_TANH) {
-            const float z2 = fminf(z * z, 4096.0f);   // (dy stays finite; there the slope is 0 or 1)
-            y = z * fmaf(-kLog2E * kGeluTanhTwice * kGeluTanhCube, z2, -kLog2E * kGeluTanhTwice);
-            dy = fmaf(3.0f * kGeluTanhTwice * kGeluTanhCube, z2, kGeluTanhTwice);
+            const Pair z2 = each(z * z, [](float v) { return fminf(v, 4096.0f); });   // (dy stays finite; there the slope is 0 or 1)
+            y = z * fma(both(-kLog2E * kGeluTanhTwice * kGeluTanhCube), z2, both(-kLog2E * kGeluTanhTwice));
+            dy = z * fma(both(3.0f * kGeluTanhTwice * kGeluTanhCube), z2, both(kGeluTanhTwice));
+        } else {
+            y = z * both(-kLog2E);
+            dy = z;
         }
         // (exp(-y) is kept finite: there s and the slope are 2^-110 and less)
-        const float e = exp2_fast(fminf(y, 110.0f)), s = rcp_fast(1.0f + e);
-        return make_float2(z * s, fmaf(z * dy * s, e * s, s));
+        const Pair e = each(y, [](float v) { return exp2_fast(fminf(v, 110.0f)); });
+        const Pair s = each(e + both(1.0f), [](float v) { return rcp_fast(v); });
+        a = z * s;
+        slope = fma(dy * s, e * s, s);
+    } else {
+        a = z;
+        slope = both(1.0f);
     }
-    return make_float2(z, 1.0f);
 }
 
 // f(std::integral_constant-like tag) with the activation as a constant.

@@ -142,8 +142,21 @@ struct UpSource {
     }
 };
 
+// The chunks of the hidden rows, block by block, that a warp of the down kernel takes.
+struct DownShare {
+    int first, end;
+    __device__ __forceinline__ DownShare(int blocks, int chunks, int warp, int ctas)
+    {
+        const long long all = static_cast<long long>(blocks) * chunks;
+        first = static_cast<int>(all * warp / (ctas * kRowsWarps));
+        end = static_cast<int>(all * (warp + 1) / (ctas * kRowsWarps));
+    }
+};
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <int KIND, bool GATED, int NB, bool SHARED>
-__global__ void __launch_bounds__(kRowsThreads, 2) layer_up_kernel(const LayerParams p, int max_blocks, int kw, int ctas)
+__global__ void __launch_bounds__(kRowsThreads, 2) layer_up_kernel(const LayerParams p, int max_blocks, int kw, int ctas, int down_ctas)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const LayerBlocks<NB> blocks(smem + rows_part_bytes(NB, kw), max_blocks, p.experts, p.tokens * p.top_k);
@@ -153,6 +166,17 @@ __global__ void __launch_bounds__(kRowsThreads, 2) layer_up_kernel(const LayerPa
     blocks.template make<false>(p);
     stream_items<KIND, GATED, NB, SHARED>(UpSource<KIND, GATED, NB>{p, blocks}, static_cast<const uint16_t *>(p.up), p.hidden, p.dim,
                                   reinterpret_cast<float *>(smem), kw, ctas);
+    // While the last CTAs finish and the down kernel starts, memory would idle: what its
+    // warps load first is brought to L2.
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
+    const int row = static_cast<int>(blockIdx.x) / down_ctas * kLayerRows + (lane >> 1), chunks = (p.hidden + 31) / 32;
+    const DownShare share(*blocks.count, chunks, static_cast<int>(blockIdx.x) % down_ctas * kRowsWarps + warp, down_ctas);
+    if (row < p.dim && share.first < share.end) {
+        const int b = share.first / chunks, k = (share.first - b * chunks) * 32 + (lane & 1) * 128;
+        const uint16_t *at = static_cast<const uint16_t *>(p.down) + ((blocks.expert[b] & 0xffffu) * static_cast<long long>(p.dim) + row) * p.hidden;
+        if (k < p.hidden) prefetch_l2(at + k);
+        if (k + 64 < p.hidden) prefetch_l2(at + k + 64);
+    }
 }
 
 // ---- down ----------------------------------------------------------------------
@@ -184,9 +208,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) layer_down_kernel(const Layer
     blocks.template make<true>(p);   // (ids and weights were there before the up kernel began)
 
     const int tiles = (p.dim + kLayerRows - 1) / kLayerRows, chunks = (p.hidden + 31) / 32;
-    const long long all = static_cast<long long>(*blocks.count) * chunks;   // block by block
-    const int first = static_cast<int>(all * (share * kRowsWarps + warp) / (ctas * kRowsWarps));
-    const int end = static_cast<int>(all * (share * kRowsWarps + warp + 1) / (ctas * kRowsWarps));
+    const DownShare mine_of(*blocks.count, chunks, share * kRowsWarps + warp, ctas);
+    const int first = mine_of.first, end = mine_of.end;
     const uint16_t *down = static_cast<const uint16_t *>(p.down), *hs = static_cast<const uint16_t *>(p.hs);
     float *mine = sums + warp * p.tokens * kDownPitch;
 
@@ -329,23 +352,22 @@ cudaError_t launch_layer_of(const LayerParams &p, cudaStream_t stream, bool over
     const int n = p.tokens * p.top_k, blocks = layer_max_blocks(n, p.experts, NB);
     const bool gated = p.act & ACT_GATED;
     const size_t tables = layer_tables<NB>(n, p.experts);
+    // few tiles: CTAs share one's contraction
+    const long long tiles = (p.dim + kLayerRows - 1) / kLayerRows;
+    int down_ctas = 1;
+    while (down_ctas < 8 && tiles * down_ctas * 2 <= 2 * p.sms) down_ctas *= 2;
     if (p.hidden > 0) {
         const int features = gated ? 8 : 16;
         const long long items = static_cast<long long>(blocks) * ((p.hidden + features - 1) / features);
         const int kw = NB == 1 ? rows_kw(items, p.dim, p.sms) : kLayerManyKw, ctas = NB == 1 ? rows_ctas(items, p.dim, p.sms) : 1;
         const auto kernel = ctas > 1 ? (gated ? layer_up_kernel<KIND, true, NB, NB == 1> : layer_up_kernel<KIND, false, NB, NB == 1>)
                                      : (gated ? layer_up_kernel<KIND, true, NB, false> : layer_up_kernel<KIND, false, NB, false>);
-        const cudaError_t e = launch_layer_kernel(kernel, items, ctas,
-                                                  rows_part_bytes(NB, kw) + tables, p, stream, overlap, blocks, kw, ctas);
+        const cudaError_t e = launch_layer_kernel(kernel, items, ctas, rows_part_bytes(NB, kw) + tables, p, stream, overlap, blocks, kw, ctas, down_ctas);
         if (e != cudaSuccess) return e;
     }
-    // few tiles: CTAs share one's contraction
-    const long long tiles = (p.dim + kLayerRows - 1) / kLayerRows;
-    int ctas = 1;
-    while (ctas < 8 && tiles * ctas * 2 <= 2 * p.sms) ctas *= 2;
     // (without an up kernel before it nothing may be read early)
-    return launch_layer_kernel(layer_down_kernel<KIND, NB>, tiles, ctas, kRowsWarps * p.tokens * kDownPitch * 4 + tables, p, stream,
-                               overlap && p.hidden > 0, blocks, ctas);
+    return launch_layer_kernel(layer_down_kernel<KIND, NB>, tiles, down_ctas, kRowsWarps * p.tokens * kDownPitch * 4 + tables, p, stream,
+                               overlap && p.hidden > 0, blocks, down_ctas);
 }
 
 template <int KIND>

@@ -4,9 +4,14 @@
 // One pass over dC and Z.  A thread owns 8 columns (16 bytes) and every TY-th
 // row of its CTA's stretch, so it keeps its columns' sums in registers, in fp32
 // and before dZ is rounded.  The rows of an expert and column block are shared
-// by a cluster of up to 8 CTAs, which add up through distributed shared memory:
-// always in the same order, without atomics and without a workspace (two
-// captured graphs share nothing).
+// by a cluster of CTAs, which add up through distributed shared memory: always
+// in the same order, without atomics and without a workspace (two captured graphs
+// share nothing).
+//
+// The bytes bound it: 16384 rows of 8192 columns, bf16, 805 MB in 134 us, 6.0 TB/s (0.89
+// of the copy bandwidth; relu^2, which computes next to nothing, 133).  Loading the next
+// rows while the last are computed took it there from 162; two values to an instruction
+// (f32x2) keep the arithmetic out of the way.
 #include "activation.cuh"
 #include "launch.cuh"
 #include "layer_launch.h"
@@ -16,7 +21,7 @@ namespace pts {
 
 namespace {
 
-constexpr int kGradThreads = 256;      // of a CTA; twice that where CTAs are few
+constexpr int kGradThreads = 256;      // of a CTA, or twice that
 constexpr int kGradRows = 2;      // rows of a thread that are loaded together, while those before are computed
 constexpr int kGradMaxCtas = 16;   // CTAs of a cluster: they share an expert's rows
 
@@ -50,7 +55,12 @@ __global__ void __launch_bounds__(2 * kGradThreads)
         hi = hi < lo ? lo : (hi > p.rows ? p.rows : hi);
     }
     const long long first = lo + (hi - lo) * rank / ctas, end = lo + (hi - lo) * (rank + 1) / ctas;
-    float sum[GATED ? 2 : 1][8] = {};
+    Pair sum[GATED ? 2 : 1][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        sum[0][q] = both(0.0f);
+        if constexpr (GATED) sum[1][q] = both(0.0f);
+    }
     struct Rows {
         uint4 d[kGradRows], g[kGradRows], u[GATED ? kGradRows : 1];
     };
@@ -82,21 +92,20 @@ __global__ void __launch_bounds__(2 * kGradThreads)
                 if constexpr (GATED) uw[0] = v.u[i].x, uw[1] = v.u[i].y, uw[2] = v.u[i].z, uw[3] = v.u[i].w;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float2 c = unpack2<KIND>(dw[q]), x = unpack2<KIND>(gw[q]);
-                    const float2 s0 = act_and_slope<A>(x.x), s1 = act_and_slope<A>(x.y);
-                    float a = c.x * s0.y, b = c.y * s1.y;
+                    const Pair c = pair(unpack2<KIND>(dw[q]));
+                    Pair value, d;
+                    act_and_slope<A>(pair(unpack2<KIND>(gw[q])), value, d);
+                    d = d * c;
                     if constexpr (GATED) {
-                        const float2 y = unpack2<KIND>(uw[q]);
-                        a *= y.x;
-                        b *= y.y;
-                        const float a2 = c.x * s0.x, b2 = c.y * s1.x;
-                        sum[1][2 * q] += a2;
-                        sum[1][2 * q + 1] += b2;
-                        o2[q] = pack2f<KIND>(a2, b2);
+                        d = d * pair(unpack2<KIND>(uw[q]));
+                        const Pair d2 = value * c;
+                        sum[1][q] = sum[1][q] + d2;
+                        const float2 f2 = split(d2);
+                        o2[q] = pack2f<KIND>(f2.x, f2.y);
                     }
-                    sum[0][2 * q] += a;
-                    sum[0][2 * q + 1] += b;
-                    o[q] = pack2f<KIND>(a, b);
+                    sum[0][q] = sum[0][q] + d;
+                    const float2 f = split(d);
+                    o[q] = pack2f<KIND>(f.x, f.y);
                 }
                 *reinterpret_cast<uint4 *>(dz + r * pitch + col) = make_uint4(o[0], o[1], o[2], o[3]);
                 if constexpr (GATED) *reinterpret_cast<uint4 *>(dz + r * pitch + p.N + col) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
@@ -112,7 +121,7 @@ __global__ void __launch_bounds__(2 * kGradThreads)
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sums[(h * ty + my) * width + mx * 8 + q] = sum[h][q];
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<float2 *>(sums + (h * ty + my) * width + mx * 8 + 2 * q) = split(sum[h][q]);
     __syncthreads();
     for (int c = static_cast<int>(threadIdx.x); c < kHalves * width; c += threads) {
         const float *from = sums + c / width * ty * width + c % width;
@@ -134,14 +143,20 @@ __global__ void __launch_bounds__(2 * kGradThreads)
 template <int KIND, bool GATED>
 cudaError_t go(const LinearGradParams &p, cudaStream_t stream, bool overlap)
 {
-    // Blocks of 64 columns, and as many CTAs to one as make a single wave (16384 x 8192,
-    // gelu's tanh form: 128 blocks by 4 135 us, by 8 144, by 2 162; blocks of 256 columns
-    // by 8 151).  Clusters need not be whole where nothing is added up.
-    const int64_t pieces = p.N / 8, each = p.rows / p.experts, tx = pieces < 8 ? 4 : 8, blocks = (pieces + tx - 1) / tx;
+    // Blocks of 64 columns, and as many CTAs of 512 threads to one as make a single wave,
+    // 8 at most; blocks of 32 where columns are few, then also 16 CTAs of 256 threads; CTAs
+    // of 256 where a wave is full without sharing (us, gelu's tanh form, bf16: 16384 rows of
+    // 8192 128 blocks by 2 133, by 4 of 256 threads 134, by 8 142; of 2048 32 by 8 38.5,
+    // 64 blocks of 32 columns by 4 44; of 1024 32 of 32 by 8 24.5, 16 of 64 by 16 29.7; of
+    // 512 16 of 32 by 16 of 256 threads 17.2, by 8 19.1; 4101 over 16 experts of 2048 gated
+    // 18.4, of 512 threads 23).  Clusters need not be whole where nothing is added up.
+    const int64_t pieces = p.N / 8, each = p.rows / p.experts, tx = p.experts * ((pieces + 7) / 8) * 8 <= p.sms ? 4 : 8;
+    const int64_t blocks = (pieces + tx - 1) / tx, units = p.experts * blocks;
+    int threads = units <= 2 * p.sms ? 2 * kGradThreads : kGradThreads;
     int64_t ctas = 1;
-    while (p.experts * blocks * ctas * 2 <= 4 * p.sms && each >= 128 * ctas && (ctas < kGradMaxCtas || !p.dbias)) ctas *= 2;
-    const int64_t grid = p.experts * blocks * ctas;
-    const int threads = 2 * grid <= 4 * p.sms ? 2 * kGradThreads : kGradThreads;
+    while (units * ctas * 2 <= 2 * p.sms && each >= 128 * ctas && (ctas < 8 || !p.dbias)) ctas *= 2;
+    if (p.dbias && ctas == 8 && units * 16 <= 2 * p.sms && each >= 128 * 8) ctas = kGradMaxCtas, threads = kGradThreads;
+    const int64_t grid = units * ctas;
     const size_t smem = (GATED ? 2 : 1) * (threads + tx) * 8 * sizeof(float);
     const auto kernel = linear_grad_kernel<KIND, GATED>;
     if (p.dbias && ctas > 8) {
