@@ -82,7 +82,7 @@ __device__ __forceinline__ Pair pair(float x, float y)
 }
 __device__ __forceinline__ Pair pair(float2 f) { return pair(f.x, f.y); }
 __device__ __forceinline__ Pair both(float x) { return pair(x, x); }
-__device__ __forceinline__ float2 split(Pair p)
+__device__ __forceinline__ float2 values(Pair p)
 {
     float2 f;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
@@ -109,8 +109,55 @@ __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
 template <class F>
 __device__ __forceinline__ Pair each(Pair p, F f)
 {
-    const float2 v = split(p);
+    const float2 v = values(p);
     return pair(f(v.x), f(v.y));
+}
+
+// 1 / a of two values of 1 to 2^61 by one reciprocal: the unit of approximate functions
+// takes 8 cycles a warp, and bounds an epilogue that needs two of them per value.
+__device__ __forceinline__ Pair rcp_fast(Pair a)
+{
+    const float2 v = values(a);
+    const float r = rcp_fast(v.x * v.y);
+    return both(r) * pair(v.y, v.x);
+}
+
+// exp(-z^2 / 2) and Phi(-|z|)
+__device__ __forceinline__ void normal_tail(Pair z, Pair &e, Pair &q)
+{
+    e = each(z * z * both(-0.5f * kLog2E), [](float v) { return exp2_fast(v); });
+    const Pair t = rcp_fast(fma(both(0.36f), each(z, [](float v) { return fminf(fabsf(v), 16.0f); }), both(1.0f)));
+    Pair g = fma(both(kTail[6]), t, both(kTail[5]));
+#pragma unroll
+    for (int i = 4; i >= 0; --i) g = fma(g, t, both(kTail[i]));
+    q = g * t * e;
+}
+
+// 2^y, y at most 60: 1 + 2^60 is as good as any larger, and two of them have a product
+__device__ __forceinline__ Pair exp2_limited(Pair y)
+{
+    return each(y, [](float v) { return exp2_fast(fminf(v, 60.0f)); });
+}
+
+template <int ACT>
+__device__ __forceinline__ Pair act(Pair z)
+{
+    if constexpr (ACT == ACT_RELU) return each(z, [](float v) { return positive(v); });
+    if constexpr (ACT == ACT_RELU2) {
+        const Pair p = each(z, [](float v) { return positive(v); });
+        return p * p;
+    }
+    if constexpr (ACT == ACT_GELU) {
+        Pair e, q;
+        normal_tail(z, e, q);
+        return fma(each(z, [](float v) { return -fminf(fabsf(v), 16.0f); }), q, each(z, [](float v) { return positive(v); }));
+    }
+    if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
+        Pair y = z * both(-kLog2E);
+        if constexpr (ACT == ACT_GELU_TANH) y = z * fma(both(-kLog2E * kGeluTanhTwice * kGeluTanhCube) * z, z, both(-kLog2E * kGeluTanhTwice));
+        return z * rcp_fast(exp2_limited(y) + both(1.0f));
+    }
+    return z;
 }
 
 // act(z) and its derivative, of two values.
@@ -125,13 +172,10 @@ __device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
         a = p * p;
         slope = p + p;
     } else if constexpr (ACT == ACT_GELU) {
-        // Phi(z) = q below 0, 1 - q above, q = Phi(-|z|) (normal_tail); Phi + z phi(z)
-        const Pair e = each(z * z * both(-0.5f * kLog2E), [](float v) { return exp2_fast(v); });
-        const Pair t = each(fma(both(0.36f), each(z, [](float v) { return fabsf(v); }), both(1.0f)), [](float v) { return rcp_fast(v); });
-        Pair g = fma(both(kTail[6]), t, both(kTail[5]));
-#pragma unroll
-        for (int i = 4; i >= 0; --i) g = fma(g, t, both(kTail[i]));
-        const float2 q = split(g * t * e), v = split(z);
+        // Phi(z) = q below 0, 1 - q above; Phi + z phi(z)
+        Pair e, tail;
+        normal_tail(z, e, tail);
+        const float2 q = values(tail), v = values(z);
         const Pair p = pair(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y);
         a = z * p;
         slope = fma(z * both(kNormalPeak), e, p);
@@ -146,9 +190,7 @@ __device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
             y = z * both(-kLog2E);
             dy = z;
         }
-        // (exp(-y) is kept finite: there s and the slope are 2^-110 and less)
-        const Pair e = each(y, [](float v) { return exp2_fast(fminf(v, 110.0f)); });
-        const Pair s = each(e + both(1.0f), [](float v) { return rcp_fast(v); });
+        const Pair e = exp2_limited(y), s = rcp_fast(e + both(1.0f));
         a = z * s;
         slope = fma(dy * s, e * s, s);
     } else {

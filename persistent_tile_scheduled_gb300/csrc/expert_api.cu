@@ -59,9 +59,10 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
         cg = 1;
         bn = kExpertTileNFew;
     }
+    const int epi_kind = !epi ? EPI_NONE : gated ? EPI_GATED : EPI_LINEAR;
     int stages = kMaxStages;
-    while (stages > 2 && expert_smem_bytes(cg, bn, stages) > h->max_smem_optin) --stages;
-    const int smem = expert_smem_bytes(cg, bn, stages);
+    while (stages > 2 && expert_smem_bytes(cg, bn, stages, epi_kind) > h->max_smem_optin) --stages;
+    const int smem = expert_smem_bytes(cg, bn, stages, epi_kind);
     const int kind = static_cast<int>(dtype);
     const ExpertOps ops = epi                  ? (kind == 0 ? linear_ops_f16 : kind == 1 ? linear_ops_bf16 : linear_ops_e4m3)(gated, cg, bn)
                           : mode == EXPERT_FWD ? expert_ops_fwd(kind, cg, bn)

@@ -78,7 +78,7 @@ template <int EPI>
 using MapsOf = std::conditional_t<EPI == EPI_NONE, ExpertMaps, LinearMaps>;
 
 template <int KIND, int MODE, int CG, int BN, int EPI = EPI_NONE>
-__global__ void __launch_bounds__(expert_threads(MODE), 1)
+__global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
     expert_kernel(const __grid_constant__ MapsOf<EPI> maps, const ExpertParams p)
 {
     // tmW: boxes of 128 features x one k-block (MN-major: 64 features x a stage); tmX: boxes
@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     // (encode_map_gated), so that a lane of the epilogue has both of its sums.
     static_assert(EPI == EPI_NONE || MODE == EXPERT_FWD, "");
     const CUtensorMap &tmW = maps.w, &tmX = maps.x, &tmXs = maps.xs, &tmO = maps.o;
+    constexpr int kEpi = expert_epi_warps(EPI), kScheduler = 2 + kEpi;
     constexpr int kFeatures = EPI == EPI_GATED ? kRowsPerCta / 2 : kRowsPerCta;   // output features of a CTA's tile
     constexpr bool kWmn = MODE != EXPERT_FWD;     // the operand's features are contiguous, the contraction is not
     constexpr bool kXmn = MODE == EXPERT_WGRAD;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
     const uint32_t full0 = bar0;                             // + 8*s
     const uint32_t empty0 = bar0 + 8 * kMaxStages;           // + 8*s
     const uint32_t fix0 = bar0 + 16 * kMaxStages;            // + 8*s (WGRAD; with an epilogue the residual's boxes)
-    const uint32_t acc_full0 = bar0 + 24 * kMaxStages;       // + 8*b
+    const uint32_t acc_full0 = fix0 + 8 * expert_fix_barriers(EPI);   // + 8*b
     const uint32_t acc_empty0 = acc_full0 + 16;              // + 8*b
     const uint32_t ring_full0 = acc_empty0 + 16;             // + 8*r
     const uint32_t ring_empty0 = ring_full0 + 8 * kRing;     // + 8*r
@@ -144,13 +145,13 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             if (MODE == EXPERT_WGRAD) mbar_init(fix0 + 8 * s, 1);
         }
         if (EPI != EPI_NONE)   // (the residual's boxes, two to an epilogue warp)
-            for (int k = 0; k < 2 * kEpiWarps; ++k) mbar_init(fix0 + 8 * k, 1);
+            for (int k = 0; k < 2 * kEpi; ++k) mbar_init(fix0 + 8 * k, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, kEpiWarps * CG);
+            mbar_init(acc_empty0 + 8 * b, kEpi * CG);
         }
         // readers of the ring: every CTA's producer, epilogue (and clearing) warps, the leader's MMA warp
-        constexpr uint32_t readers = 1 + CG * (1 + kEpiWarps + (MODE == EXPERT_WGRAD ? 1 : 0));
+        constexpr uint32_t readers = 1 + CG * (1 + kEpi + (MODE == EXPERT_WGRAD ? 1 : 0));
         for (int r = 0; r < kRing; ++r) {
             mbar_init(ring_full0 + 8 * r, 1);
             mbar_init(ring_empty0 + 8 * r, readers);
@@ -388,26 +389,32 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             if (last_stage >= 0) ctl.drain(empty0 + 8 * last_stage, last_phase, 10000000ull);
         }
         __syncwarp();
-    } else if (warp < 2 + kEpiWarps) {
+    } else if (warp < 2 + kEpi) {
         // ============================== epilogue ===============================
         if constexpr (EPI != EPI_NONE) {
-            // As below, with chunks of 32 rows: a warp's 8 KB are four boxes.  C goes
-            // out through a ring of them, into which the residual's boxes are loaded
-            // ahead, so that each is added in place; Z takes two of the four.
+            // As below, with two warps to every 32 features, which take chunks of 16 rows
+            // in turn: a warp's 4 KB are four boxes.  C goes out through a ring of them,
+            // into which the residual's boxes are loaded ahead, so that each is added in
+            // place; Z takes two of the four.
             constexpr int kF = EPI == EPI_GATED ? 16 : 32;   // output features of a warp
             constexpr uint32_t kRow = 2 * kF, kBox = kLinearChunk * kRow;
-            constexpr uint32_t kSlot = kEpiBufsPerWarp * kEpiBufBytes / 4;
+            constexpr uint32_t kSlot = epi_bytes() / kEpi / 4;
             const uint32_t q = warp & 3u;
-            const uint32_t stage_base = sEpi + (warp - 2) * (kEpiBufsPerWarp * kEpiBufBytes);
+            const int turn = static_cast<int>(warp - 2) / kEpiWarps;   // chunks turn, turn + 2, ...
+            const uint32_t stage_base = sEpi + (warp - 2) * (4 * kSlot);
             const uint32_t res0 = fix0 + 16 * (warp - 2);   // + 8 * (chunk & 1): the residual's box is there
             const bool keep = p.z != nullptr, res = p.residual != nullptr;
             const uint32_t bufs = keep ? 2 : 4;
-            const int lead = static_cast<int>(bufs) / 2;    // chunks that the residual's loads are ahead
+            const int lead = static_cast<int>(bufs) / 2;    // own chunks that the residual's loads are ahead
             // stmatrix: this lane's row and 16 bytes of it (32 features: 8 rows at a time; gated 16)
             const uint32_t st_row = EPI == EPI_GATED ? (lane & 7u) + ((lane >> 4) << 3) : lane & 7u;
             const uint32_t st_chunk = EPI == EPI_GATED ? (lane >> 3) & 1u : lane >> 3;
             auto at = [&](uint32_t buf, uint32_t row, uint32_t chunk) -> uint32_t {   // (the store maps' swizzles)
                 return buf + row * kRow + ((chunk ^ (EPI == EPI_GATED ? (row >> 2) & 1u : (row >> 1) & 3u)) << 4);
+            };
+            auto packed = [&](Pair v) -> uint32_t {
+                const float2 f = values(v);
+                return pack2f<KIND>(f.x, f.y);
             };
             int acc = 0;
             uint32_t acc_phase = 0;
@@ -421,10 +428,10 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                     break;
                 }
                 const bool empty_sum = t.nkb == 0;
-                const int chunks = (t.n_len + kLinearChunk - 1) / kLinearChunk;
+                const int chunks = t.n_len / kLinearChunk;
                 const int f = t.f0 + static_cast<int>(rank) * kFeatures + static_cast<int>(q) * kF;
+                // (what was read and written in a box was before the fence of its store)
                 auto load_residual = [&](int c) {
-                    fence_proxy_async_smem();
                     __syncwarp();
                     if (elect_one()) {
                         const uint32_t bar = res0 + 8 * (loads & 1u);
@@ -436,96 +443,92 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                 };
                 if (res) {
                     bulk_wait_read<1>();
-                    for (int c = 0; c < lead && c < chunks; ++c) load_residual(c);
+                    for (int c = turn; c < turn + 2 * lead && c < chunks; c += 2) load_residual(c);
                 }
                 // a lane's features are f + lane / 4 + 0, 8, 16, 24; gated 0 of both matrices and 8 of both
-                float bias[4] = {};
-                if (p.bias) {
-                    const uint16_t *b = static_cast<const uint16_t *>(p.bias)
-                                        + static_cast<long long>(t.e) * (EPI == EPI_GATED ? 2ll * p.features : p.features);
+                Pair bias[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int ff = f + static_cast<int>(lane >> 2) + 8 * (EPI == EPI_GATED ? k >> 1 : k);
-                        if (ff < p.features) bias[k] = unpack1<KIND>(ld_global(b + ff + (EPI == EPI_GATED && (k & 1) ? p.features : 0)));
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int ff = f + static_cast<int>(lane >> 2) + 8 * (EPI == EPI_GATED ? k >> 1 : k);
+                    float v = 0.0f;
+                    if (p.bias && ff < p.features)
+                        v = unpack1<KIND>(ld_global(static_cast<const uint16_t *>(p.bias) + static_cast<long long>(t.e) * p.features * (EPI == EPI_GATED ? 2 : 1)
+                                                    + ff + (EPI == EPI_GATED && (k & 1) ? p.features : 0)));
+                    bias[k] = both(v);
                 }
                 if (!ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL)) break;
                 tc_fence_after();
                 const uint32_t tbase = tmem_base + ((q * 32u) << 16) + static_cast<uint32_t>(acc * BN);
+                auto release = [&]() {   // (this warp has read its part of the accumulator)
+                    tc_fence_before();
+                    __syncwarp();
+                    if (CG == 2 && !leader)
+                        mbar_arrive_cluster_if(one, mapa(acc_empty0 + 8 * acc, 0u));
+                    else
+                        mbar_arrive_if(one, acc_empty0 + 8 * acc);
+                };
+                if (turn >= chunks) release();
                 bool ok = true;
-                for (int c = 0; c < chunks; ++c) {
-                    uint32_t lo[16], hi[16];
-                    tmem_ld_16x256b_x4(tbase + c * kLinearChunk, lo);
-                    tmem_ld_16x256b_x4(tbase + (16u << 16) + c * kLinearChunk, hi);
+                for (int c = turn; c < chunks; c += 2) {
+                    uint32_t lo[8], hi[8];
+                    tmem_ld_16x256b_x2(tbase + c * kLinearChunk, lo);
+                    tmem_ld_16x256b_x2(tbase + (16u << 16) + c * kLinearChunk, hi);
                     tmem_wait_ld();
-                    if (c + 1 == chunks) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (CG == 2 && !leader)
-                            mbar_arrive_cluster_if(one, mapa(acc_empty0 + 8 * acc, 0u));
-                        else
-                            mbar_arrive_if(one, acc_empty0 + 8 * acc);
-                    }
-                    float x[16], y[16];   // [rows 8j ..][feature 0, 8; y: 16, 24 (gated 0 of both matrices; y: 8)][2 rows]
+                    if (c + 2 >= chunks) release();
+                    Pair x[4], y[4];   // [rows 0, 8][feature 0, 8; y: 16, 24 (gated 0 of both matrices; y: 8)], two rows each
+                    const Pair scale = both(p.out_scale);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        x[j] = fmaf(empty_sum ? 0.0f : __uint_as_float(lo[j]), p.out_scale, bias[(j >> 1) & 1]);
-                        y[j] = fmaf(empty_sum ? 0.0f : __uint_as_float(hi[j]), p.out_scale, bias[2 + ((j >> 1) & 1)]);
+                    for (int j = 0; j < 4; ++j) {
+                        x[j] = pair(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]));
+                        y[j] = pair(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1]));
+                        if (empty_sum) x[j] = y[j] = both(0.0f);
+                        x[j] = fma(x[j], scale, bias[j & 1]);
+                        y[j] = fma(y[j], scale, bias[2 + (j & 1)]);
                     }
                     const uint32_t buf = stage_base + n % bufs * kSlot, zbuf = stage_base + (2 + (n & 1u)) * kSlot;
                     bulk_wait_read<1>();   // the stores that used these boxes have read them
                     __syncwarp();
                     if (keep) {
-                        if constexpr (EPI == EPI_GATED) {
+                        if constexpr (EPI == EPI_GATED) {   // (16 rows of each matrix)
 #pragma unroll
-                            for (int j = 0; j < 16; j += 8)   // 16 rows, of each matrix
-#pragma unroll
-                                for (int k = 0; k < 4; k += 2)
-                                    stmatrix_x4_trans(at(zbuf + k / 2 * kBox, 2 * j + st_row, st_chunk), pack2f<KIND>(x[j + k], x[j + k + 1]),
-                                                      pack2f<KIND>(y[j + k], y[j + k + 1]), pack2f<KIND>(x[j + k + 4], x[j + k + 5]),
-                                                      pack2f<KIND>(y[j + k + 4], y[j + k + 5]));
+                            for (int k = 0; k < 2; ++k)
+                                stmatrix_x4_trans(at(zbuf + k * kBox, st_row, st_chunk), packed(x[k]), packed(y[k]), packed(x[2 + k]), packed(y[2 + k]));
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                stmatrix_x4_trans(at(zbuf, 2 * j + st_row, st_chunk), pack2f<KIND>(x[j], x[j + 1]), pack2f<KIND>(x[j + 2], x[j + 3]),
-                                                  pack2f<KIND>(y[j], y[j + 1]), pack2f<KIND>(y[j + 2], y[j + 3]));
+                            for (int j = 0; j < 4; j += 2)
+                                stmatrix_x4_trans(at(zbuf, 4 * j + st_row, st_chunk), packed(x[j]), packed(x[j + 1]), packed(y[j]), packed(y[j + 1]));
                         }
                     }
                     with_act(p.act, [&](auto tag) {
                         constexpr int A = decltype(tag)::value;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (EPI == EPI_GATED && (j & 2)) continue;
+                        for (int j = 0; j < 4; ++j) {
+                            if (EPI == EPI_GATED && (j & 1)) continue;
                             x[j] = act<A>(x[j]);
                             y[j] = act<A>(y[j]);
-                            if (EPI == EPI_GATED) x[j] *= x[j + 2], y[j] *= y[j + 2];
+                            if (EPI == EPI_GATED) x[j] = x[j] * x[j + 1], y[j] = y[j] * y[j + 1];
                         }
                     });
                     if (res) {
                         ok = ctl.wait_all(res0 + 8 * (n & 1u), (n >> 1) & 1u, WHERE_FULL);
                         if (!ok) break;
-                        if (c + lead < chunks) {
+                        if (c + 2 * lead < chunks) {
                             if (lead == 1) bulk_wait_read<0>();   // (its box is the last chunk's)
-                            load_residual(c + lead);
+                            load_residual(c + 2 * lead);
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; j += EPI == EPI_GATED ? 8 : 4) {
+                    for (int j = 0; j < (EPI == EPI_GATED ? 1 : 4); j += 2) {
                         // four matrices of 8 rows x 8 features
-                        float *v[4] = {x + j, EPI == EPI_GATED ? y + j : x + j + 2, EPI == EPI_GATED ? x + j + 4 : y + j, EPI == EPI_GATED ? y + j + 4 : y + j + 2};
-                        const uint32_t to = at(buf, 2 * j + st_row, st_chunk);
+                        Pair v[4] = {x[j], EPI == EPI_GATED ? y[j] : x[j + 1], EPI == EPI_GATED ? x[j + 2] : y[j], EPI == EPI_GATED ? y[j + 2] : y[j + 1]};
+                        const uint32_t to = at(buf, 4 * j + st_row, st_chunk);
                         if (res) {
                             uint32_t r[4];
                             ldmatrix_x4_trans(to, r[0], r[1], r[2], r[3]);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 a = unpack2<KIND>(r[k]);
-                                v[k][0] += a.x;
-                                v[k][1] += a.y;
-                            }
+                            for (int k = 0; k < 4; ++k) v[k] = v[k] + pair(unpack2<KIND>(r[k]));
                         }
-                        stmatrix_x4_trans(to, pack2f<KIND>(v[0][0], v[0][1]), pack2f<KIND>(v[1][0], v[1][1]), pack2f<KIND>(v[2][0], v[2][1]),
-                                          pack2f<KIND>(v[3][0], v[3][1]));
+                        stmatrix_x4_trans(to, packed(v[0]), packed(v[1]), packed(v[2]), packed(v[3]));
                     }
                     const int row0 = t.row0 + c * kLinearChunk;
                     if (row0 + kLinearChunk <= t.row_end) {
@@ -551,6 +554,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
                             *reinterpret_cast<uint4 *>(z) = ld_shared_v4(at(zbuf, r, ch));
                             if constexpr (EPI == EPI_GATED) *reinterpret_cast<uint4 *>(z + p.features) = ld_shared_v4(at(zbuf + kBox, r, ch));
                         }
+                        fence_proxy_async_smem();
                         __syncwarp();
                     }
                     bulk_commit();
@@ -646,7 +650,7 @@ __global__ void __launch_bounds__(expert_threads(MODE), 1)
             bulk_wait_read<0>();
             __syncwarp();
         }
-    } else if (warp == kSchedWarp) {
+    } else if (warp == kScheduler) {
         // ============================== scheduler ==============================
         // Tile w of all experts' tiles in order, w = cluster, cluster + grid, ...
         if (leader) {
@@ -873,7 +877,7 @@ struct ExpertInst {
     {
         cfg = cudaLaunchConfig_t{};
         cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-        cfg.blockDim = dim3(expert_threads(MODE), 1, 1);
+        cfg.blockDim = dim3(expert_threads(MODE, EPI), 1, 1);
         cfg.dynamicSmemBytes = static_cast<size_t>(smem);
         cfg.stream = stream;
         cfg.attrs = attr;

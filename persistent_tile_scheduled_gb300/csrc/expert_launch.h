@@ -47,15 +47,27 @@ struct LinearMaps : ExpertMaps {
     CUtensorMap r, z;   // residual, Z: boxes as o's
 };
 
-// producer, MMA, 4 epilogue warps, scheduler; WGRAD has a clearing warp too
-__host__ __device__ constexpr int expert_threads(int mode) { return kThreads + (mode == EXPERT_WGRAD ? 32 : 0); }
+// Epilogue warps.  One with activations computes some 25 instructions per element, which
+// 4 warps, one to a scheduler, take too long for (bf16 4096^2, K = 512, gated silu: 42
+// us with 4, 37 with 8).
+__host__ __device__ constexpr int expert_epi_warps(int epi) { return epi == EPI_NONE ? kEpiWarps : 2 * kEpiWarps; }
+
+// producer, MMA, epilogue warps, scheduler; WGRAD has a clearing warp too
+__host__ __device__ constexpr int expert_threads(int mode, int epi = EPI_NONE)
+{
+    return 96 + 32 * expert_epi_warps(epi) + (mode == EXPERT_WGRAD ? 32 : 0);
+}
+static_assert(expert_threads(EXPERT_FWD) == kThreads, "");
+
+// Barriers that only some kernels use: WGRAD's cleared stages, an epilogue's residual.
+__host__ __device__ constexpr int expert_fix_barriers(int epi) { return epi == EPI_NONE ? kMaxStages : 2 * expert_epi_warps(epi); }
 
 // Dynamic shared memory for `stages` stages of a tile of bn rows (plus 1 KB
 // for aligning the base to the swizzle period).
-__host__ __device__ constexpr int expert_smem_bytes(int cg, int bn, int stages)
+__host__ __device__ constexpr int expert_smem_bytes(int cg, int bn, int stages, int epi = EPI_NONE)
 {
     return 1024 + stages * kb_per_stage(cg) * (kRowsPerCta + bn / cg) * kKBlockBytes + epi_bytes()
-           + 8 * (3 * kMaxStages + 4 + 2 * kRing) + 16   // mbarriers, alignment
+           + 8 * (2 * kMaxStages + expert_fix_barriers(epi) + 4 + 2 * kRing) + 16   // mbarriers, alignment
            + 4 * kRingWords * kRing + 16;                // ring payload, TMEM base, abort flag
 }
 
@@ -77,7 +89,7 @@ ExpertOps expert_ops_wgrad(int kind, int cg);
 ExpertOps linear_ops_f16(bool gated, int cg, int bn);
 ExpertOps linear_ops_bf16(bool gated, int cg, int bn);
 ExpertOps linear_ops_e4m3(bool gated, int cg, int bn);
-constexpr int kLinearChunk = 32;   // output rows per store box with an epilogue
+constexpr int kLinearChunk = 16;   // output rows per store box with an epilogue
 
 // The same for few rows (linear_rows.cu): fp16 and bf16.
 struct LinearRowsParams {

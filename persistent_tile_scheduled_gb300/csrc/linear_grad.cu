@@ -100,11 +100,11 @@ __global__ void __launch_bounds__(2 * kGradThreads)
                         d = d * pair(unpack2<KIND>(uw[q]));
                         const Pair d2 = value * c;
                         sum[1][q] = sum[1][q] + d2;
-                        const float2 f2 = split(d2);
+                        const float2 f2 = values(d2);
                         o2[q] = pack2f<KIND>(f2.x, f2.y);
                     }
                     sum[0][q] = sum[0][q] + d;
-                    const float2 f = split(d);
+                    const float2 f = values(d);
                     o[q] = pack2f<KIND>(f.x, f.y);
                 }
                 *reinterpret_cast<uint4 *>(dz + r * pitch + col) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(2 * kGradThreads)
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<float2 *>(sums + (h * ty + my) * width + mx * 8 + 2 * q) = split(sum[h][q]);
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<float2 *>(sums + (h * ty + my) * width + mx * 8 + 2 * q) = values(sum[h][q]);
     __syncthreads();
     for (int c = static_cast<int>(threadIdx.x); c < kHalves * width; c += threads) {
         const float *from = sums + c / width * ty * width + c % width;
