@@ -1,13 +1,16 @@
 """A layer of experts, trained and served with the library's operators.
 
 ExpertLayer holds E pairs of matrices, up (hidden x dim) and down (dim x
-hidden).  Every token goes to top_k of them:
+hidden), and a router's gate (E x dim).  Every token goes to top_k of them:
 
-    forward    sort -> gather -> up product -> relu^2 -> down product -> combine
-    backward   combine's gradient -> down's gradients -> relu^2' -> up's
+    route      the gate's logits -> expert ids and weights
+    forward    sort -> gather -> up product with relu^2 -> down product -> combine
+    backward   combine's gradient -> down's gradients -> relu^2's -> up's
                gradients -> the gather's gradient (combine without weights)
+    route_backward   the weights' gradient -> the logits' -> gate's and the tokens'
     decode     the same forward for a few tokens with both matrices in 4 bits
                (gemm_run_nibble)
+    decode16   the whole layer for a few tokens in two launches (gemm_expert_layer)
 
 Nothing is read back in between: the experts' row counts stay on the device.
 
@@ -47,6 +50,11 @@ class ExpertLayer:
         gen = torch.Generator().manual_seed(seed)
         self.up = (torch.randn(experts, hidden, dim, generator=gen) / dim ** 0.5).to(torch.bfloat16).cuda()
         self.down = (torch.randn(experts, dim, hidden, generator=gen) / hidden ** 0.5).to(torch.bfloat16).cuda()
+        # the router's matrix: products want a multiple of 8 features, so it is filled up with experts that nobody may choose
+        self.routed = -(-experts // 8) * 8
+        self.gate = (torch.randn(1, self.routed, dim, generator=gen) / dim ** 0.5).to(torch.bfloat16).cuda()
+        self.gate_bias = torch.zeros(1, self.routed, dtype=torch.bfloat16, device="cuda")
+        self.gate_bias[0, experts:] = float("-inf")
         self.up4, self.down4 = quantise(self.up, group), quantise(self.down, group)
         self.h = pts.gemm_create(device)
 
@@ -59,35 +67,51 @@ class ExpertLayer:
         pts.gemm_expert_sort(self.h, T, k, E, ids, offsets, row_of, src_of, stream=torch.cuda.current_stream())
         return offsets, row_of
 
+    def route(self, x):
+        """-> ids (T, top_k), weights (T, top_k): softmax over the chosen; and what route_backward needs."""
+        T, k, D, E, s = x.shape[0], self.top_k, self.dim, self.routed, torch.cuda.current_stream()
+        logits, ids, w = _new(T, E), _new(T, k, dtype=torch.int32), _new(T, k, dtype=torch.float32)
+        pts.gemm_run_linear(self.h, T, 1, E, D, x, self.gate, self.gate_bias, None, None, logits, None, pts.GEMM_ACT_NONE, DT, stream=s)
+        pts.gemm_expert_route(self.h, T, k, E, logits, ids, w, pts.GEMM_ROUTE_SELECTED, DT, stream=s)
+        return ids, w, (x, logits, ids)
+
+    def route_backward(self, dw, saved):
+        """-> dx, d(gate) from d(weights)."""
+        x, logits, ids = saved
+        T, k, D, E, s = x.shape[0], self.top_k, self.dim, self.routed, torch.cuda.current_stream()
+        dlogits, dx, dgate = _new(T, E), _new(T, D), torch.empty_like(self.gate)
+        offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")   # (the products' gradients of one matrix)
+        pts.gemm_expert_route_grad(self.h, T, k, E, logits, ids, dw, dlogits, pts.GEMM_ROUTE_SELECTED, DT, stream=s)
+        pts.gemm_run_experts_dgrad(self.h, T, 1, E, D, dlogits, self.gate, offsets, dx, DT, stream=s)
+        pts.gemm_run_experts_wgrad(self.h, T, 1, E, D, dlogits, x, offsets, dgate, DT, stream=s)
+        return dx, dgate
+
     def forward(self, x, ids, weights):
         """x (T, dim) bf16, ids (T, top_k) int32 (outside [0, experts): not this layer's), weights (T, top_k) fp32."""
         T, k, D, H, E, s = x.shape[0], self.top_k, self.dim, self.hidden, self.experts, torch.cuda.current_stream()
         offsets, row_of = self._route(ids)
-        # rows of no expert stay as they are: zeros keep the elementwise steps finite
-        xs, a = torch.zeros(T * k, D, dtype=x.dtype, device="cuda"), torch.zeros(T * k, H, dtype=x.dtype, device="cuda")
-        ys, y = _new(T * k, D), _new(T, D)
+        # (rows of no expert are neither read nor written, so nothing need be in them)
+        xs, a, z, ys, y = _new(T * k, D), _new(T * k, H), _new(T * k, H), _new(T * k, D), _new(T, D)
         pts.gemm_expert_gather(self.h, T, k, D, x, row_of, xs, DT, stream=s)
-        pts.gemm_run_experts(self.h, T * k, E, H, D, xs, self.up, offsets, a, DT, stream=s)
-        r = a.relu()
-        z = r * r
-        pts.gemm_run_experts(self.h, T * k, E, D, H, z, self.down, offsets, ys, DT, stream=s)
+        pts.gemm_run_linear(self.h, T * k, E, H, D, xs, self.up, None, None, offsets, a, z, pts.GEMM_ACT_RELU2, DT, stream=s)
+        pts.gemm_run_experts(self.h, T * k, E, D, H, a, self.down, offsets, ys, DT, stream=s)
         pts.gemm_expert_combine(self.h, T, k, D, ys, row_of, weights, y, DT, stream=s)
-        return y, (x, offsets, row_of, weights, xs, r, z, ys)
+        return y, (x, offsets, row_of, weights, xs, a, z, ys)
 
     def backward(self, dy, saved):
         """-> dx, d(weights), d(up), d(down)."""
-        x, offsets, row_of, weights, xs, r, z, ys = saved
+        x, offsets, row_of, weights, xs, a, z, ys = saved
         T, k, D, H, E, s = x.shape[0], self.top_k, self.dim, self.hidden, self.experts, torch.cuda.current_stream()
         R = T * k
-        dys, dw = torch.zeros_like(ys), torch.empty_like(weights)
-        dz, da, dxs, dx = torch.zeros_like(z), None, _new(R, D), _new(T, D)
+        dys, dw = torch.empty_like(ys), torch.empty_like(weights)
+        da, dz, dxs, dx = torch.empty_like(a), torch.empty_like(z), _new(R, D), _new(T, D)
         dup, ddown = torch.empty_like(self.up), torch.empty_like(self.down)
         pts.gemm_expert_combine_grad(self.h, T, k, D, dy, ys, row_of, weights, dys, dw, DT, stream=s)
-        pts.gemm_run_experts_dgrad(self.h, R, E, D, H, dys, self.down, offsets, dz, DT, stream=s)
-        pts.gemm_run_experts_wgrad(self.h, R, E, D, H, dys, z, offsets, ddown, DT, stream=s)
-        da = 2.0 * r * dz
-        pts.gemm_run_experts_dgrad(self.h, R, E, H, D, da, self.up, offsets, dxs, DT, stream=s)
-        pts.gemm_run_experts_wgrad(self.h, R, E, H, D, da, xs, offsets, dup, DT, stream=s)
+        pts.gemm_run_experts_dgrad(self.h, R, E, D, H, dys, self.down, offsets, da, DT, stream=s)
+        pts.gemm_run_experts_wgrad(self.h, R, E, D, H, dys, a, offsets, ddown, DT, stream=s)
+        pts.gemm_linear_grad(self.h, R, E, H, da, z, offsets, dz, None, pts.GEMM_ACT_RELU2, DT, stream=s)
+        pts.gemm_run_experts_dgrad(self.h, R, E, H, D, dz, self.up, offsets, dxs, DT, stream=s)
+        pts.gemm_run_experts_wgrad(self.h, R, E, H, D, dz, xs, offsets, dup, DT, stream=s)
         pts.gemm_expert_combine(self.h, T, k, D, dxs, row_of, None, dx, DT, stream=s)
         return dx, dw, dup, ddown
 
@@ -104,11 +128,12 @@ class ExpertLayer:
         pts.gemm_expert_combine(self.h, T, k, D, ys, row_of, weights, y, DT, stream=s)
         return y
 
-
-def router(x, gate, top_k):
-    """Expert ids and weights of the top_k largest scores, softmax over those."""
-    v, ids = torch.topk(x.float() @ gate, top_k, dim=1)
-    return ids.to(torch.int32).contiguous(), torch.softmax(v, dim=1).contiguous()
+    def decode16(self, x, ids, weights):
+        """forward for a few tokens (at most pts.gemm.GEMM_EXPERT_LAYER_MAX_TOKENS) in two launches."""
+        T, k, D, H, E, s = x.shape[0], self.top_k, self.dim, self.hidden, self.experts, torch.cuda.current_stream()
+        hs, y = _new(T * k, H), _new(T, D)
+        pts.gemm_expert_layer(self.h, T, k, E, D, H, x, ids, weights, self.up, None, self.down, None, None, hs, y, pts.GEMM_ACT_RELU2, DT, stream=s)
+        return y
 
 
 def main():
@@ -122,7 +147,6 @@ def main():
     a = ap.parse_args()
     layer = ExpertLayer(a.dim, a.hidden, a.experts, a.top_k)
     gen = torch.Generator().manual_seed(1)
-    gate = torch.randn(a.dim, a.experts, generator=gen).cuda() / a.dim ** 0.5
 
     def timed(what, f, flops):
         f()
@@ -136,15 +160,19 @@ def main():
         print(f"{what:10} {us:9.1f} us  {flops / us / 1e6:8.1f} TFLOP/s")
 
     x = torch.randn(a.tokens, a.dim, generator=gen).to(torch.bfloat16).cuda()
-    ids, w = router(x, gate, a.top_k)
+    ids, w, routed = layer.route(x)
     per_pass = 4.0 * a.tokens * a.top_k * a.dim * a.hidden
     y, saved = layer.forward(x, ids, w)
     timed("forward", lambda: layer.forward(x, ids, w), per_pass)
     timed("backward", lambda: layer.backward(y, saved), 2 * per_pass)
+    dw = layer.backward(y, saved)[1]
+    timed("route", lambda: (layer.route(x), layer.route_backward(dw, routed)), 6.0 * a.tokens * a.dim * layer.routed)
     xd = x[:a.decode_tokens].contiguous()
-    idd, wd = router(xd, gate, a.top_k)
+    idd, wd, _ = layer.route(xd)
     timed("decode", lambda: layer.decode(xd, idd, wd), 4.0 * a.decode_tokens * a.top_k * a.dim * a.hidden)
-    y4 = layer.decode(xd, idd, wd).float()
+    timed("decode16", lambda: layer.decode16(xd, idd, wd), 4.0 * a.decode_tokens * a.top_k * a.dim * a.hidden)
+    y16, y4 = layer.decode16(xd, idd, wd).float(), layer.decode(xd, idd, wd).float()
+    print(f"decode in two launches against forward: {float((y16 - y[:a.decode_tokens].float()).norm() / y16.norm()):.4f} of the norm")
     print(f"decode in 4 bits against bf16: {float((y4 - y[:a.decode_tokens].float()).norm() / y4.norm()):.3f} of the norm")
     status, word = pts.gemm_check(layer.h)
     layer.close()
