@@ -1,17 +1,21 @@
 // A router's choice: each token's top_k experts and their weights, and the
 // gradient of its logits.
 //
-// A warp per token; lane l holds the logits of experts PER l .. PER l + PER - 1 in
-// registers, loaded together where rows allow it.  The top_k are taken one by one:
-// the largest key of the warp (redux.sync on unsigned keys that order like the
-// values).  The key of a 16-bit logit holds its expert too, the lower first, so one
-// reduction finds both; of fp32 logits the lowest lane that has the largest.  Lane
-// j keeps the j-th choice, so the softmax over the chosen is a sum over lanes.  The
-// gradient brings dweights to the lanes that own their logits through shared memory.
+// G lanes per token (8, 16 or a warp), lane l of them with the logits of experts PER l ..
+// PER l + PER - 1 in registers, loaded together (where rows do not allow it, of experts l,
+// l + G, ..., one by one).  The key of a 16-bit logit, unsigned and in the order of the
+// values, holds its expert too, the lower first.  A lane sorts its keys; then the top_k
+// are taken one by one, each the largest of the lanes' first, which its lane pops.  fp32
+// logits, and more than 8 choices, take a warp per token and redux.sync, and the lowest
+// expert that has the largest.  Lane j keeps the j-th choice, so the softmax over the
+// chosen is a sum over lanes.  The gradient brings dweights to the lanes that own their
+// logits through shared memory.
 //
-// Instructions bound it, 320 a token (an integer one takes a scheduler two cycles):
-// 16384 tokens, 8 of 128 experts, bf16 (4 MB in, 1 MB out), 6.4 us and 5.9 back; 16
-// tokens 1.5, a launch.
+// Instructions bound it, and fetching them: every warp runs through the code once.
+// 16384 tokens, 8 of 128 experts, bf16 (4 MB in, 1 MB out): 5.5 us, and 4.1 back (16
+// lanes per token; 8 lanes of 16 logits 6.2 and 4.2, a warp 6.9 and 6.2; merging sorted
+// lists of 8 across the lanes instead of taking choices one by one 6.9).  16 tokens 1.2,
+// a launch.
 #include "activation.cuh"
 #include "launch.cuh"
 #include "layer_launch.h"
@@ -25,28 +29,21 @@ enum : int { ROUTE_SELECTED = 0, ROUTE_ALL = 1, ROUTE_SIGMOID = 2 };
 
 constexpr int kRouteWarps = 4;
 constexpr float kMaxFinite = 3.402823466e38f;
+#define kNothing __int_as_float(0xFF800000)   // -infinity
 constexpr uint32_t kIndex = 0x1FFFu;   // of a 16-bit logit's fp32 bits the lowest 13 are 0: they hold the expert
 
-// Unsigned keys in the order of the values, 0 where there is nothing to choose
-// (-infinity, NaN).  -0 and 0 are one value, +infinity is the largest finite one.
-__device__ __forceinline__ uint32_t ordered(float v)   // v: finite
-{
-    const uint32_t b = __float_as_uint(v);
-    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
+// Unsigned keys in the order of the values.  -0 and 0 are one value, +infinity is the
+// largest finite one; what cannot be chosen (-infinity, NaN) is below kLeast.
+constexpr uint32_t kLeast = 0x00800000u;   // the key of the lowest finite value
 
-__device__ __forceinline__ float unordered(uint32_t key)
-{
-    return __uint_as_float(key ^ (static_cast<uint32_t>(~static_cast<int32_t>(key) >> 31) | 0x80000000u));
-}
+__device__ __forceinline__ float cleaned(float v) { return fminf(fmaxf(v, kNothing), kMaxFinite); }   // (NaN: -infinity)
 
 template <int KIND>
-__device__ __forceinline__ uint32_t key_of(float v, int e)
+__device__ __forceinline__ uint32_t key_of(float v, int e)   // v: cleaned
 {
-    const bool there = v >= -kMaxFinite;
-    if constexpr (KIND == 3) return there ? ordered(fminf(v, kMaxFinite) + 0.0f) : 0u;
-    constexpr float kMost = 3.40261e38f;   // (above both types' finite values; its lowest 13 bits are cleared)
-    return there ? (ordered(fminf(v, kMost) + 0.0f) & ~kIndex) | (kIndex - static_cast<uint32_t>(e)) : 0u;
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+    return KIND == 3 ? key : (key & ~kIndex) | (kIndex - static_cast<uint32_t>(e));
 }
 
 template <int KIND>
@@ -54,56 +51,55 @@ __device__ __forceinline__ float value_of(uint32_t key)
 {
     // (of a negative value the key's bits are the complement: the expert's place is filled with ones)
     if constexpr (KIND != 3) key = key & 0x80000000u ? key & ~kIndex : key | kIndex;
-    return unordered(key);
+    return __uint_as_float(key ^ (static_cast<uint32_t>(~static_cast<int32_t>(key) >> 31) | 0x80000000u));
 }
 
-__device__ __forceinline__ float warp_sum(float v)
+// A lane's i-th expert.
+template <int PER, int G, bool WHOLE>
+__device__ __forceinline__ int expert_of(int sub, int i)
 {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    return v;
+    return WHOLE ? sub * PER + i : sub + G * i;
 }
 
-// A lane's PER logits of a row as keys; `whole`: rows are a multiple of PER long and
-// aligned to PER logits.
-template <int KIND, int PER>
-__device__ __forceinline__ void load_keys(uint32_t (&key)[PER], const void *logits, long long row, int experts, bool whole)
+// A lane's PER logits of a row, cleaned (-infinity behind the last).  WHOLE: rows are a
+// multiple of PER long and aligned to PER logits.
+template <int KIND, int PER, int G, bool WHOLE>
+__device__ __forceinline__ void load_logits(float (&x)[PER], const void *logits, long long row, int sub, int experts)
 {
-    const int e0 = static_cast<int>(lane_id()) * PER;
     constexpr int kBytes = PER * (KIND == 3 ? 4 : 2);
-    if (whole) {
+    if constexpr (WHOLE) {
+        const int e0 = sub * PER;
         uint32_t v[(kBytes + 3) / 4] = {};
-        if (e0 < experts) {
-            const uint8_t *at = static_cast<const uint8_t *>(logits) + (row + e0) * (KIND == 3 ? 4 : 2);
-            if constexpr (kBytes == 2) v[0] = ld_global(reinterpret_cast<const uint16_t *>(at));
-            if constexpr (kBytes == 4) v[0] = ld_global(reinterpret_cast<const uint32_t *>(at));
-            if constexpr (kBytes == 8) {
-                const uint2 q = ld_global(reinterpret_cast<const uint2 *>(at));
-                v[0] = q.x, v[1] = q.y;
-            }
-            if constexpr (kBytes >= 16) {
+        const uint8_t *at = static_cast<const uint8_t *>(logits) + (row + (e0 < experts ? e0 : 0)) * (KIND == 3 ? 4 : 2);
+        if constexpr (kBytes == 2) v[0] = ld_global(reinterpret_cast<const uint16_t *>(at));
+        if constexpr (kBytes == 4) v[0] = ld_global(reinterpret_cast<const uint32_t *>(at));
+        if constexpr (kBytes == 8) {
+            const uint2 q = ld_global(reinterpret_cast<const uint2 *>(at));
+            v[0] = q.x, v[1] = q.y;
+        }
+        if constexpr (kBytes >= 16) {
 #pragma unroll
-                for (int i = 0; i < kBytes / 16; ++i) {
-                    const uint4 q = ld_global(reinterpret_cast<const uint4 *>(at) + i);
-                    v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-                }
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 q = ld_global(reinterpret_cast<const uint4 *>(at) + i);
+                v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
             }
         }
+        const float most = e0 < experts ? kMaxFinite : kNothing;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            float x;
-            if constexpr (KIND == 3) x = __uint_as_float(v[i]);
-            else x = i % 2 ? unpack2<KIND>(v[i / 2]).y : unpack2<KIND>(v[i / 2]).x;
-            key[i] = key_of<KIND>(x, e0 + i);
-            if (e0 >= experts) key[i] = 0u;
+            if constexpr (KIND == 3) x[i] = __uint_as_float(v[i]);
+            else x[i] = i % 2 ? unpack2<KIND>(v[i / 2]).y : unpack2<KIND>(v[i / 2]).x;
+            x[i] = fminf(fmaxf(x[i], kNothing), most);   // (cleaned)
         }
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            key[i] = 0u;
-            if (e0 + i >= experts) continue;
-            if constexpr (KIND == 3) key[i] = key_of<KIND>(ld_global(static_cast<const float *>(logits) + row + e0 + i), e0 + i);
-            else key[i] = key_of<KIND>(unpack1<KIND>(ld_global(static_cast<const uint16_t *>(logits) + row + e0 + i)), e0 + i);
+            const int e = sub + G * i;
+            x[i] = kNothing;
+            if (e >= experts) continue;
+            if constexpr (KIND == 3) x[i] = ld_global(static_cast<const float *>(logits) + row + e);
+            else x[i] = unpack1<KIND>(ld_global(static_cast<const uint16_t *>(logits) + row + e));
+            x[i] = cleaned(x[i]);
         }
     }
 }
@@ -118,226 +114,260 @@ __device__ __forceinline__ float share_of(float l, float best, int mode)
     return exp_fast(fminf(l, 0.0f) - fminf(best, 0.0f)) * rcp_fast(1.0f + exp_fast(-fabsf(l)));
 }
 
+// The sum of exp(x - best) of a lane.
+template <int PER>
+__device__ __forceinline__ float exp_sum(const float (&x)[PER], float best)
+{
+    best = fmaxf(best, -kMaxFinite);   // (a row of nothing: 0)
+    float all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) all += exp_fast(x[i] - best);
+    return all;
+}
+
 __device__ __forceinline__ void order(uint32_t &a, uint32_t &b)
 {
     const uint32_t hi = max(a, b), lo = min(a, b);
     a = hi, b = lo;
 }
 
-// PER: logits per lane, TOKENS: tokens of a warp
-template <int KIND, int PER, int TOKENS>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p, bool whole)
+// Sums and maxima over the G lanes of a token.
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+#pragma unroll
+    for (int s = 1; s < G; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+    return v;
+}
+
+template <int G, class T>
+__device__ __forceinline__ T lanes_max(T v)
+{
+#pragma unroll
+    for (int s = 1; s < G; s <<= 1) {
+        const T o = __shfl_xor_sync(0xffffffffu, v, s);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// Descending (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&a)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(a[i + j], a[i + j + k]);
+}
+
+// The choice's weight, and the stores, of lane j < top_k of a token.
+__device__ __forceinline__ void write_choice(const RouteParams &p, long long t, int j, bool there, int id, float w, float all)
+{
+    p.ids[t * p.top_k + j] = there ? id : -1;
+    p.weights[t * p.top_k + j] = there ? w * rcp_fast(all) : 0.0f;
+}
+
+// 16-bit logits, top_k <= 8: G lanes per token
+template <int KIND, int PER, int G, bool WHOLE>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(const RouteParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int sub = static_cast<int>(lane_id()) % G;
+    const long long t = (static_cast<long long>(blockIdx.x) * (32 * kRouteWarps) + threadIdx.x) / G;
+    float x[PER];
+    uint32_t key[PER];
+    // (behind the last token: the last again, not written)
+    load_logits<KIND, PER, G, WHOLE>(x, p.logits, (t < p.tokens ? t : p.tokens - 1) * p.experts, sub, p.experts);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key_of<KIND>(x[i], expert_of<PER, G, WHOLE>(sub, i));
+    sort_keys(key);
+    const float best = fminf(value_of<KIND>(lanes_max<G>(key[0])), kMaxFinite);
+    float all = p.mode == ROUTE_ALL ? lanes_sum<G>(exp_sum(x, best)) : 0.0f;
+    constexpr int kKeep = PER < 8 ? PER : 8;   // (a lane has 8 choices at most)
+    uint32_t mine = 0u;                        // this lane's choice
+#pragma unroll 1
+    for (int j = 0; j < p.top_k; ++j) {
+        const uint32_t top = lanes_max<G>(key[0]);   // (below kLeast where nothing is left)
+        if (sub == j) mine = top;
+        if (key[0] == top) {
+#pragma unroll
+            for (int i = 0; i + 1 < kKeep; ++i) key[i] = key[i + 1];
+            key[kKeep - 1] = 0u;
+        }
+    }
+    const float w = mine >= kLeast ? share_of(fminf(value_of<KIND>(mine), kMaxFinite), best, p.mode) : 0.0f;
+    if (p.mode != ROUTE_ALL) all = lanes_sum<G>(w);
+    if (sub < p.top_k && t < p.tokens) write_choice(p, t, sub, mine >= kLeast, static_cast<int>(kIndex - (mine & kIndex)), w, all);
+}
+
+// A warp per token, PER logits per lane.
+template <int KIND, int PER, bool WHOLE>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int lane = static_cast<int>(lane_id());
-    const long long first = (static_cast<long long>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5)) * TOKENS;
-    uint32_t key[TOKENS][PER];
-    float best[TOKENS], all[TOKENS];
+    const long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    if (t >= p.tokens) return;
+    uint32_t key[PER], most = 0u;
+    float x[PER];
+    load_logits<KIND, PER, 32, WHOLE>(x, p.logits, t * p.experts, lane, p.experts);
 #pragma unroll
-    for (int q = 0; q < TOKENS; ++q)   // (behind the last token: the last again, not written)
-        load_keys<KIND, PER>(key[q], p.logits, (first + q < p.tokens ? first + q : p.tokens - 1) * p.experts, p.experts, whole);
-    if (p.mode == ROUTE_ALL) {
-#pragma unroll
-        for (int q = 0; q < TOKENS; ++q) {
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) m = max(m, key[q][i]);
-            best[q] = value_of<KIND>(__reduce_max_sync(0xffffffffu, m));
-            all[q] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) all[q] += key[q][i] ? exp_fast(value_of<KIND>(key[q][i]) - best[q]) : 0.0f;
-            all[q] = warp_sum(all[q]);
-        }
+    for (int i = 0; i < PER; ++i) {
+        key[i] = key_of<KIND>(x[i], expert_of<PER, 32, WHOLE>(lane, i));
+        most = max(most, key[i]);
     }
-    uint32_t mine[TOKENS];   // this lane's choice
-    int mine_id[TOKENS];
-    // (the keys of a lane in descending order: the largest is the first, and is popped)
-    constexpr bool kSorted = KIND != 3 && PER <= 4;
-#pragma unroll
-    for (int q = 0; q < TOKENS; ++q) {
-        mine[q] = 0u, mine_id[q] = -1;
-        if constexpr (kSorted && PER >= 2) {
-            order(key[q][0], key[q][1]);
-            if constexpr (PER == 4) {
-                order(key[q][2], key[q][3]);
-                order(key[q][0], key[q][2]);
-                order(key[q][1], key[q][3]);
-                order(key[q][1], key[q][2]);
-            }
-        }
-    }
+    const float best = fminf(value_of<KIND>(__reduce_max_sync(0xffffffffu, most)), kMaxFinite);
+    float all = p.mode == ROUTE_ALL ? lanes_sum<32>(exp_sum(x, best)) : 0.0f;
+    uint32_t mine = 0u;   // this lane's choice
+    int mine_id = -1;
     for (int j = 0; j < p.top_k; ++j) {
+        uint32_t m = 0u;
 #pragma unroll
-        for (int q = 0; q < TOKENS; ++q) {
-            uint32_t m = key[q][0];
-            if constexpr (!kSorted) {
+        for (int i = 0; i < PER; ++i) m = max(m, key[i]);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, m);
+        if (top < kLeast) break;
+        // the lowest expert that has it
+        uint32_t e = 0xffffffffu;
 #pragma unroll
-                for (int i = 1; i < PER; ++i) m = max(m, key[q][i]);
-            }
-            const uint32_t top = __reduce_max_sync(0xffffffffu, m);   // (0: nothing is left, and mine stays 0)
-            if (lane == j) mine[q] = top;
-            if constexpr (KIND == 3) {
-                const int owner = __ffs(__ballot_sync(0xffffffffu, m == top)) - 1;
-                int at = 0;
-                bool taken = lane != owner;
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] == top) e = static_cast<uint32_t>(expert_of<PER, 32, WHOLE>(lane, i));
+        const int id = static_cast<int>(__reduce_min_sync(0xffffffffu, e));
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (!taken && key[q][i] == top) key[q][i] = 0u, at = i, taken = true;
-                const int id = __shfl_sync(0xffffffffu, lane * PER + at, owner);
-                if (lane == j) mine_id[q] = id;
-            } else if constexpr (kSorted) {
-                if (m == top) {
-#pragma unroll
-                    for (int i = 0; i + 1 < PER; ++i) key[q][i] = key[q][i + 1];
-                    key[q][PER - 1] = 0u;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (key[q][i] == top) key[q][i] = 0u;
-            }
-        }
+        for (int i = 0; i < PER; ++i)
+            if (expert_of<PER, 32, WHOLE>(lane, i) == id) key[i] = 0u;
+        if (lane == j) mine = top, mine_id = id;
     }
-#pragma unroll
-    for (int q = 0; q < TOKENS; ++q) {
-        if (KIND != 3) mine_id[q] = static_cast<int>(kIndex - (mine[q] & kIndex));
-        const float l = value_of<KIND>(mine[q]);
-        if (p.mode != ROUTE_ALL) best[q] = __shfl_sync(0xffffffffu, l, 0);
-        const float w = mine[q] ? share_of(l, best[q], p.mode) : 0.0f;
-        if (p.mode != ROUTE_ALL) all[q] = warp_sum(w);
-        if (lane < p.top_k && first + q < p.tokens) {
-            p.ids[(first + q) * p.top_k + lane] = mine[q] ? mine_id[q] : -1;
-            p.weights[(first + q) * p.top_k + lane] = mine[q] ? __fdividef(w, all[q]) : 0.0f;
-        }
-    }
+    const float w = mine ? share_of(fminf(value_of<KIND>(mine), kMaxFinite), best, p.mode) : 0.0f;
+    if (p.mode != ROUTE_ALL) all = lanes_sum<32>(w);
+    if (lane < p.top_k) write_choice(p, t, lane, mine != 0u, mine_id, w, all);
 }
 
 // With w = softmax of the scores over the chosen (ALL: over all experts):
 // dl_i = w_i (dw_i - sum_j w_j dw_j) u'(l_i), dw = 0 where nothing was chosen.
-template <int KIND, int PER, int TOKENS>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const RouteParams p, bool whole)
+template <int KIND, int PER, int G, bool WHOLE>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const RouteParams p)
 {
-    __shared__ __align__(16) float gradient[kRouteWarps][TOKENS][32 * PER];   // dweights by expert
-    __shared__ uint32_t chosen[kRouteWarps][TOKENS][32];                      // by lane, a bit per logit of it
+    constexpr int kTokens = 32 * kRouteWarps / G;   // of a CTA
+    __shared__ __align__(16) float gradient[kTokens][G * PER];   // dweights by expert
+    __shared__ uint32_t chosen[kTokens][G];                      // by lane, a bit per logit of it
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x >> 5);
-    const long long first = (static_cast<long long>(blockIdx.x) * kRouteWarps + warp) * TOKENS;
-    uint32_t key[TOKENS][PER];
-    int id[TOKENS];
-    float d[TOKENS];
-#pragma unroll
-    for (int q = 0; q < TOKENS; ++q) {
-        const bool there = first + q < p.tokens;
-        load_keys<KIND, PER>(key[q], p.logits, (there ? first + q : p.tokens - 1) * p.experts, p.experts, whole);
-        id[q] = -1, d[q] = 0.0f;
-        if (there && lane < p.top_k) {
-            id[q] = ld_global(p.ids + (first + q) * p.top_k + lane);
-            d[q] = ld_global(p.dweights + (first + q) * p.top_k + lane);
+    const int sub = static_cast<int>(lane_id()) % G, mine = static_cast<int>(threadIdx.x) / G;
+    const long long t = static_cast<long long>(blockIdx.x) * kTokens + mine;
+    const bool there = t < p.tokens;
+    float x[PER];
+    load_logits<KIND, PER, G, WHOLE>(x, p.logits, (there ? t : p.tokens - 1) * p.experts, sub, p.experts);
+    chosen[mine][sub] = 0u;
+    __syncwarp();
+    // (a token's ids differ; were one there twice, its dweights would add up)
+    for (int j0 = 0; j0 < p.top_k; j0 += G) {
+        int id = -1;
+        float d = 0.0f;
+        if (there && j0 + sub < p.top_k) {
+            id = ld_global(p.ids + t * p.top_k + j0 + sub);
+            d = ld_global(p.dweights + t * p.top_k + j0 + sub);
         }
-        chosen[warp][q][lane] = 0u;
+        const bool counts = id >= 0 && id < p.experts;
+        const int lane = WHOLE ? id / PER : id % G, place = WHOLE ? id % PER : id / G;
+        const uint32_t bit = counts ? 1u << place : 0u;
+        const bool again = counts && (atomicOr(&chosen[mine][lane], bit) & bit);
+        if (counts && !again) gradient[mine][lane * PER + place] = d;
+        __syncwarp();
+        if (again) atomicAdd(&gradient[mine][lane * PER + place], d);
+        __syncwarp();
     }
-    __syncwarp();
-    bool again[TOKENS];   // (a token's ids differ; were one there twice, its dweights would add up)
+    const uint32_t in = chosen[mine][sub], counted = p.mode == ROUTE_ALL ? 0xffffffffu : in;
+    float g[PER], best = kNothing;
 #pragma unroll
-    for (int q = 0; q < TOKENS; ++q) {
-        again[q] = false;
-        if (id[q] < 0 || id[q] >= p.experts) continue;
-        const uint32_t bit = 1u << (id[q] % PER);
-        again[q] = atomicOr(&chosen[warp][q][id[q] / PER], bit) & bit;
-        if (!again[q]) gradient[warp][q][id[q]] = d[q];
+    for (int i = 0; i < PER; ++i) {
+        if (!(counted >> i & 1u)) x[i] = kNothing;
+        best = fmaxf(best, x[i]);
+        g[i] = (in >> i & 1u) && x[i] > kNothing ? gradient[mine][sub * PER + i] : 0.0f;
     }
-    __syncwarp();
+    best = fmaxf(lanes_max<G>(best), -kMaxFinite);
+    float all = 0.0f, inner = 0.0f, w[PER];
 #pragma unroll
-    for (int q = 0; q < TOKENS; ++q)
-        if (again[q]) atomicAdd(&gradient[warp][q][id[q]], d[q]);
-    __syncwarp();
+    for (int i = 0; i < PER; ++i) {
+        w[i] = share_of(x[i], best, p.mode);   // (0 of -infinity)
+        all += w[i];
+        inner = fmaf(w[i], g[i], inner);
+    }
+    all = lanes_sum<G>(all);
+    const float scale = all > 0.0f ? rcp_fast(all) : 0.0f;
+    inner = lanes_sum<G>(inner) * scale;
 #pragma unroll
-    for (int q = 0; q < TOKENS; ++q) {
-        const uint32_t in = chosen[warp][q][lane];
-        float w[PER], g[PER];
-        uint32_t m = 0u;
+    for (int i = 0; i < PER; ++i) {
+        w[i] = w[i] * scale * (g[i] - inner);
+        if (p.mode == ROUTE_SIGMOID) w[i] *= rcp_fast(1.0f + exp_fast(x[i]));
+    }
+    if (!there) return;
+    const int e0 = sub * PER;
+    const long long at = t * p.experts + (WHOLE ? e0 : sub);
+    if constexpr (KIND == 3) {
+        float *out = static_cast<float *>(p.dlogits) + at;
+        if constexpr (WHOLE && PER >= 4) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (p.mode != ROUTE_ALL && !(in >> i & 1u)) key[q][i] = 0u;   // (those that do not count)
-            g[i] = key[q][i] && (in >> i & 1u) ? gradient[warp][q][lane * PER + i] : 0.0f;
-            m = max(m, key[q][i]);
-        }
-        const float best = value_of<KIND>(__reduce_max_sync(0xffffffffu, m));
-        float all = 0.0f, inner = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            w[i] = key[q][i] ? share_of(value_of<KIND>(key[q][i]), best, p.mode) : 0.0f;
-            all += w[i];
-            inner = fmaf(w[i], g[i], inner);
-        }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) {
-            all += __shfl_xor_sync(0xffffffffu, all, s);
-            inner += __shfl_xor_sync(0xffffffffu, inner, s);
-        }
-        const float scale = all > 0.0f ? __fdividef(1.0f, all) : 0.0f;
-        inner *= scale;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            w[i] = w[i] * scale * (g[i] - inner);
-            if (p.mode == ROUTE_SIGMOID && key[q][i]) w[i] *= rcp_fast(1.0f + exp_fast(value_of<KIND>(key[q][i])));
-        }
-        const int e0 = lane * PER;
-        if (first + q >= p.tokens || e0 >= p.experts) continue;
-        const long long at = (first + q) * p.experts + e0;
-        if constexpr (KIND == 3) {
-            float *out = static_cast<float *>(p.dlogits) + at;
-            if (whole && PER >= 4) {
-#pragma unroll
-                for (int i = 0; i < PER / 4; ++i) reinterpret_cast<float4 *>(out)[i] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (e0 + i < p.experts) out[i] = w[i];
-            }
+            for (int i = 0; i < PER / 4; ++i)
+                if (e0 < p.experts) reinterpret_cast<float4 *>(out)[i] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         } else {
-            uint16_t *out = static_cast<uint16_t *>(p.dlogits) + at;
-            if (whole && PER >= 4) {
 #pragma unroll
-                for (int i = 0; i < PER / 4; ++i)
+            for (int i = 0; i < PER; ++i)
+                if (expert_of<PER, G, WHOLE>(sub, i) < p.experts) out[WHOLE ? i : G * i] = w[i];
+        }
+    } else {
+        uint16_t *out = static_cast<uint16_t *>(p.dlogits) + at;
+        if constexpr (WHOLE && PER >= 4) {
+#pragma unroll
+            for (int i = 0; i < PER / 4; ++i)
+                if (e0 < p.experts)
                     reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack2f<KIND>(w[4 * i], w[4 * i + 1]), pack2f<KIND>(w[4 * i + 2], w[4 * i + 3]));
-            } else {
+        } else {
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (e0 + i < p.experts) out[i] = static_cast<uint16_t>(pack2f<KIND>(w[i], 0.0f));
-            }
+            for (int i = 0; i < PER; ++i)
+                if (expert_of<PER, G, WHOLE>(sub, i) < p.experts) out[WHOLE ? i : G * i] = static_cast<uint16_t>(pack2f<KIND>(w[i], 0.0f));
         }
     }
 }
 
-template <int KIND, int PER>
+template <int KIND, int PER, int G>
 cudaError_t go(bool grad, const RouteParams &p, cudaStream_t stream, bool overlap)
 {
     // (a lane's logits at once: up to 16 bytes at a time)
     constexpr uintptr_t kBytes = PER * (KIND == 3 ? 4 : 2), kAlign = kBytes < 16 ? kBytes : 16;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(p.dlogits);
     const bool whole = p.experts % PER == 0 && at % kAlign == 0;
-    const auto run = [&](auto kernel, int tokens) {
-        const int64_t each = kRouteWarps * tokens;
-        return launch_kernel(kernel, dim3(static_cast<unsigned>((p.tokens + each - 1) / each)), 32 * kRouteWarps, 0, 1, stream, overlap, p, whole);
-    };
-    // (16384 tokens, 2 of 8 experts, and back: two tokens to a warp 7.8 us, one 8.7; 8 of 128 14.1 and 13.2)
-    constexpr int kTokens = PER <= 2 ? 2 : 1;
-    if (p.tokens <= 4096) return grad ? run(route_grad_kernel<KIND, PER, 1>, 1) : run(route_kernel<KIND, PER, 1>, 1);
-    return grad ? run(route_grad_kernel<KIND, PER, kTokens>, kTokens) : run(route_kernel<KIND, PER, kTokens>, kTokens);
+    constexpr int64_t kTokens = 32 * kRouteWarps / G;
+    const dim3 grid(static_cast<unsigned>((p.tokens + kTokens - 1) / kTokens));
+    const auto run = [&](auto kernel) { return launch_kernel(kernel, grid, 32 * kRouteWarps, 0, 1, stream, overlap, p); };
+    if (grad) return whole ? run(route_grad_kernel<KIND, PER, G, true>) : run(route_grad_kernel<KIND, PER, G, false>);
+    if constexpr (G < 32 && KIND != 3) return whole ? run(route_lanes_kernel<KIND, PER, G, true>) : run(route_lanes_kernel<KIND, PER, G, false>);
+    else if constexpr (G < 32) return cudaErrorInvalidValue;   // (not picked)
+    else return whole ? run(route_kernel<KIND, PER, true>) : run(route_kernel<KIND, PER, false>);
 }
 
 template <int KIND>
 cudaError_t pick(bool grad, const RouteParams &p, cudaStream_t stream, bool overlap)
 {
-    if (p.experts <= 32) return go<KIND, 1>(grad, p, stream, overlap);
-    if (p.experts <= 64) return go<KIND, 2>(grad, p, stream, overlap);
-    if (p.experts <= 128) return go<KIND, 4>(grad, p, stream, overlap);
-    if (p.experts <= 256) return go<KIND, 8>(grad, p, stream, overlap);
-    if (p.experts <= 512) return go<KIND, 16>(grad, p, stream, overlap);
-    return go<KIND, 32>(grad, p, stream, overlap);
+    if (grad || (KIND != 3 && p.top_k <= 8)) {
+        if (p.experts <= 32) return go<KIND, 4, 8>(grad, p, stream, overlap);
+        if (p.experts <= 64) return go<KIND, 4, 16>(grad, p, stream, overlap);
+        if (p.experts <= 128) return go<KIND, 8, 16>(grad, p, stream, overlap);
+        if (p.experts <= 256) return go<KIND, 16, 16>(grad, p, stream, overlap);
+    }
+    if (p.experts <= 32) return go<KIND, 1, 32>(grad, p, stream, overlap);
+    if (p.experts <= 64) return go<KIND, 2, 32>(grad, p, stream, overlap);
+    if (p.experts <= 128) return go<KIND, 4, 32>(grad, p, stream, overlap);
+    if (p.experts <= 256) return go<KIND, 8, 32>(grad, p, stream, overlap);
+    if (p.experts <= 512) return go<KIND, 16, 32>(grad, p, stream, overlap);
+    return go<KIND, 32, 32>(grad, p, stream, overlap);
 }
 
 cudaError_t run(bool grad, int kind, const RouteParams &p, cudaStream_t stream, bool overlap)
