@@ -476,7 +476,7 @@ typedef enum { GEMM_ROUTE_SELECTED = 0, GEMM_ROUTE_ALL = 1, GEMM_ROUTE_SIGMOID =
  * gemm_expert_sort, gemm_expert_combine and gemm_expert_layer take.  A logit of
  * -infinity, or NaN, is never chosen; where fewer than top_k are left, the
  * others' ids are -1 and their weights 0 (a padded token: all of them).
- * +infinity counts as the largest finite value.
+ * +infinity counts as a finite value above all others.
  * logits: tokens x experts, fp32, fp16 or bf16, aligned to its type.  experts in
  * [1, GEMM_EXPERT_SORT_MAX_EXPERTS], top_k in [1, min(experts,
  * GEMM_EXPERT_ROUTE_MAX_TOP_K)]; tokens * experts < 2^40. */

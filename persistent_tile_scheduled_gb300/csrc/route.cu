@@ -29,14 +29,24 @@ enum : int { ROUTE_SELECTED = 0, ROUTE_ALL = 1, ROUTE_SIGMOID = 2 };
 
 constexpr int kRouteWarps = 4;
 constexpr float kMaxFinite = 3.402823466e38f;
+// What +infinity counts as: fp32's largest value; of 16-bit logits one above all of
+// theirs whose lowest 13 bits are 0.
+template <int KIND>
+__device__ __forceinline__ float infinite()
+{
+    return KIND == 3 ? kMaxFinite : __int_as_float(0x7F7FE000);
+}
 #define kNothing __int_as_float(0xFF800000)   // -infinity
 constexpr uint32_t kIndex = 0x1FFFu;   // of a 16-bit logit's fp32 bits the lowest 13 are 0: they hold the expert
 
-// Unsigned keys in the order of the values.  -0 and 0 are one value, +infinity is the
-// largest finite one; what cannot be chosen (-infinity, NaN) is below kLeast.
+// Unsigned keys in the order of the values.  -0 and 0 are one value; what cannot be chosen (-infinity, NaN) is below kLeast.
 constexpr uint32_t kLeast = 0x00800000u;   // the key of the lowest finite value
 
-__device__ __forceinline__ float cleaned(float v) { return fminf(fmaxf(v, kNothing), kMaxFinite); }   // (NaN: -infinity)
+template <int KIND>
+__device__ __forceinline__ float cleaned(float v)   // (NaN: -infinity)
+{
+    return fminf(fmaxf(v, kNothing), infinite<KIND>());
+}
 
 template <int KIND>
 __device__ __forceinline__ uint32_t key_of(float v, int e)   // v: cleaned
@@ -84,7 +94,7 @@ __device__ __forceinline__ void load_logits(float (&x)[PER], const void *logits,
                 v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
             }
         }
-        const float most = e0 < experts ? kMaxFinite : kNothing;
+        const float most = e0 < experts ? infinite<KIND>() : kNothing;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if constexpr (KIND == 3) x[i] = __uint_as_float(v[i]);
@@ -99,7 +109,7 @@ __device__ __forceinline__ void load_logits(float (&x)[PER], const void *logits,
             if (e >= experts) continue;
             if constexpr (KIND == 3) x[i] = ld_global(static_cast<const float *>(logits) + row + e);
             else x[i] = unpack1<KIND>(ld_global(static_cast<const uint16_t *>(logits) + row + e));
-            x[i] = cleaned(x[i]);
+            x[i] = cleaned<KIND>(x[i]);
         }
     }
 }
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(const Rou
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = key_of<KIND>(x[i], expert_of<PER, G, WHOLE>(sub, i));
     sort_keys(key);
-    const float best = fminf(value_of<KIND>(lanes_max<G>(key[0])), kMaxFinite);
+    const float best = value_of<KIND>(lanes_max<G>(key[0]));
     float all = p.mode == ROUTE_ALL ? lanes_sum<G>(exp_sum(x, best)) : 0.0f;
     constexpr int kKeep = PER < 8 ? PER : 8;   // (a lane has 8 choices at most)
     uint32_t mine = 0u;                        // this lane's choice
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_lanes_kernel(const Rou
             key[kKeep - 1] = 0u;
         }
     }
-    const float w = mine >= kLeast ? share_of(fminf(value_of<KIND>(mine), kMaxFinite), best, p.mode) : 0.0f;
+    const float w = mine >= kLeast ? share_of(value_of<KIND>(mine), best, p.mode) : 0.0f;
     if (p.mode != ROUTE_ALL) all = lanes_sum<G>(w);
     if (sub < p.top_k && t < p.tokens) write_choice(p, t, sub, mine >= kLeast, static_cast<int>(kIndex - (mine & kIndex)), w, all);
 }
@@ -224,7 +234,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
         key[i] = key_of<KIND>(x[i], expert_of<PER, 32, WHOLE>(lane, i));
         most = max(most, key[i]);
     }
-    const float best = fminf(value_of<KIND>(__reduce_max_sync(0xffffffffu, most)), kMaxFinite);
+    const float best = value_of<KIND>(__reduce_max_sync(0xffffffffu, most));
     float all = p.mode == ROUTE_ALL ? lanes_sum<32>(exp_sum(x, best)) : 0.0f;
     uint32_t mine = 0u;   // this lane's choice
     int mine_id = -1;
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
             if (expert_of<PER, 32, WHOLE>(lane, i) == id) key[i] = 0u;
         if (lane == j) mine = top, mine_id = id;
     }
-    const float w = mine ? share_of(fminf(value_of<KIND>(mine), kMaxFinite), best, p.mode) : 0.0f;
+    const float w = mine ? share_of(value_of<KIND>(mine), best, p.mode) : 0.0f;
     if (p.mode != ROUTE_ALL) all = lanes_sum<32>(w);
     if (lane < p.top_k) write_choice(p, t, lane, mine != 0u, mine_id, w, all);
 }

@@ -136,6 +136,37 @@ def test_infinite_and_extreme_logits(h):
             assert (w[3].double().cpu() - torch.softmax(torch.tensor([-199.0, -200.0, -250.0]).double(), 0)).abs().max() < 1e-6
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("experts,k", [(4, 3), (10, 3), (40, 9), (130, 3), (300, 3)])
+def test_infinite_and_extreme_16_bit_logits(h, kind, experts, k):
+    """Rows of a type's extremes among zeros (masked ones where fewer are wanted), in every kernel: with 8 and 16 lanes and a warp to
+    a token, rows that can and cannot be loaded at once, more than 8 choices."""
+    code, dtype, _ = TYPES[kind]
+    big = torch.finfo(dtype).max
+    x = torch.full((5, experts), -INF, dtype=dtype)
+    x[0, :4] = torch.tensor([INF, 0.0, INF, -INF], dtype=dtype)
+    x[1, :4] = torch.tensor([big, INF, -big, 1.0], dtype=dtype)
+    x[2, :4] = torch.tensor([-big, -big, -INF, NAN], dtype=dtype)
+    x[3, :4] = torch.tensor([-200.0, -300.0, -250.0, -199.0], dtype=dtype)
+    x[4] = NAN
+    pad = [-1] * (k - 3)
+    want = [[0, 2, 1], [1, 0, 3], [0, 1, -1], [3, 0, 2], [-1, -1, -1]]
+    if k > 3:
+        want = [[0, 2, 1, -1], [1, 0, 3, 2], [0, 1, -1, -1], [3, 0, 2, 1], [-1] * 4]
+        pad = [-1] * (k - 4)
+    for mode in (SELECTED, ALL, SIGMOID):
+        ids, w = torch.zeros(5, k, dtype=torch.int32, device="cuda"), torch.full((5, k), NAN, device="cuda")
+        pts.gemm_expert_route(h, 5, k, experts, x.cuda(), ids, w, mode, code)
+        dl, dw = torch.full((5, experts), NAN, dtype=dtype, device="cuda"), torch.arange(1.0, k + 1, device="cuda").expand(5, k).contiguous()
+        pts.gemm_expert_route_grad(h, 5, k, experts, x.cuda(), ids, dw, dl, mode, code)
+        assert ids.tolist() == [row + pad for row in want]
+        assert torch.isfinite(w).all() and torch.isfinite(dl).all()
+        assert (w[:4].sum(1) - 1.0).abs().max() < (1e-6 if mode != ALL or k > 3 else 1e-3) and (w[4] == 0).all() and (dl[4] == 0).all()
+        if mode != SIGMOID:
+            assert w[0, :3].tolist() == [0.5, 0.5, 0.0]
+            assert w[1, 0] == 1.0   # (+infinity counts as more than the largest finite value)
+
+
 def test_ids_that_lead_nowhere_have_no_gradient(h):
     x = torch.randn(4, 8, generator=torch.Generator().manual_seed(1)).cuda()
     x[2, 5] = -INF
