@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const Rout
     inner = lanes_sum<G>(inner) * scale;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        w[i] = w[i] * scale * (g[i] - inner);
+        // (a logit that nothing depends on has none, also where a dweight is infinite)
+        w[i] = x[i] > kNothing ? w[i] * scale * (g[i] - inner) : 0.0f;
         if (p.mode == ROUTE_SIGMOID) w[i] *= rcp_fast(1.0f + exp_fast(x[i]));
     }
     if (!there) return;

@@ -197,3 +197,60 @@ def test_rows_at_odd_addresses(h):
 def test_no_tokens(h):
     assert pts.gemm_expert_route(h, 0, 2, 8, None, None, None, SELECTED, pts.GEMM_F32) == 0
     assert pts.gemm_expert_route_grad(h, 0, 2, 8, None, None, None, None, SELECTED, pts.GEMM_F32) == 0
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("mode", [SELECTED, ALL, SIGMOID], ids=["selected", "all", "sigmoid"])
+@pytest.mark.parametrize("experts", [7, 128, 1000])
+def test_infinite_dweights_reach_what_depends_on_them(h, experts, mode, kind):
+    """A token with infinite or NaN dweights: zeros where a logit was masked or, but for the softmax over all, not chosen; the other
+    tokens' gradients are as without it."""
+    code, dtype, _ = TYPES[kind]
+    x = (torch.randn(6, experts, generator=torch.Generator().manual_seed(5))).to(dtype)
+    x[:, 3] = -INF
+    ids = chosen(x, 3)
+    dw = torch.randn(6, 3, generator=torch.Generator().manual_seed(6))
+    got = []
+    for bad in (0.0, INF, NAN):
+        d = dw.clone()
+        if bad:
+            d[1, 0], d[4, 2] = bad, bad
+        dl = torch.full((6, experts), 9.0, dtype=dtype, device="cuda")
+        pts.gemm_expert_route_grad(h, 6, 3, experts, x.cuda(), ids.int().cuda(), d.cuda(), dl, mode, code)
+        got.append(dl.cpu())
+    free = torch.ones(6, experts, dtype=torch.bool)
+    if mode == ALL:
+        free[:] = False
+    free.scatter_(1, ids, False)
+    free[:, 3] = True
+    for dl in got[1:]:
+        assert (dl[free] == 0).all() and torch.equal(dl[[0, 2, 3, 5]], got[0][[0, 2, 3, 5]])
+        assert not torch.isfinite(dl[[1, 4]].gather(1, ids[[1, 4]])).any(1).all()
+
+
+def test_an_id_that_is_there_twice_adds_up(h):
+    x = torch.randn(3, 40, generator=torch.Generator().manual_seed(1)).cuda()
+    for mode in (SELECTED, ALL, SIGMOID):
+        out = []
+        for ids, dw in (([5, 9, 5], [0.5, -2.0, 0.75]), ([5, 9, -1], [1.25, -2.0, 3.0])):
+            dl = torch.zeros(3, 40, device="cuda")
+            pts.gemm_expert_route_grad(h, 3, 3, 40, x, torch.tensor([ids] * 3, dtype=torch.int32, device="cuda"), torch.tensor([dw] * 3, device="cuda"),
+                                       dl, mode, pts.GEMM_F32)
+            out.append(dl)
+        assert torch.equal(*out)
+
+
+def test_calls_that_are_refused(h):
+    x, ids, w = torch.zeros(4096, device="cuda"), torch.zeros(4096, dtype=torch.int32, device="cuda"), torch.zeros(4096, device="cuda")
+    route = lambda T, k, E, mode=0, dtype=pts.GEMM_F32, X=x.data_ptr(), i=ids.data_ptr(), v=w.data_ptr(): pts.gemm_expert_route(h, T, k, E, X, i, v, mode, dtype)  # noqa: E731
+    back = lambda T, k, E, mode=0, dtype=pts.GEMM_F32, X=x.data_ptr(), i=ids.data_ptr(), v=w.data_ptr(), o=x.data_ptr(): pts.gemm_expert_route_grad(h, T, k, E, X, i, v, o, mode, dtype)  # noqa: E731
+    for f in (route, back):
+        assert f(2, 2, 8) == 0
+        for bad in ((-1, 2, 8), (2, 0, 8), (2, 9, 8), (2, 33, 64), (2, 2, 0), (2, 2, 1025), (1 << 31, 2, 8), (2, 2, 8, 3), (2, 2, 8, -1), (2, 2, 8, 0, pts.GEMM_E4M3),
+                    (2, 2, 8, 0, pts.GEMM_F32, x.data_ptr() + 2), (2, 2, 8, 0, pts.GEMM_F16, x.data_ptr() + 1), (2, 2, 8, 0, pts.GEMM_F32, None),
+                    (2, 2, 8, 0, pts.GEMM_F32, x.data_ptr(), ids.data_ptr() + 2), (2, 2, 8, 0, pts.GEMM_F32, x.data_ptr(), ids.data_ptr(), None)):
+            with pytest.raises(pts.GemmError) as err:
+                f(*bad)
+            assert err.value.status == 1, bad
+    with pytest.raises(pts.GemmError):
+        back(2, 2, 8, 0, pts.GEMM_F32, x.data_ptr(), ids.data_ptr(), w.data_ptr(), x.data_ptr() + 2)
