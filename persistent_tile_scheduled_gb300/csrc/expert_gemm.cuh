@@ -43,10 +43,10 @@
 // contraction and add up through distributed shared memory, each its part of the
 // rows, in order (one row of 4096^2 11.3 us instead of 18.6).
 //
-// Warp roles as in gemm_kernel.cuh: producer, MMA, 4 epilogue warps, scheduler
-// (a static stride over the tiles of all experts, which it counts from the
-// offsets as it walks them), and in WGRAD a warp that clears.  Waits are
-// bounded in the same way.
+// Warp roles as in gemm_kernel.cuh: producer, MMA, 4 epilogue warps (8 where
+// there is more to do than to round), scheduler (a static stride over the tiles
+// of all experts, which it counts from the offsets as it walks them), and in
+// WGRAD a warp that clears.  Waits are bounded in the same way.
 #pragma once
 #include <type_traits>
 
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
 {
     // tmW: boxes of 128 features x one k-block (MN-major: 64 features x a stage); tmX: boxes
     // of BN / CG rows x one k-block, tmXs: of 16 rows (MN-major: both as tmW);
-    // tmO: the store box, 32 features x 64 rows.  With an epilogue 32 rows, gated 16
+    // tmO: the store box, 32 features x 64 rows.  With an epilogue 16 rows, gated 16
     // features, and a box of W holds 64 features of a gate and of what it multiplies
     // (encode_map_gated), so that a lane of the epilogue has both of its sums.
     static_assert(EPI == EPI_NONE || MODE == EXPERT_FWD, "");
