@@ -57,9 +57,22 @@ __device__ __forceinline__ float normal_tail(float z, float e)
 // max(z, 0), and NaN for NaN
 __device__ __forceinline__ float positive(float z) { return z <= 0.0f ? 0.0f : z; }
 
+// max(z, lo), and NaN for NaN
+__device__ __forceinline__ float at_least(float z, float lo)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(lo));
+    return y;
+}
+
+// silu and the tanh form of gelu of anything below this are less than 2^-54 away from 0:
+// there z counts as this, -infinity too, since the factor that it meets stops falling.
+constexpr float kLowest = -44.0f;
+
 template <int ACT>
 __device__ __forceinline__ float act(float z)
 {
+    if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) z = at_least(z, kLowest);
     if constexpr (ACT == ACT_RELU) return positive(z);
     if constexpr (ACT == ACT_RELU2) return positive(z) * positive(z);
     // z Phi(z): z - z Phi(-z) above 0 (the factor of the tail, 0 from 14 on, is kept finite)
@@ -133,7 +146,13 @@ __device__ __forceinline__ void normal_tail(Pair z, Pair &e, Pair &q)
     q = g * t * e;
 }
 
-// 2^y, y at most 60: 1 + 2^60 is as good as any larger, and two of them have a product
+__device__ __forceinline__ Pair at_least(Pair z, float lo)
+{
+    return each(z, [=](float v) { return at_least(v, lo); });
+}
+
+// 2^y, y at most 60: 1 / (1 + 2^60), of kLowest at most, is next to nothing, and two of
+// them have a product (a NaN is taken for 60: it comes back with z, and not into the other value)
 __device__ __forceinline__ Pair exp2_limited(Pair y)
 {
     return each(y, [](float v) { return exp2_fast(fminf(v, 60.0f)); });
@@ -155,7 +174,7 @@ __device__ __forceinline__ Pair act(Pair z)
     if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
         Pair y = z * both(-kLog2E);
         if constexpr (ACT == ACT_GELU_TANH) y = z * fma(both(-kLog2E * kGeluTanhTwice * kGeluTanhCube) * z, z, both(-kLog2E * kGeluTanhTwice));
-        return z * rcp_fast(exp2_limited(y) + both(1.0f));
+        return at_least(z, kLowest) * rcp_fast(exp2_limited(y) + both(1.0f));
     }
     return z;
 }
@@ -173,6 +192,7 @@ __device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
         slope = p + p;
     } else if constexpr (ACT == ACT_GELU) {
         // Phi(z) = q below 0, 1 - q above; Phi + z phi(z)
+        z = at_least(z, -16.0f);   // (e is 0 there; -infinity times it would not be)
         Pair e, tail;
         normal_tail(z, e, tail);
         const float2 q = values(tail), v = values(z);
@@ -181,6 +201,7 @@ __device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
         slope = fma(z * both(kNormalPeak), e, p);
     } else if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
         // z s(y), s = 1 / (1 + exp(-y)): s + z s (1 - s) y', with 1 - s = exp(-y) s
+        z = at_least(z, kLowest);
         Pair y, dy;   // (y: the exponent of 2)
         if constexpr (ACT == ACT_GELU_TANH) {
             const Pair z2 = each(z * z, [](float v) { return fminf(v, 4096.0f); });   // (dy stays finite; there the slope is 0 or 1)

@@ -295,3 +295,69 @@ def test_a_wait_that_runs_out(opts, counts, N, K, load, act, keep):
         if flags:
             assert st == pts.gemm.GEMM_ERR_TIMEOUT and dev >> 24 == 1
     assert st == 0 and torch.equal(C.double(), want + residual.double())
+
+
+# ---- extremes -----------------------------------------------------------------------
+
+EXTREMES = [-float("inf"), -3e38, -1e30, -1e10, -65504.0, -5000.0, -300.0, -90.0, -60.0, -44.0, -41.0, -20.0, -6.7, -0.0, 0.0, 2.0 ** -20, 5.0, 20.0, 90.0,
+            5000.0, 65504.0, 1e10, 1e18]
+
+
+def extreme(dtype, N, seed):
+    """N values, each of EXTREMES next to each other one sometimes; f: their activation in 64 bits, whose limit at -infinity is 0."""
+    x = torch.tensor(EXTREMES)
+    x = x[(x.abs() <= torch.finfo(dtype).max) | torch.isinf(x)]
+    return x[torch.randint(0, len(x), (N,), generator=torch.Generator().manual_seed(seed))].to(dtype).cuda()
+
+
+def at_limits(code, z):
+    a, s, sa = ref.act(code, z.double().clamp(min=-1e300))
+    return torch.where(torch.isnan(a), 0.0, a), torch.where(torch.isnan(s), (z > 0).double(), s), torch.where(torch.isnan(sa), (z > 0).double(), sa)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=NAMES)
+@pytest.mark.parametrize("rows,K", [(1, 16), (1, 8192), (30, 16), (12, 4096), (300, 16)])
+@pytest.mark.parametrize("code", range(1, 6), ids=ref.ACTS[1:])
+def test_extreme_sums(hv, code, rows, K, dtype):
+    """Sums from -infinity up to 1e18 (the bias; the operands are 0): the activation's limits, without a NaN, beside a NaN."""
+    N, t = 272, TORCH[dtype]
+    A, B = torch.zeros(rows, K, dtype=t, device="cuda"), torch.zeros(2 * N, K, dtype=t, device="cuda")
+    for gated in (0, GATED):
+        bias = torch.cat([extreme(t, N, 1), torch.full((N,), -0.75, dtype=t, device="cuda")])[None, :N * (2 if gated else 1)].contiguous()
+        bias[0, 5] = float("nan")
+        A[rows // 2, 3] = float("nan") if rows > 1 else 0.0
+        C = torch.zeros(rows, N, dtype=t, device="cuda")
+        pts.gemm_run_linear(hv, rows, 1, N, K, A, B, bias, None, None, C, None, code | gated, dtype)
+        if rows > 1:
+            assert torch.isnan(C[rows // 2]).all()
+            C[rows // 2] = C[0]
+        a = at_limits(code, bias[0, :N])[0] * (-0.75 if gated else 1.0)
+        assert torch.isnan(C[:, 5]).all()
+        a = a.to(t).double().expand(rows, N).clone()   # (rounded: what overflows is infinite on both sides)
+        a[:, 5], C[:, 5] = 0.0, 0.0
+        same = C.double() == a
+        assert (same | ((C.double() - a).abs() <= 2 * ref.U[t] * a.abs() + 2 * ref.EPS_ACT * a.abs() + ref.TINY)).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=NAMES)
+@pytest.mark.parametrize("code", range(1, 6), ids=ref.ACTS[1:])
+def test_extreme_gradients(h, code, dtype):
+    rows, N, t = 9, 272, TORCH[dtype]
+    for gated in (0, GATED):
+        g = torch.stack([extreme(t, N, r) for r in range(rows)])
+        Z = torch.cat([g, torch.full_like(g, -0.75)], 1)[:, :N * (2 if gated else 1)].contiguous()
+        dC, dZ = torch.full_like(g, 0.5), torch.zeros_like(Z)
+        dC[3, 7], Z[4, 8] = float("nan"), float("nan")
+        pts.gemm_linear_grad(h, rows, 1, N, dC, Z, None, dZ, None, code | gated, dtype)
+        a, s, sa = at_limits(code, g)
+        want = torch.cat([s * 0.5 * -0.75, a * 0.5], 1) if gated else s * 0.5
+        err = 2 * ref.EPS_ACT * (torch.cat([sa * 0.5 * 0.75, a.abs() * 0.5], 1) if gated else sa * 0.5)
+        want = want.to(t).double()   # (rounded: what overflows is infinite on both sides)
+        err = torch.where(torch.isinf(want), 0.0, err)
+        for half in (dZ[:, :N], want[:, :N], dZ[:, N:], want[:, N:]):
+            if half.shape[1]:
+                if half.dtype == t and code > 2:   # (of relu the slope at NaN is 0)
+                    assert torch.isnan(half[[3, 4], [7, 8]]).all()
+                half[[3, 4], [7, 8]] = 0.0
+        same = dZ.double() == want
+        assert (same | ((dZ.double() - want).abs() <= 2 * ref.U[t] * want.abs() + 2 * err + ref.TINY)).all(), code
