@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
 {
     // tmW: boxes of 128 features x one k-block (MN-major: 64 features x a stage); tmX: boxes
     // of BN / CG rows x one k-block, tmXs: of 16 rows (MN-major: both as tmW);
-    // tmO: the store box, 32 features x 64 rows.  With an epilogue 16 rows, gated 16
+    // tmO: the store box, 32 features x 64 rows.  With an epilogue 32 rows, gated 16
     // features, and a box of W holds 64 features of a gate and of what it multiplies
     // (encode_map_gated), so that a lane of the epilogue has both of its sums.
     static_assert(EPI == EPI_NONE || MODE == EXPERT_FWD, "");
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
             mbar_init(empty0 + 8 * s, 1);
             if (MODE == EXPERT_WGRAD) mbar_init(fix0 + 8 * s, 1);
         }
-        if (EPI != EPI_NONE)   // (the residual's boxes, two to an epilogue warp)
-            for (int k = 0; k < 2 * kEpi; ++k) mbar_init(fix0 + 8 * k, 1);
+        if (EPI != EPI_NONE)   // (the residual's boxes)
+            for (int k = 0; k < expert_fix_barriers(EPI); ++k) mbar_init(fix0 + 8 * k, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
             mbar_init(acc_empty0 + 8 * b, kEpi * CG);
@@ -392,20 +392,28 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
     } else if (warp < 2 + kEpi) {
         // ============================== epilogue ===============================
         if constexpr (EPI != EPI_NONE) {
-            // As below, with two warps to every 32 features, which take chunks of 16 rows
-            // in turn: a warp's 4 KB are four boxes.  C goes out through a ring of them,
-            // into which the residual's boxes are loaded ahead, so that each is added in
-            // place; Z takes two of the four.
+            // As below, with two warps to every 32 features, which take chunks of 32 rows in
+            // turn.  A warp's 4 KB are boxes of a chunk: one that the residual's are loaded
+            // into, each a chunk ahead, and one or two that Z and C leave through.  Z is on
+            // its way while the activation is computed.
             constexpr int kF = EPI == EPI_GATED ? 16 : 32;   // output features of a warp
-            constexpr uint32_t kRow = 2 * kF, kBox = kLinearChunk * kRow;
-            constexpr uint32_t kSlot = epi_bytes() / kEpi / 4;
+            constexpr uint32_t kRow = 2 * kF, kBox = kLinearChunk * kRow, kBytes = epi_bytes() / kEpi;
+            static_assert(kBytes == 4096 && kBox == (EPI == EPI_GATED ? 1024 : 2048), "");
             const uint32_t q = warp & 3u;
             const int turn = static_cast<int>(warp - 2) / kEpiWarps;   // chunks turn, turn + 2, ...
-            const uint32_t stage_base = sEpi + (warp - 2) * (4 * kSlot);
-            const uint32_t res0 = fix0 + 16 * (warp - 2);   // + 8 * (chunk & 1): the residual's box is there
+            const uint32_t stage_base = sEpi + (warp - 2) * kBytes;   // (the residual's box)
+            const uint32_t res_bar = fix0 + 8 * (warp - 2);           // it is there
             const bool keep = p.z != nullptr, res = p.residual != nullptr;
-            const uint32_t bufs = keep ? 2 : 4;
-            const int lead = static_cast<int>(bufs) / 2;    // own chunks that the residual's loads are ahead
+            // C's box, every other chunk's, and Z's (gated two): 32 features with a residual have one for all
+            const bool one_box = EPI != EPI_GATED && res;
+            const uint32_t cbuf = stage_base + (EPI == EPI_GATED ? (keep ? 1 : 2) * kBox : (keep || res ? 1 : 0) * kBox);
+            const uint32_t cbuf2 = cbuf + (keep || one_box ? 0 : kBox);
+            const uint32_t zbuf = stage_base + (EPI == EPI_GATED ? 2 : one_box ? 1 : 0) * kBox;
+            auto wait_box = [&]() {   // the last store from the box that comes next has read it
+                if (one_box) bulk_wait_read<0>();
+                else bulk_wait_read<1>();
+                __syncwarp();
+            };
             // stmatrix: this lane's row and 16 bytes of it (32 features: 8 rows at a time; gated 16)
             const uint32_t st_row = EPI == EPI_GATED ? (lane & 7u) + ((lane >> 4) << 3) : lane & 7u;
             const uint32_t st_chunk = EPI == EPI_GATED ? (lane >> 3) & 1u : lane >> 3;
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
             };
             int acc = 0;
             uint32_t acc_phase = 0;
-            uint32_t n = 0, loads = 0;   // chunks done, residual boxes asked for
+            uint32_t n = 0, loads = 0;   // chunks done, residual boxes asked for and read
             for (int i = 0;; ++i) {
                 ExpertItem t;
                 if (ring_read(i, t) <= 0) break;
@@ -428,23 +436,17 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
                     break;
                 }
                 const bool empty_sum = t.nkb == 0;
-                const int chunks = t.n_len / kLinearChunk;
+                const int chunks = (t.n_len + kLinearChunk - 1) / kLinearChunk;
                 const int f = t.f0 + static_cast<int>(rank) * kFeatures + static_cast<int>(q) * kF;
-                // (what was read and written in a box was before the fence of its store)
                 auto load_residual = [&](int c) {
-                    __syncwarp();
                     if (elect_one()) {
-                        const uint32_t bar = res0 + 8 * (loads & 1u);
-                        mbar_arrive_expect_tx(bar, kBox);
-                        tma_load_3d(1u, stage_base + loads % bufs * kSlot, &maps.r, bar, f, t.row0 + c * kLinearChunk, 0);
+                        mbar_arrive_expect_tx(res_bar, kBox);
+                        tma_load_3d(1u, stage_base, &maps.r, res_bar, f, t.row0 + c * kLinearChunk, 0);
                     }
                     __syncwarp();
                     ++loads;
                 };
-                if (res) {
-                    bulk_wait_read<1>();
-                    for (int c = turn; c < turn + 2 * lead && c < chunks; c += 2) load_residual(c);
-                }
+                if (res && turn < chunks) load_residual(turn);
                 // a lane's features are f + lane / 4 + 0, 8, 16, 24; gated 0 of both matrices and 8 of both
                 Pair bias[4];
 #pragma unroll
@@ -470,93 +472,112 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
                 if (turn >= chunks) release();
                 bool ok = true;
                 for (int c = turn; c < chunks; c += 2) {
-                    uint32_t lo[8], hi[8];
-                    tmem_ld_16x256b_x2(tbase + c * kLinearChunk, lo);
-                    tmem_ld_16x256b_x2(tbase + (16u << 16) + c * kLinearChunk, hi);
-                    tmem_wait_ld();
+                    // (of a last chunk of 16 rows the other 16 are whatever the accumulator held)
+                    uint32_t lo[16], hi[16];
+                    if (!empty_sum) {
+                        tmem_ld_16x256b_x4(tbase + c * kLinearChunk, lo);
+                        tmem_ld_16x256b_x4(tbase + (16u << 16) + c * kLinearChunk, hi);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) lo[j] = hi[j] = 0u;
+                    }
                     if (c + 2 >= chunks) release();
-                    Pair x[4], y[4];   // [rows 0, 8][feature 0, 8; y: 16, 24 (gated 0 of both matrices; y: 8)], two rows each
+                    Pair x[8], y[8];   // [rows 0, 8, 16, 24][feature 0, 8; y: 16, 24 (gated 0 of both matrices; y: 8)], two rows each
                     const Pair scale = both(p.out_scale);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         x[j] = pair(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]));
                         y[j] = pair(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1]));
-                        if (empty_sum) x[j] = y[j] = both(0.0f);
                         x[j] = fma(x[j], scale, bias[j & 1]);
                         y[j] = fma(y[j], scale, bias[2 + (j & 1)]);
                     }
-                    const uint32_t buf = stage_base + n % bufs * kSlot, zbuf = stage_base + (2 + (n & 1u)) * kSlot;
-                    bulk_wait_read<1>();   // the stores that used these boxes have read them
-                    __syncwarp();
-                    if (keep) {
-                        if constexpr (EPI == EPI_GATED) {   // (16 rows of each matrix)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                stmatrix_x4_trans(at(zbuf + k * kBox, st_row, st_chunk), packed(x[k]), packed(y[k]), packed(x[2 + k]), packed(y[2 + k]));
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; j += 2)
-                                stmatrix_x4_trans(at(zbuf, 4 * j + st_row, st_chunk), packed(x[j]), packed(x[j + 1]), packed(y[j]), packed(y[j + 1]));
-                        }
-                    }
-                    with_act(p.act, [&](auto tag) {
-                        constexpr int A = decltype(tag)::value;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (EPI == EPI_GATED && (j & 1)) continue;
-                            x[j] = act<A>(x[j]);
-                            y[j] = act<A>(y[j]);
-                            if (EPI == EPI_GATED) x[j] = x[j] * x[j + 1], y[j] = y[j] * y[j + 1];
-                        }
-                    });
-                    if (res) {
-                        ok = ctl.wait_all(res0 + 8 * (n & 1u), (n >> 1) & 1u, WHERE_FULL);
-                        if (!ok) break;
-                        if (c + 2 * lead < chunks) {
-                            if (lead == 1) bulk_wait_read<0>();   // (its box is the last chunk's)
-                            load_residual(c + 2 * lead);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < (EPI == EPI_GATED ? 1 : 4); j += 2) {
-                        // four matrices of 8 rows x 8 features
-                        Pair v[4] = {x[j], EPI == EPI_GATED ? y[j] : x[j + 1], EPI == EPI_GATED ? x[j + 2] : y[j], EPI == EPI_GATED ? y[j + 2] : y[j + 1]};
-                        const uint32_t to = at(buf, 4 * j + st_row, st_chunk);
-                        if (res) {
-                            uint32_t r[4];
-                            ldmatrix_x4_trans(to, r[0], r[1], r[2], r[3]);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] = v[k] + pair(unpack2<KIND>(r[k]));
-                        }
-                        stmatrix_x4_trans(to, packed(v[0]), packed(v[1]), packed(v[2]), packed(v[3]));
-                    }
                     const int row0 = t.row0 + c * kLinearChunk;
-                    if (row0 + kLinearChunk <= t.row_end) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        const uint32_t go = f < p.features ? one : 0u;
-                        tma_store_3d_if(go, &tmO, buf, f, row0, 0);
-                        if (keep) {
-                            tma_store_3d_if(go, &maps.z, zbuf, f, EPI == EPI_GATED ? 0 : row0, EPI == EPI_GATED ? row0 : 0);
-                            if constexpr (EPI == EPI_GATED) tma_store_3d_if(go, &maps.z, zbuf + kBox, f, 1, row0);
-                        }
-                    } else {
+                    const bool whole = row0 + kLinearChunk <= t.row_end;
+                    // a box that ends inside an expert's last rows is copied out, 16 bytes at a time
+                    auto copy_out = [&](uint32_t buf, void *to, long long pitch, int at0) {
                         __syncwarp();
                         constexpr uint32_t kPieces = kF / 8;   // 16-byte pieces of a row
                         for (uint32_t piece = lane; piece < kLinearChunk * kPieces; piece += 32) {
                             const uint32_t r = piece / kPieces, ch = piece % kPieces;
                             const long long row = row0 + static_cast<long long>(r);
                             const int ff = f + 8 * static_cast<int>(ch);
-                            if (row >= t.row_end || ff >= p.features) continue;
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * p.features + ff) = ld_shared_v4(at(buf, r, ch));
-                            if (!keep) continue;
-                            uint16_t *z = static_cast<uint16_t *>(p.z) + row * p.features * (EPI == EPI_GATED ? 2 : 1) + ff;
-                            *reinterpret_cast<uint4 *>(z) = ld_shared_v4(at(zbuf, r, ch));
-                            if constexpr (EPI == EPI_GATED) *reinterpret_cast<uint4 *>(z + p.features) = ld_shared_v4(at(zbuf + kBox, r, ch));
+                            if (row < t.row_end && ff < p.features)
+                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + row * pitch + at0 + ff) = ld_shared_v4(at(buf, r, ch));
                         }
+                        __syncwarp();
+                    };
+                    // (what was read and written in a box is ordered before its next load or store)
+                    auto fence_box = [&]() {
                         fence_proxy_async_smem();
                         __syncwarp();
+                    };
+                    if (keep) {
+                        wait_box();
+                        if constexpr (EPI == EPI_GATED) {   // (16 rows of each matrix)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int j = (k >> 1) * 4 + (k & 1);
+                                stmatrix_x4_trans(at(zbuf + (k & 1) * kBox, 4 * (j & 4) + st_row, st_chunk), packed(x[j]), packed(y[j]), packed(x[j + 2]), packed(y[j + 2]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2)
+                                stmatrix_x4_trans(at(zbuf, 4 * j + st_row, st_chunk), packed(x[j]), packed(x[j + 1]), packed(y[j]), packed(y[j + 1]));
+                        }
+                        const long long pitch = static_cast<long long>(p.features) * (EPI == EPI_GATED ? 2 : 1);
+                        if (!whole) {
+                            copy_out(zbuf, p.z, pitch, 0);
+                            if constexpr (EPI == EPI_GATED) copy_out(zbuf + kBox, p.z, pitch, p.features);
+                        }
+                        fence_box();
+                        if (whole && f < p.features && elect_one()) {
+                            tma_store_3d_if(1u, &maps.z, zbuf, f, EPI == EPI_GATED ? 0 : row0, EPI == EPI_GATED ? row0 : 0);
+                            if constexpr (EPI == EPI_GATED) tma_store_3d_if(1u, &maps.z, zbuf + kBox, f, 1, row0);
+                        }
+                        bulk_commit();
                     }
+                    uint32_t r[EPI == EPI_GATED ? 2 : 4][4];
+                    if (res) {
+                        ok = __all_sync(0xffffffffu, mbar_try_wait_cta(res_bar, n & 1u)) || ctl.wait_all(res_bar, n & 1u, WHERE_FULL);
+                        if (!ok) break;
+#pragma unroll
+                        for (int j = 0; j < (EPI == EPI_GATED ? 2 : 4); ++j) {
+                            const uint32_t from = at(stage_base, (EPI == EPI_GATED ? 16 : 8) * j + st_row, st_chunk);
+                            ldmatrix_x4_trans(from, r[j][0], r[j][1], r[j][2], r[j][3]);
+                        }
+                        fence_box();
+                        if (c + 2 < chunks) load_residual(c + 2);
+                    }
+                    with_act(p.act, [&](auto tag) {
+                        constexpr int A = decltype(tag)::value;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (EPI == EPI_GATED && (j & 1)) continue;
+                            x[j] = act<A>(x[j]);
+                            y[j] = act<A>(y[j]);
+                            if (EPI == EPI_GATED) x[j] = x[j] * x[j + 1], y[j] = y[j] * y[j + 1];
+                        }
+                    });
+                    // four matrices of 8 rows x 8 features at a time
+                    auto quad = [&](int j, int k) -> Pair & {
+                        if (EPI == EPI_GATED) return k & 1 ? y[4 * j + (k & 2)] : x[4 * j + (k & 2)];
+                        return k & 2 ? y[2 * j + (k & 1)] : x[2 * j + (k & 1)];
+                    };
+                    if (res) {
+#pragma unroll
+                        for (int j = 0; j < (EPI == EPI_GATED ? 2 : 4); ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) quad(j, k) = quad(j, k) + pair(unpack2<KIND>(r[j][k]));
+                    }
+                    const uint32_t buf = n & 1u ? cbuf2 : cbuf;
+                    wait_box();
+#pragma unroll
+                    for (int j = 0; j < (EPI == EPI_GATED ? 2 : 4); ++j)
+                        stmatrix_x4_trans(at(buf, (EPI == EPI_GATED ? 16 : 8) * j + st_row, st_chunk), packed(quad(j, 0)), packed(quad(j, 1)), packed(quad(j, 2)), packed(quad(j, 3)));
+                    if (!whole) copy_out(buf, p.out, p.features, 0);
+                    fence_box();
+                    if (whole && f < p.features && elect_one()) tma_store_3d_if(1u, &tmO, buf, f, row0, 0);
                     bulk_commit();
                     ++n;
                 }
@@ -566,7 +587,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
                     acc_phase ^= 1u;
                 }
             }
-            for (; n < loads; ++n) ctl.drain(res0 + 8 * (n & 1u), (n >> 1) & 1u, 10000000ull);   // (stopped early)
+            for (; n < loads; ++n) ctl.drain(res_bar, n & 1u, 10000000ull);   // (stopped early)
             bulk_wait_read<0>();
             __syncwarp();
         } else {

@@ -48,8 +48,8 @@ struct LinearMaps : ExpertMaps {
 };
 
 // Epilogue warps.  One with activations computes some 25 instructions per element, which
-// 4 warps, one to a scheduler, take too long for (bf16 4096^2, K = 512, gated silu: 42
-// us with 4, 37 with 8).
+// 4 warps, one to a scheduler, take too long for (bf16 4096^2, K = 512, gated silu, chunks
+// of 16 rows: 42 us with 4, 37 with 8).
 __host__ __device__ constexpr int expert_epi_warps(int epi) { return epi == EPI_NONE ? kEpiWarps : 2 * kEpiWarps; }
 
 // producer, MMA, epilogue warps, scheduler; WGRAD has a clearing warp too
@@ -60,7 +60,7 @@ __host__ __device__ constexpr int expert_threads(int mode, int epi = EPI_NONE)
 static_assert(expert_threads(EXPERT_FWD) == kThreads, "");
 
 // Barriers that only some kernels use: WGRAD's cleared stages, an epilogue's residual.
-__host__ __device__ constexpr int expert_fix_barriers(int epi) { return epi == EPI_NONE ? kMaxStages : 2 * expert_epi_warps(epi); }
+__host__ __device__ constexpr int expert_fix_barriers(int epi) { return epi == EPI_NONE ? kMaxStages : expert_epi_warps(epi); }
 
 // Dynamic shared memory for `stages` stages of a tile of bn rows (plus 1 KB
 // for aligning the base to the swizzle period).
@@ -89,7 +89,11 @@ ExpertOps expert_ops_wgrad(int kind, int cg);
 ExpertOps linear_ops_f16(bool gated, int cg, int bn);
 ExpertOps linear_ops_bf16(bool gated, int cg, int bn);
 ExpertOps linear_ops_e4m3(bool gated, int cg, int bn);
-constexpr int kLinearChunk = 16;   // output rows per store box with an epilogue
+// Output rows per box of an epilogue with more to do than to round.  What a chunk costs
+// whatever its size, waits, fence and store, is some 500 cycles of a warp (bf16 4096^2, K =
+// 256, chunks of 16 / 32 rows: nothing in the epilogue 18 / 14 us, gated silu with Z 41 /
+// 30); of 64 rows a warp's 4 KB hold no second box.
+constexpr int kLinearChunk = 32;
 
 // The same for few rows (linear_rows.cu): fp16 and bf16.
 struct LinearRowsParams {
