@@ -91,8 +91,19 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     int split = 1;
     const int64_t length_kb = (contraction + kelems - 1) / kelems;
     if (mode == EXPERT_FWD && bn == kExpertTileNFew && h->opts.cta_group == 0 && h->opts.max_clusters == 0 && length_kb >= 24) {
-        while (split < 4 && tiles * split * 2 <= h->sm_count) split *= 2;
-        if (split == 4 && length_kb >= 64 && tiles * 16 <= h->sm_count) split = 8;
+        // (of an epilogue's kernels only what fits at once: 38 tiles by 4 are 152 CTAs, but the
+        // device's parts hold fewer clusters of 4)
+        const auto fits = [&](int cluster) -> bool {
+            if (!epi) return true;
+            int &n = h->linear_shared[kind][gated][cluster / 4];
+            if (n == 0 && (ops.fit(cluster, smem, &n) != cudaSuccess || n < 1)) {
+                cudaGetLastError();
+                n = -1;
+            }
+            return tiles <= n;
+        };
+        while (split < 4 && tiles * split * 2 <= h->sm_count && fits(2 * split)) split *= 2;
+        if (split == 4 && length_kb >= 64 && tiles * 16 <= h->sm_count && fits(8)) split = 8;
         if (split == 2 && length_kb < 32) split = 1;
     }
 

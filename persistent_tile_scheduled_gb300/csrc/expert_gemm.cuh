@@ -172,12 +172,16 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
+    if (kSplit && split > 1) cluster_arrive_relaxed();   // (waited for before the first store to another CTA)
     tc_fence_after();
     const uint32_t tmem_base = ld_shared_u32(tmem_slot);
     const uint32_t one = lane == 0 ? 1u : 0u;
 
     pdl_launch_dependents();
-    pdl_wait();   // the offsets and operands may be the previous grid's outputs
+    // The offsets and operands may be the previous grid's outputs.  One matrix's tiles need
+    // nothing of it: they are handed out before, and only the loads wait.
+    const bool early = EPI != EPI_NONE && !p.offsets;
+    if (!early || (warp != 0 && warp != kScheduler)) pdl_wait();
 
     // ---- work-item broadcast ring (as in gemm_kernel.cuh) ---------------------
     auto publish = [&](int i, bool valid, const ExpertItem &t) -> bool {
@@ -232,6 +236,9 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
         return v0.x != 0 ? 1 : 0;
     };
 
+    // of a shared tile: what its first outputs are added to
+    [[maybe_unused]] uint4 join_bias[EPI == EPI_GATED ? 2 : 1] = {}, join_res = {};
+
     if (warp == 0) {
         // =============================== producer ==============================
         int stage = 0;
@@ -240,7 +247,9 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
         bool ok = true;
         for (int i = 0;; ++i) {
             ExpertItem t;
-            if (ring_read(i, t) <= 0) break;
+            const int got = ring_read(i, t);
+            if (early && i == 0) pdl_wait();
+            if (got <= 0) break;
             const int xr = t.n_len / CG;   // this CTA's accumulator columns
             const int wf = t.f0 + static_cast<int>(rank) * kFeatures;
             const int xrow = t.row0 + static_cast<int>(rank) * xr;
@@ -315,8 +324,8 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
         // not announce is given time at the teardown.
         if (CG == 1 || leader) {
             const long long n = issued < S ? issued : S;
-            for (long long j = 0; j < n; ++j) {
-                const long long g = issued - 1 - j;
+            if (static_cast<long long>(lane) < n) {   // (a lane each: one after another they take some 300 cycles each)
+                const long long g = issued - 1 - static_cast<long long>(lane);
                 ctl.drain(full0 + 8 * static_cast<int>(g % S), static_cast<uint32_t>((g / S) & 1), 10000000ull);
             }
         }
@@ -431,6 +440,16 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
                 ExpertItem t;
                 if (ring_read(i, t) <= 0) break;
                 if (kSplit && split > 1) {   // (the only tile; added up below)
+                    const int item = static_cast<int>(threadIdx.x) - 64, ff = t.f0 + item % (kFeatures / 8) * 8;
+                    const int row = item / (kFeatures / 8), part = t.n_len / split;
+                    const long long out_row = t.row0 + share * part + row;
+                    if (p.bias && ff < p.features) {
+                        const uint16_t *b = static_cast<const uint16_t *>(p.bias) + static_cast<long long>(t.e) * p.features * (EPI == EPI_GATED ? 2 : 1) + ff;
+                        join_bias[0] = ld_global(reinterpret_cast<const uint4 *>(b));
+                        if constexpr (EPI == EPI_GATED) join_bias[1] = ld_global(reinterpret_cast<const uint4 *>(b + p.features));
+                    }
+                    if (p.residual && row < part && out_row < t.row_end && ff < p.features)
+                        join_res = ld_global(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + out_row * p.features + ff));
                     ctl.wait_all(acc_full0 + 8 * acc, acc_phase, WHERE_ACC_FULL);
                     tc_fence_after();
                     break;
@@ -798,76 +817,86 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
 
     // ---- a tile whose contraction is shared ------------------------------------
     if (kSplit && split > 1) {
-        // CTA j of the cluster adds up rows j * part ..: [CTA][row][feature], where the
-        // stages were; the tile is the ring's first item
-        const int part = BN / split, shift = __ffs(part) - 1;   // (split is 2, 4 or 8)
-        __syncthreads();
-        cluster_sync();   // (every CTA is through with its stages)
-        const bool published = mbar_try_wait(ring_full0, 0);
+        // CTA j of the cluster adds up rows j * part ..: [CTA][row][feature], where tiles
+        // are staged otherwise; the tile is the ring's first item
+        cluster_wait();
+        const bool adds = warp >= 2 && warp < 2 + kEpi;
+        const bool there = adds && mbar_try_wait(ring_full0, 0) && ld_shared_u32(ring0) != 0;
         const uint4 v0 = ld_shared_v4(ring0), v1 = ld_shared_v4(ring0 + 16);
-        const bool there = published && v0.x != 0;
-        if (there && warp >= 2 && warp < 2 + kEpiWarps) {
-            const uint32_t q = warp & 3u;
+        const int n_len = static_cast<int>(v1.y), part = there ? n_len / split : 1;   // (a multiple of 16 by 2, 4 or 8)
+        if (there) {
+            const uint32_t q = warp & 3u, inv = (65536u + static_cast<uint32_t>(part) - 1u) / static_cast<uint32_t>(part);
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem_base + ((q * 32u) << 16) + 32 * c, v);
+            for (int c = static_cast<int>(warp - 2) / kEpiWarps * 16; c < n_len; c += kEpi / kEpiWarps * 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(tmem_base + ((q * 32u) << 16) + c, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int row = 32 * c + i, to = row >> shift;
-                    st_cluster_u32(mapa(base + ((share * part + (row & (part - 1))) * kRowsPerCta + q * 32 + lane) * 4,
-                                        static_cast<uint32_t>(to)), v[i]);
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t row = static_cast<uint32_t>(c + i), to = row * inv >> 16;   // row / part
+                    st_cluster_u32(mapa(sEpi + ((share * part + row - to * part) * kRowsPerCta + q * 32 + lane) * 4, to), v[i]);
                 }
             }
         }
         cluster_sync();
-        if (there)
-            for (int i = static_cast<int>(threadIdx.x); i < part * kFeatures / 2; i += static_cast<int>(blockDim.x)) {
-                const int row = i / (kFeatures / 2), n = 2 * (i % (kFeatures / 2));
-                const int m = EPI == EPI_GATED ? (n / 8) * 16 + n % 8 : n;   // the accumulator's row
-                float lo = 0.0f, hi = 0.0f, lo2 = 0.0f, hi2 = 0.0f;
-                for (int c = 0; c < split; ++c) {
-                    const uint32_t from = base + ((c * part + row) * kRowsPerCta + m) * 4;
-                    lo += __uint_as_float(ld_shared_u32(from));
-                    hi += __uint_as_float(ld_shared_u32(from + 4));
-                    if constexpr (EPI == EPI_GATED) {
-                        lo2 += __uint_as_float(ld_shared_u32(from + 32));
-                        hi2 += __uint_as_float(ld_shared_u32(from + 36));
-                    }
-                }
+        if (there) {
+            constexpr int kPieces = kFeatures / 8;   // 8 features at a time
+            const int first = static_cast<int>(threadIdx.x) - 64, n = first % kPieces * 8, f = static_cast<int>(v0.z) + n;
+            const int m = EPI == EPI_GATED ? 2 * n : n;   // the accumulator's row
+            constexpr int kSums = EPI == EPI_GATED ? 16 : 8;
+            for (int item = first; item < part * kPieces; item += 32 * kEpi) {
+                const int row = item / kPieces;
                 const long long out_row = static_cast<long long>(v0.w) + share * part + row;
-                const int f = static_cast<int>(v0.z) + n;
                 if (out_row >= static_cast<int>(v1.x) || f >= p.features) continue;
-                uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + out_row * p.features + f);
+                float sum[kSums] = {};
+                for (int c = 0; c < split; ++c)
+#pragma unroll
+                    for (int i = 0; i < kSums; i += 4) {
+                        const uint4 w = ld_shared_v4(sEpi + ((c * part + row) * kRowsPerCta + m + i) * 4);
+                        sum[i] += __uint_as_float(w.x), sum[i + 1] += __uint_as_float(w.y);
+                        sum[i + 2] += __uint_as_float(w.z), sum[i + 3] += __uint_as_float(w.w);
+                    }
+                uint32_t o[4];
+                const long long at = out_row * p.features + f;
                 if constexpr (EPI == EPI_NONE) {
-                    *out = pack2<KIND>(__float_as_uint(lo), __float_as_uint(hi), p.out_scale);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = pack2<KIND>(__float_as_uint(sum[2 * i]), __float_as_uint(sum[2 * i + 1]), p.out_scale);
                 } else {
                     constexpr int kBoth = EPI == EPI_GATED ? 2 : 1;
-                    float2 b0 = make_float2(0.0f, 0.0f), b1 = b0, r = b0;
-                    if (p.bias) {
-                        const uint16_t *bias = static_cast<const uint16_t *>(p.bias) + static_cast<long long>(v0.y) * kBoth * p.features + f;
-                        b0 = unpack2<KIND>(ld_global(reinterpret_cast<const uint32_t *>(bias)));
-                        if constexpr (EPI == EPI_GATED) b1 = unpack2<KIND>(ld_global(reinterpret_cast<const uint32_t *>(bias + p.features)));
-                    }
-                    if (p.residual)
-                        r = unpack2<KIND>(ld_global(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.residual) + out_row * p.features + f)));
-                    lo = fmaf(lo, p.out_scale, b0.x), hi = fmaf(hi, p.out_scale, b0.y);
-                    lo2 = fmaf(lo2, p.out_scale, b1.x), hi2 = fmaf(hi2, p.out_scale, b1.y);
-                    if (p.z) {
-                        uint16_t *z = static_cast<uint16_t *>(p.z) + out_row * kBoth * p.features + f;
-                        *reinterpret_cast<uint32_t *>(z) = pack2f<KIND>(lo, hi);
-                        if constexpr (EPI == EPI_GATED) *reinterpret_cast<uint32_t *>(z + p.features) = pack2f<KIND>(lo2, hi2);
+                    uint4 r = join_res;
+                    if (p.residual && item != first) r = ld_global(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + at));
+                    const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int k = 0; k < kBoth; ++k) {
+                        const uint32_t bw[4] = {join_bias[k].x, join_bias[k].y, join_bias[k].z, join_bias[k].w};
+                        uint32_t zw[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 b = unpack2<KIND>(bw[i]);
+                            float *x = sum + 8 * k + 2 * i;
+                            x[0] = fmaf(x[0], p.out_scale, b.x), x[1] = fmaf(x[1], p.out_scale, b.y);
+                            zw[i] = pack2f<KIND>(x[0], x[1]);
+                        }
+                        if (p.z)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.z) + out_row * kBoth * p.features + k * p.features + f) = make_uint4(zw[0], zw[1], zw[2], zw[3]);
                     }
                     with_act(p.act, [&](auto tag) {
                         constexpr int A = decltype(tag)::value;
-                        lo = act<A>(lo), hi = act<A>(hi);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            sum[i] = act<A>(sum[i]);
+                            if constexpr (EPI == EPI_GATED) sum[i] *= sum[8 + i];
+                        }
                     });
-                    if constexpr (EPI == EPI_GATED) lo *= lo2, hi *= hi2;
-                    *out = pack2f<KIND>(lo + r.x, hi + r.y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 e = p.residual ? unpack2<KIND>(rw[i]) : make_float2(0.0f, 0.0f);
+                        o[i] = pack2f<KIND>(sum[2 * i] + e.x, sum[2 * i + 1] + e.y);
+                    }
                 }
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+        }
     }
 
     // ---- teardown ------------------------------------------------------------
@@ -934,6 +963,15 @@ struct ExpertInst {
         return cudaOccupancyMaxActiveClusters(clusters, expert_kernel<KIND, MODE, CG, BN, EPI>, &cfg);
     }
 
+    // Clusters of so many CTAs that the device holds.
+    static cudaError_t fit(int cluster, int smem, int *clusters)
+    {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        config(cfg, attr, cluster, cluster, smem, nullptr, false);
+        return cudaOccupancyMaxActiveClusters(clusters, expert_kernel<KIND, MODE, CG, BN, EPI>, &cfg);
+    }
+
     static cudaError_t launch(const LinearMaps &maps, const ExpertParams &p, int grid, int smem, cudaStream_t stream, bool overlap)
     {
         cudaLaunchConfig_t cfg;
@@ -942,7 +980,7 @@ struct ExpertInst {
         return cudaLaunchKernelEx(&cfg, expert_kernel<KIND, MODE, CG, BN, EPI>, static_cast<const MapsOf<EPI> &>(maps), p);
     }
 
-    static ExpertOps ops() { return ExpertOps{&prepare, &launch}; }
+    static ExpertOps ops() { return ExpertOps{&prepare, &launch, &fit}; }
 };
 
 }  // namespace pts

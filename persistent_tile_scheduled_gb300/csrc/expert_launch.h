@@ -78,6 +78,7 @@ constexpr int64_t kExpertFewRows = 32;  // at most so many on average
 struct ExpertOps {
     cudaError_t (*prepare)(int smem, int sms, int *clusters);
     cudaError_t (*launch)(const LinearMaps &maps, const ExpertParams &p, int grid, int smem, cudaStream_t stream, bool overlap);
+    cudaError_t (*fit)(int cluster, int smem, int *clusters);
 };
 
 // kind: 0 fp16, 1 bf16, 2 e4m3 (forward only); bn: kExpertTileN, or

@@ -75,6 +75,7 @@ struct gemm_ctx {
     // 2: single CTAs with the short row tile); 0 = not asked yet
     int expert_clusters[3][3][3] = {};
     int linear_clusters[3][2][3] = {};        // gemm_run_linear: the same per dtype, plain or gated, and variant
+    int linear_shared[3][2][3] = {};          // and clusters of 2, 4 and 8 CTAs that share a tile
     bool sort_smem[2] = {};                   // gemm_expert_sort: limits raised, per kernel
     pts::NibPrepared nibble[2] = {};          // gemm_run_nibble, per dtype
 };
