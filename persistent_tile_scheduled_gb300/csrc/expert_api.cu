@@ -90,11 +90,20 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     // 16 tiles of that contraction take 20.7 by 8 CTAs each, 14.6 by 4.
     int split = 1;
     const int64_t length_kb = (contraction + kelems - 1) / kelems;
-    if (mode == EXPERT_FWD && bn == kExpertTileNFew && h->opts.cta_group == 0 && h->opts.max_clusters == 0 && length_kb >= 24) {
-        // (of an epilogue's kernels only what fits at once: 38 tiles by 4 are 152 CTAs, but the
-        // device's parts hold fewer clusters of 4)
+    const bool share = mode == EXPERT_FWD && bn == kExpertTileNFew && h->opts.cta_group == 0 && h->opts.max_clusters == 0;
+    if (share && !epi && length_kb >= 24) {
+        while (split < 4 && tiles * split * 2 <= h->sm_count) split *= 2;
+        if (split == 4 && length_kb >= 64 && tiles * 16 <= h->sm_count) split = 8;
+        if (split == 2 && length_kb < 32) split = 1;
+    }
+    if (share && epi) {
+        // With an epilogue, where joining costs 1.5 us, only as many as fit at once (24 rows, us
+        // by 1 / 2 / 4 / 8 CTAs: of 1024 x 512 5.0 / 4.1 / 4.0 / 4.3, of 1024 x 2048 11.0 / 7.2 /
+        // 5.5 / 5.1, of 2048 x 1024 7.1 / 5.2 / 4.7 / 8.5 (16 clusters of 8 do not fit), of 4096
+        // x 512 5.2 / 4.3 / 5.0, x 1024 7.2 / 5.4 / 5.6, x 4096 19.8 / 12.1 / 9.7, of 4864 x 4096
+        // 19.7 / 12.2 / 17.8 (38 of 4 do not), of 9728 x 1024 8.0 / 7.6).
         const auto fits = [&](int cluster) -> bool {
-            if (!epi) return true;
+            if (tiles * cluster > h->sm_count) return false;
             int &n = h->linear_shared[kind][gated][cluster / 4];
             if (n == 0 && (ops.fit(cluster, smem, &n) != cudaSuccess || n < 1)) {
                 cudaGetLastError();
@@ -102,9 +111,9 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
             }
             return tiles <= n;
         };
-        while (split < 4 && tiles * split * 2 <= h->sm_count && fits(2 * split)) split *= 2;
-        if (split == 4 && length_kb >= 64 && tiles * 16 <= h->sm_count && fits(8)) split = 8;
-        if (split == 2 && length_kb < 32) split = 1;
+        if (length_kb >= 8 && fits(2)) split = 2;
+        if (length_kb >= (tiles * 8 <= h->sm_count ? 8 : 24) && fits(4)) split = 4;
+        if (length_kb >= 24 && fits(8)) split = 8;
     }
 
     LinearMaps m;
@@ -227,9 +236,9 @@ bool few_rows(const gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64
     // (told which variant of the others to take, or to let a wait run out, it takes one of those)
     if (!is16(dtype) || h->opts.cta_group != 0 || h->opts.max_clusters != 0 || (h->opts.debug_flags & GEMM_DEBUG_FAULT_SKIP_TMA)) return false;
     // Up to 8 rows a matrix is read once from memory; of the 9th on a second time, from
-    // L2 (us, this / through shared memory: one row of 4096^2 gated 13.1 / 17.3, 8 13.4 /
-    // 17.5, 9 18.4 / 17.6; 1 of 1024^2 3.1 / 7.6; 16 over 8 experts of 4096^2 38.3 /
-    // 45.3, 40 44.2 / 47.2, 64 50 / 47.7).
+    // L2 (us, this / through shared memory: one row of 1024^2 3.6 / 4.0, of 4096^2 8.3 / 9.5,
+    // 8 of 4096 x 8192 13.6 / 14.6, 9 19.9 / 14.7; of 8192^2 either 24.5; 16 over 8 experts
+    // of 4096^2 43.8 / 45.4, 40 44.8 / 45.7, 64 45.3 / 45.8; 64 over 32 of 512^2 7.7 / 7.5).
     return K > 0 && rows <= kLinearRowsMax && experts <= kLinearRowsMax && rows <= (experts == 1 ? 8 : 5 * experts)
            && rows_items(rows, experts, N, gated) <= kIntMax;
 }
