@@ -19,17 +19,21 @@ struct RowBlocks {
     // (at most max_blocks, which ascending offsets do not pass)
     __device__ void make(const LinearRowsParams &p, int max_blocks) const
     {
+        if (!p.offsets) {   // (one matrix)
+            const int n = (p.rows + 7) / 8;
+            for (int b = threadIdx.x; b < n; b += kRowsThreads) block[b] = make_int2((p.rows - 8 * b < 8 ? p.rows - 8 * b : 8) << 16, 8 * b);
+            if (threadIdx.x == 0) *count = n;
+            __syncthreads();
+            return;
+        }
         int carry = 0;
         for (int e0 = 0; e0 < p.experts; e0 += kRowsThreads) {
             const int e = e0 + static_cast<int>(threadIdx.x);
             int lo = 0, hi = 0;
             if (e < p.experts) {
-                hi = p.rows;
-                if (p.offsets) {
-                    lo = ld_global(p.offsets + e), hi = ld_global(p.offsets + e + 1);
-                    lo = lo < 0 ? 0 : (lo > p.rows ? p.rows : lo);
-                    hi = hi < lo ? lo : (hi > p.rows ? p.rows : hi);
-                }
+                lo = ld_global(p.offsets + e), hi = ld_global(p.offsets + e + 1);
+                lo = lo < 0 ? 0 : (lo > p.rows ? p.rows : lo);
+                hi = hi < lo ? lo : (hi > p.rows ? p.rows : hi);
             }
             const int mine = (hi - lo + 7) / 8, first = rows_scan(mine, carry, count + 1);
             for (int b = 0; b < mine && first + b < max_blocks; ++b) {
@@ -54,13 +58,35 @@ struct LinearSource {
     {
         return static_cast<const uint16_t *>(p.x) + static_cast<long long>(blocks.block[b].y + place) * p.K;
     }
-    __device__ __forceinline__ void finish(int b, int place, int have, long long e, int f, float (&s)[4], bool two) const
+    struct Early {
+        uint32_t bias[2], residual[2][2];   // [token][feature f, f + 8]
+    };
+    __device__ __forceinline__ Early early(int b, int have, int f, bool two) const
+    {
+        Early v{};
+        if (p.bias) {
+            const uint16_t *bias = static_cast<const uint16_t *>(p.bias) + expert(b) * p.N * (GATED ? 2 : 1);
+            v.bias[0] = ld_global(bias + f);
+            if (two) v.bias[1] = ld_global(bias + (GATED ? p.N + f : f + 8));
+        }
+        if (p.residual) {
+            const int place = 2 * static_cast<int>(lane_id() & 3u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (place + i >= have) break;
+                const uint16_t *r = static_cast<const uint16_t *>(p.residual) + static_cast<long long>(blocks.block[b].y + place + i) * p.N + f;
+                v.residual[i][0] = ld_global(r);
+                if (!GATED && two) v.residual[i][1] = ld_global(r + 8);
+            }
+        }
+        return v;
+    }
+    __device__ __forceinline__ void finish(int b, int place, int have, int f, float (&s)[4], bool two, const Early &early) const
     {
         constexpr int kBoth = GATED ? 2 : 1;
-        const int f2 = GATED ? p.N + f : f + 8;   // of bias and Z
+        const int f2 = GATED ? p.N + f : f + 8;   // of Z
         if (p.bias) {
-            const uint16_t *bias = static_cast<const uint16_t *>(p.bias) + e * p.N * kBoth;
-            const float b0 = unpack1<KIND>(ld_global(bias + f)), b1 = two ? unpack1<KIND>(ld_global(bias + f2)) : 0.0f;
+            const float b0 = unpack1<KIND>(early.bias[0]), b1 = unpack1<KIND>(early.bias[1]);
             s[0] += b0, s[1] += b0, s[2] += b1, s[3] += b1;
         }
 #pragma unroll
@@ -86,9 +112,8 @@ struct LinearSource {
             const long long at = static_cast<long long>(blocks.block[b].y + place + i) * p.N + f;
             const bool second = !GATED && two;
             if (p.residual) {
-                const uint16_t *r = static_cast<const uint16_t *>(p.residual) + at;
-                s[i] += unpack1<KIND>(ld_global(r));
-                if (second) s[2 + i] += unpack1<KIND>(ld_global(r + 8));
+                s[i] += unpack1<KIND>(early.residual[i][0]);
+                if (second) s[2 + i] += unpack1<KIND>(early.residual[i][1]);
             }
             uint16_t *c = static_cast<uint16_t *>(p.c) + at;
             const uint32_t both = pack2f<KIND>(s[i], s[2 + i]);
@@ -106,8 +131,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const Line
     blocks.block = reinterpret_cast<int2 *>(smem + rows_part_bytes(1, kw));
     blocks.count = reinterpret_cast<int *>(blocks.block + max_blocks);
     pdl_launch_dependents();
-    pdl_wait();
+    if (p.offsets) pdl_wait();
     blocks.make(p, max_blocks);
+    if (!p.offsets) pdl_wait();
     stream_items<KIND, GATED, 1, SHARED>(LinearSource<KIND, GATED>{p, blocks}, static_cast<const uint16_t *>(p.w), p.N, p.K,
                                  reinterpret_cast<float *>(smem), kw, ctas);
 }

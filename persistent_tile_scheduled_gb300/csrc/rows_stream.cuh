@@ -167,7 +167,9 @@ __device__ __forceinline__ int rows_scan(int mine, int &carry, int *sums)
 // Source: what a block is:
 //   count(), expert(b), have(b)          blocks; a block's expert and tokens
 //   row(b, place)                        a token's row of the operand
-//   finish(b, place, have, e, f, s, two) s[0], s[1]: feature f of tokens place and place + 1, s[2], s[3]:
+//   early(b, have, f, two)               what finish adds, loaded when the item begins: bias, residual
+//   finish(b, place, have, f, s, two, early)
+//                                        s[0], s[1]: feature f of tokens place and place + 1, s[2], s[3]:
 //                                        feature f + 8 (gated: the gate's f and the other's f)
 template <int KIND, bool GATED, int NB, bool SHARED, class Source>
 __device__ __forceinline__ void stream_items(const Source &source, const uint16_t *weights, int features, int width, float *part, int kw, int ctas)
@@ -202,11 +204,15 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
     RowsStream<KIND, NB> stream;
     int item = static_cast<int>(blockIdx.x) / ctas + static_cast<int>(gridDim.x) * team;
     const int only = item;
+    typename Source::Early early{};
     RowsGroup<NB> group = group_of(item, first);
     stream.start_w(group);
     stream.start_x(group);
     for (int n = 0; item < items; item += step, ++n) {
         const int b = item / tiles, f = (item - b * tiles) * kFeatures + g, have = source.have(b);
+        const bool two = GATED || f + 8 < features;
+        const int turn = n % kw, bar = 1 + team * kw + turn;
+        if (NB == 1 && member == turn) early = source.early(b, have, f, two);   // (by 32 the registers are taken)
         float acc[NB][4] = {};
         for (int at = first; at < end; at += kChunks) {
             const bool more = at + kChunks < end;
@@ -217,7 +223,6 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
         // Over the team's warps: one of them in turn, the others run on.  It waits for all
         // at this item, so every warp does once in kw items: none can come back to an
         // item's place (and barrier) before its reader is through with it.
-        const int turn = n % kw, bar = 1 + team * kw + turn;
         float *mine = part + (team * kw + turn) * kw * NB * 128;   // [member][NB][32 lanes][4]
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -227,6 +232,7 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
             continue;
         }
         asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * kw) : "memory");
+        if (NB > 1) early = source.early(b, have, f, two);
         // a lane has rows g and g + 8 of two tokens
         for (int nb = 0; nb < NB && 8 * nb < have; ++nb) {
             float s[4] = {};
@@ -237,7 +243,7 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
             if constexpr (SHARED)   // (where the first warp's were, which only this lane has read)
                 *reinterpret_cast<float4 *>(mine + (nb * 32 + lane) * 4) = make_float4(s[0], s[1], s[2], s[3]);
             else
-                source.finish(b, 8 * nb + 2 * (lane & 3), have, source.expert(b), f, s, GATED || f + 8 < features);
+                source.finish(b, 8 * nb + 2 * (lane & 3), have, f, s, two, early);
         }
     }
     if constexpr (SHARED) {
@@ -250,7 +256,7 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
                     const float4 q = ld_cluster_f32x4(mapa(smem_u32(part + (nb * 32 + lane) * 4), static_cast<uint32_t>(c)));
                     s[0] += q.x, s[1] += q.y, s[2] += q.z, s[3] += q.w;
                 }
-                source.finish(b, 8 * nb + 2 * (lane & 3), have, source.expert(b), f, s, GATED || f + 8 < features);
+                source.finish(b, 8 * nb + 2 * (lane & 3), have, f, s, GATED || f + 8 < features, early);
             }
         }
         cluster_sync();
