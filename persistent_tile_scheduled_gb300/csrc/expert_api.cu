@@ -394,7 +394,7 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, int64_t rows, int64_t experts, in
         p.offsets = offsets;
         p.c = C;
         p.z = Z;
-        return launched(launch_linear_rows(static_cast<int>(dtype), p, h->sm_count, static_cast<cudaStream_t>(stream), overlap(h)));
+        return launched(launch_linear_rows(static_cast<int>(dtype), p, rows_room(h), static_cast<cudaStream_t>(stream), overlap(h)));
     }
     const Epilogue epi{bias, residual, Z, act};
     return run_product(h, EXPERT_FWD, rows, experts, N, K, B, A, offsets, C, dtype, scale, static_cast<cudaStream_t>(stream), &epi);

@@ -32,6 +32,12 @@ inline gemm_status_t on_device(const gemm_ctx *h)
     return cudaSetDevice(h->device) == cudaSuccess ? GEMM_OK : cuda_fail(cudaErrorInvalidDevice);
 }
 
+inline const RowsRoom &rows_room(gemm_ctx *h)
+{
+    if (h->rows_room.clusters[1] == 0) ask_rows_room(h->rows_room, h->sm_count);
+    return h->rows_room;
+}
+
 inline bool overlap(const gemm_ctx *h) { return h->opts.overlap_launch >= 0; }
 
 }  // namespace pts

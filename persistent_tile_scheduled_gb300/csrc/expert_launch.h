@@ -106,7 +106,14 @@ struct LinearRowsParams {
 };
 constexpr int kLinearRowsMax = 1024;   // rows, and experts: tables in shared memory
 
-cudaError_t launch_linear_rows(int kind, const LinearRowsParams &p, int sms, cudaStream_t stream, bool overlap);
+// Clusters of 1, 2, 4 or 8 of these kernels' CTAs (two to an SM) that the device holds at once:
+// fewer CTAs than there is room for, since its parts are no multiples of a cluster.
+struct RowsRoom {
+    int clusters[9];   // [CTAs of a cluster]; [1] 0: not asked yet
+};
+void ask_rows_room(RowsRoom &room, int sms);
+
+cudaError_t launch_linear_rows(int kind, const LinearRowsParams &p, const RowsRoom &room, cudaStream_t stream, bool overlap);
 
 // ---- rows to the experts and back (expert_route.cu) ---------------------------
 

@@ -131,8 +131,7 @@ gemm_status_t gemm_expert_layer(gemm_handle_t h, int64_t tokens, int64_t top_k, 
     p.residual = residual;
     p.hs = Hs;
     p.y = Y;
-    p.sms = h->sm_count;
-    return launched((dtype == GEMM_F16 ? launch_layer_f16 : launch_layer_bf16)(p, static_cast<cudaStream_t>(stream), overlap(h)));
+    return launched((dtype == GEMM_F16 ? launch_layer_f16 : launch_layer_bf16)(p, rows_room(h), static_cast<cudaStream_t>(stream), overlap(h)));
 }
 
 }  // extern "C"

@@ -49,10 +49,10 @@ struct LayerParams {
     const float *weights;
     const void *up, *up_bias, *down, *down_bias, *residual;
     void *hs, *y;
-    int32_t sms;
 };
 
-cudaError_t launch_layer_f16(const LayerParams &p, cudaStream_t stream, bool overlap);
-cudaError_t launch_layer_bf16(const LayerParams &p, cudaStream_t stream, bool overlap);
+struct RowsRoom;   // expert_launch.h
+cudaError_t launch_layer_f16(const LayerParams &p, const RowsRoom &room, cudaStream_t stream, bool overlap);
+cudaError_t launch_layer_bf16(const LayerParams &p, const RowsRoom &room, cudaStream_t stream, bool overlap);
 
 }  // namespace pts

@@ -140,14 +140,35 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const Line
 
 }  // namespace
 
-cudaError_t launch_linear_rows(int kind, const LinearRowsParams &p, int sms, cudaStream_t stream, bool overlap)
+void ask_rows_room(RowsRoom &room, int sms)
+{
+    room.clusters[1] = 2 * sms;
+    for (int c = 2; c <= 8; c *= 2) {
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(c);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(c));
+        cfg.blockDim = dim3(kRowsThreads);
+        cfg.dynamicSmemBytes = rows_part_bytes(1, 8);
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&room.clusters[c], linear_rows_kernel<0, false, true>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            room.clusters[c] = 0;
+        }
+    }
+}
+
+cudaError_t launch_linear_rows(int kind, const LinearRowsParams &p, const RowsRoom &room, cudaStream_t stream, bool overlap)
 {
     const bool gated = p.act & ACT_GATED;
     const int blocks = p.experts == 1 ? (p.rows + 7) / 8 : (p.rows < p.experts ? p.rows : p.experts) + p.rows / 8;
     const int features = gated ? 8 : 16, tiles = (p.N + features - 1) / features;
     const long long items = static_cast<long long>(blocks) * tiles;
-    const int kw = rows_kw(items, p.K, sms), ctas = rows_ctas(items, p.K, sms), teams = kRowsWarps / kw;
-    const long long most = 2 * sms / ctas, wanted = (items + teams - 1) / teams, clusters = wanted < most ? wanted : most;
+    const int kw = rows_kw(items, p.K, room), ctas = rows_ctas(items, p.K, room), teams = kRowsWarps / kw;
+    const long long most = room.clusters[ctas], wanted = (items + teams - 1) / teams, clusters = wanted < most ? wanted : most;
     const size_t smem = rows_part_bytes(1, kw) + RowBlocks::bytes(blocks);
     static_assert(rows_part_bytes(1, 8) + RowBlocks::bytes(kLinearRowsMax + kLinearRowsMax / 8) <= 48 * 1024, "");
     const auto run = [&](auto kernel) {

@@ -11,6 +11,7 @@
 // experts of 4096 x 16384, 122 us), and some 3 us to start and end a launch.
 #pragma once
 #include "activation.cuh"
+#include "expert_launch.h"
 #include "launch.cuh"
 #include "ptx.cuh"
 
@@ -264,18 +265,21 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
 }
 
 // CTAs of a cluster for at most so many items: one wave of clusters, and stretches of
-// 4 chunks a warp at least (one row of 1024 x 8192: 4 CTAs to each of 64 items).
-inline int rows_ctas(long long items, int width, int sms)
+// 4 chunks a warp at least (one row of 1024 x 8192: 4 CTAs to each of 64 items).  Powers
+// of 2: others find less room than they are said to (one row of 1536 x 8192, 96 items, by
+// 3 8.2 us, by 2 7.5).
+inline int rows_ctas(long long items, int width, const RowsRoom &room)
 {
     int ctas = 1;
-    while (ctas < 8 && items * ctas * 2 <= 2 * sms && width >= 32 * 4 * kRowsWarps * 2 * ctas) ctas *= 2;
+    for (int c = 2; c <= 8; c *= 2)
+        if (items <= room.clusters[c] && width >= 32 * 4 * kRowsWarps * c) ctas = c;
     return ctas;
 }
 
 // Warps of a team (blocks of 8): all, unless half of them have a full group each and
 // there are items for more teams (8 rows of 8192 x 1024 5.6 us by 4, 6.7 by 8; but
 // one of 1024^2 3.5 and 3.1, and of 4096 x 8192 17 and 13.2).
-inline int rows_kw(long long items, int width, int sms) { return width < 64 * 32 && items > 2 * sms ? 4 : 8; }
+inline int rows_kw(long long items, int width, const RowsRoom &room) { return width < 64 * 32 && items > room.clusters[1] ? 4 : 8; }
 
 // Shared memory of the sums.
 __host__ __device__ constexpr size_t rows_part_bytes(int nb, int kw) { return static_cast<size_t>(kRowsWarps) * kw * nb * 512; }
