@@ -179,13 +179,14 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
 
     pdl_launch_dependents();
     // The offsets and operands may be the previous grid's outputs.  One matrix's tiles need
-    // nothing of it: they are handed out before, and only the loads wait.
+    // nothing of it: the first is handed out before, and only the loads wait.
     const bool early = EPI != EPI_NONE && !p.offsets;
     if (!early || (warp != 0 && warp != kScheduler)) pdl_wait();
 
     // ---- work-item broadcast ring (as in gemm_kernel.cuh) ---------------------
     auto publish = [&](int i, bool valid, const ExpertItem &t) -> bool {
         const int slot = i % kRing;
+        if (early && i == 1) pdl_wait();   // (no bounded wait runs while the grid before does)
         if (i >= kRing && !ctl.wait_all(ring_empty0 + 8 * slot, ((i / kRing) & 1) ^ 1, WHERE_RING_EMPTY))
             return false;
         if (lane == 0) {
