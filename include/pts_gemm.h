@@ -444,7 +444,8 @@ typedef enum {
 } gemm_act_t;
 
 /* Z[r] = A[r] . B_e + bias_e and C[r] = act(Z[r]) + residual[r] for every row r
- * of every expert e, one launch.  As gemm_run_experts, and
+ * of every expert e, in one launch (two where a second wave of tiles would be
+ * short).  As gemm_run_experts, and
  *   offsets   as there, or NULL with experts == 1: every row uses that matrix;
  *   B         experts x N' x K with N' = N, gated 2N;
  *   bias      experts x N', of C's type, or NULL;

@@ -96,25 +96,34 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
         if (split == 4 && length_kb >= 64 && tiles * 16 <= h->sm_count) split = 8;
         if (split == 2 && length_kb < 32) split = 1;
     }
-    if (share && epi) {
-        // With an epilogue, where joining costs 1.5 us, only as many as fit at once (24 rows, us
-        // by 1 / 2 / 4 / 8 CTAs: of 1024 x 512 5.0 / 4.1 / 4.0 / 4.3, of 1024 x 2048 11.0 / 7.2 /
-        // 5.5 / 5.1, of 2048 x 1024 7.1 / 5.2 / 4.7 / 8.5 (16 clusters of 8 do not fit), of 4096
-        // x 512 5.2 / 4.3 / 5.0, x 1024 7.2 / 5.4 / 5.6, x 4096 19.8 / 12.1 / 9.7, of 4864 x 4096
-        // 19.7 / 12.2 / 17.8 (38 of 4 do not), of 9728 x 1024 8.0 / 7.6).
+    // With an epilogue, where joining costs 1.5 us, only as many as fit at once (24 rows, us
+    // by 1 / 2 / 4 / 8 CTAs: of 1024 x 512 5.0 / 4.1 / 4.0 / 4.3, of 1024 x 2048 11.0 / 7.2 /
+    // 5.5 / 5.1, of 2048 x 1024 7.1 / 5.2 / 4.7 / 8.5 (16 clusters of 8 do not fit), of 4096
+    // x 512 5.2 / 4.3 / 5.0, x 1024 7.2 / 5.4 / 5.6, x 4096 19.8 / 12.1 / 9.7, of 4864 x 4096
+    // 19.7 / 12.2 / 17.8 (38 of 4 do not), of 9728 x 1024 8.0 / 7.6).
+    const auto split_of = [&](int64_t n) -> int {
         const auto fits = [&](int cluster) -> bool {
-            if (tiles * cluster > h->sm_count) return false;
-            int &n = h->linear_shared[kind][gated][cluster / 4];
-            if (n == 0 && (ops.fit(cluster, smem, &n) != cudaSuccess || n < 1)) {
+            if (n * cluster > h->sm_count) return false;
+            int &room = h->linear_shared[kind][gated][cluster / 4];
+            if (room == 0 && (ops.fit(cluster, smem, &room) != cudaSuccess || room < 1)) {
                 cudaGetLastError();
-                n = -1;
+                room = -1;
             }
-            return tiles <= n;
+            return n <= room;
         };
-        if (length_kb >= 8 && fits(2)) split = 2;
-        if (length_kb >= (tiles * 8 <= h->sm_count ? 8 : 24) && fits(4)) split = 4;
-        if (length_kb >= 24 && fits(8)) split = 8;
-    }
+        int by = 1;
+        if (length_kb >= 8 && fits(2)) by = 2;
+        if (length_kb >= (n * 8 <= h->sm_count ? 8 : 24) && fits(4)) by = 4;
+        if (length_kb >= 24 && fits(8)) by = 8;
+        return by;
+    };
+    if (share && epi) split = split_of(tiles);
+    // One matrix's tiles that are more than the SMs, but less than twice as many, would take
+    // two waves: those of the second are shared, in a launch of their own (16 rows, two launches
+    // / one: of 2 x 11008 x 4096 36.6 / 42.2, of 2 x 13824 x 4096 42.7 / 43.6, of 28672 x 8192
+    // 79 / 84).
+    const int64_t rest = share && epi && !offsets && tiles == tf && length_kb >= 24 && overlap(h) ? tiles - h->sm_count : 0;
+    const int rest_split = rest > 0 && rest < h->sm_count ? split_of(rest) : 1;
 
     LinearMaps m;
     std::memset(&m, 0, sizeof(m));
@@ -162,6 +171,18 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
         p.bias = epi->bias;
         p.residual = epi->residual;
         p.z = epi->z;
+    }
+    p.tiles_f = static_cast<int32_t>(tf);
+    if (rest_split > 1) {
+        p.tiles_f = h->sm_count;
+        p.chain = 1;
+        const gemm_status_t st = launched(ops.launch(m, p, h->sm_count, smem, stream, true));
+        if (st != GEMM_OK) return st;
+        p.tile0 = h->sm_count;
+        p.tiles_f = static_cast<int32_t>(rest);
+        p.chain = 2;
+        p.split = rest_split;
+        return launched(ops.launch(m, p, static_cast<int>(rest) * rest_split, smem, stream, true));
     }
     return launched(ops.launch(m, p, static_cast<int>(clusters) * cg * split, smem, stream, overlap(h)));
 }

@@ -177,11 +177,15 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
     const uint32_t tmem_base = ld_shared_u32(tmem_slot);
     const uint32_t one = lane == 0 ? 1u : 0u;
 
-    pdl_launch_dependents();
     // The offsets and operands may be the previous grid's outputs.  One matrix's tiles need
-    // nothing of it: the first is handed out before, and only the loads wait.
-    const bool early = EPI != EPI_NONE && !p.offsets;
-    if (!early || (warp != 0 && warp != kScheduler)) pdl_wait();
+    // nothing of it: the first is handed out before, and only the loads wait.  Of two
+    // launches that share a product's tiles the first lets the second start when it has
+    // waited itself; the second then reads what the first reads, and waits for it at its end.
+    const bool first = EPI != EPI_NONE && p.chain == 1, second = EPI != EPI_NONE && p.chain == 2;
+    const bool early = EPI != EPI_NONE && !p.offsets && !first && !second;
+    if (!first) pdl_launch_dependents();
+    if (!second && (!early || (warp != 0 && warp != kScheduler))) pdl_wait();
+    if (first) pdl_launch_dependents();
 
     // ---- work-item broadcast ring (as in gemm_kernel.cuh) ---------------------
     auto publish = [&](int i, bool valid, const ExpertItem &t) -> bool {
@@ -695,7 +699,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
         // ============================== scheduler ==============================
         // Tile w of all experts' tiles in order, w = cluster, cluster + grid, ...
         if (leader) {
-            const int tiles_f = (p.features + kFeatures * CG - 1) / (kFeatures * CG);
+            const int tiles_f = EPI != EPI_NONE ? p.tiles_f : (p.features + kFeatures * CG - 1) / (kFeatures * CG);
             bool ok = true;
             int i = 0;
             auto offset = [&](int e) -> int {   // clamped, so that no offsets lead outside the arrays
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
                         const int size = ((ecnt - 1) / etn + kGran) / kGran * kGran;
                         ExpertItem t;
                         t.e = e0 + src;
-                        t.f0 = itf * (kFeatures * CG);
+                        t.f0 = (EPI != EPI_NONE ? p.tile0 + itf : itf) * (kFeatures * CG);
                         t.row0 = elo + it * size;
                         t.row_end = elo + ((it + 1) * size < ecnt ? (it + 1) * size : ecnt);
                         const int rows = t.row_end - t.row0;
@@ -919,6 +923,7 @@ __global__ void __launch_bounds__(expert_threads(MODE, EPI), 1)
         tc_fence_after();
         tmem_dealloc<CG>(tmem_base, kAccCols);
     }
+    if (second) pdl_wait();   // (what comes after this grid comes after the first too)
 }
 
 template <int KIND, int MODE, int CG, int BN, int EPI = EPI_NONE>

@@ -37,6 +37,8 @@ struct ExpertParams {
     int32_t act;              // gemm_act_t
     const void *bias, *residual;   // experts x N', rows x N, or null
     void *z;                  // rows x N', or null
+    int32_t tile0, tiles_f;   // first tile of features and tiles of this launch
+    int32_t chain;            // 1: another launch takes the other tiles, 2: this is it
 };
 
 // Tensor maps of a product, and of one with an epilogue.

@@ -186,6 +186,36 @@ def test_calls_on_several_streams_at_once(h):
             assert all(torch.equal(x, y) for x, y in zip(a.results(), results))
 
 
+@pytest.mark.parametrize("N,act,dtype", [(19456 + 8, 2, F16), (22528, SILU, BF16), (28000, 0, F16), (9736, SILU | GATED, BF16), (14336, 3 | GATED, F16), (22528, 1, pts.GEMM_E4M3)])
+@pytest.mark.parametrize("rows", [9, 24, 32])
+def test_a_wave_and_a_part(h, rows, N, act, dtype):
+    """Tiles that are more than the SMs but less than twice as many, as one of two products queued one after the other: the second
+    reads all that the first has written, and neither writes before the call in front has read."""
+    K = 2048 if dtype != pts.GEMM_E4M3 else 4096
+    all_, out = N * (2 if act & GATED else 1), torch.bfloat16 if dtype != F16 else torch.float16
+    t = {F16: torch.float16, BF16: torch.bfloat16, pts.GEMM_E4M3: torch.float8_e4m3fn}[dtype]
+    A, B = rand((rows, K), torch.float32, 1).clamp(-448, 448).to(t), large((all_, K), torch.float32, 2, 1.0 if dtype == pts.GEMM_E4M3 else K ** -0.5).clamp(-448, 448).to(t)
+    scale = K ** 0.5 if dtype == pts.GEMM_E4M3 else 1.0
+    bias, res = rand((1, all_), out, 3), rand((rows, N), out, 4)
+    back = large((64, N), out, 5, N ** -0.5)
+    C, Z, D = torch.zeros(rows, N, dtype=out, device="cuda"), torch.zeros(rows, all_, dtype=out, device="cuda"), torch.zeros(8, rows, 64, dtype=out, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(8):   # C starts as the residual, so every call changes it
+        C.copy_(res) if i % 4 == 0 else None
+        pts.gemm_run_linear(h, rows, 1, N, K, A, B, bias, C, None, C, Z, act, dtype, 1.0, float(torch.tensor(scale).float()))
+        pts.gemm_run_linear(h, rows, 1, 64, N, C, back, None, None, None, D[i], None, 0, F16 if out == torch.float16 else BF16)
+    torch.cuda.synchronize()
+    assert torch.equal(D[:4], D[4:])
+    last = C.clone()
+    C.copy_(res)
+    pts.gemm_run_linear(h, rows, 1, N, K, A, B, bias, C, None, C, Z, act, dtype, 1.0, float(torch.tensor(scale).float()))
+    (c, dc), (z, dz) = ref.linear(act, A, B, bias[0], res, float(torch.tensor(scale).float()))
+    ref.close(C, c, dc, "C")
+    ref.close(Z, z, dz, "Z")
+    (d, dd), _ = ref.linear(0, last, back)
+    ref.close(D[3], d, dd, "D")
+
+
 def test_products_that_are_refused(h):
     x = torch.zeros(1 << 16, dtype=torch.float16, device="cuda").data_ptr()
     off = offsets_of([8, 0]).data_ptr()
