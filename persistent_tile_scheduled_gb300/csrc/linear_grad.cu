@@ -8,7 +8,7 @@
 // in the same order, without atomics and without a workspace (two captured graphs
 // share nothing).
 //
-// The bytes bound it: 16384 rows of 8192 columns, bf16, 805 MB in 134 us, 6.0 TB/s (0.89
+// The bytes bound it: 16384 rows of 8192 columns, bf16, 805 MB in 133 us, 6.0 TB/s (0.89
 // of the copy bandwidth; relu^2, which computes next to nothing, 133).  Loading the next
 // rows while the last are computed took it there from 162; two values to an instruction
 // (f32x2) keep the arithmetic out of the way.
@@ -144,26 +144,31 @@ template <int KIND, bool GATED>
 cudaError_t go(const LinearGradParams &p, cudaStream_t stream, bool overlap)
 {
     // Blocks of 64 columns, and as many CTAs of 512 threads (two to an SM; gated, with more
-    // registers, of 256) to one as make a single wave, 8 at most; blocks of 32 where columns
-    // are few, then also 16 CTAs of 256 threads (us, gelu's tanh form, bf16: 16384 rows of
-    // 8192 128 blocks by 2 133, by 4 of 256 threads 134, by 8 142; of 2048 32 by 8 38.5,
-    // 64 blocks of 32 columns by 4 44; of 1024 32 of 32 by 8 24.5, 16 of 64 by 16 29.7; of
-    // 512 16 of 32 by 16 of 256 threads 17.2, by 8 19.1; 3326 over 8 experts of 272 gated
-    // 5.8, of 512 threads 8.9).  Rows that are no multiple of 32 bytes share those at a
-    // block's edges: blocks of 128 columns (9115 rows of 7000 75, of 64 84).  More experts
-    // and columns than a wave holds: wider blocks, which take one (4101 over 16 experts of
-    // 2048 gated 17.0, of 64 columns 19.3; of 4568 34.6 and 40.4).
+    // registers, one, and two of 256) to one as make a single wave, 8 at most; blocks of 32
+    // where columns are few, then also 16 CTAs of 256 threads (us, gelu's tanh form, bf16:
+    // 16384 rows of 8192 128 blocks by 2 133, by 4 of 256 threads 134, by 8 142; of 2048 32
+    // by 8 38.5, 64 blocks of 32 columns by 4 44; of 1024 32 of 32 by 8 24.5, 16 of 64 by 16
+    // 29.7; of 512 16 of 32 by 16 of 256 threads 17.2, by 8 19.1; 9115 gated of 1024 by 256
+    // threads 21, by 512 33).  Rows that are no multiple of 32 bytes share those at a
+    // block's edges: blocks of 128 columns (9115 rows of 7000 76, of 64 84).
+    // Experts' rows are uneven: where there are many of them a block is shared although a
+    // wave is full, so that the largest does not end last (16384 over 8 of 2048, uneven as
+    // exp of half a normal / even: 54 / 41, not shared 67 / 37; gated 67 / 68, 76 / 61).
+    // Few rows each and more blocks than five waves: wider ones (4000 over 64 of 4096 35 /
+    // 20, of 64 columns 32 / 30; gated 44 / 33, 51 / 50).
     // Clusters need not be whole where nothing is added up.
     const int64_t pieces = p.N / 8, each = p.rows / p.experts, by8 = p.experts * ((pieces + 7) / 8);
-    const bool fills = p.dbias && by8 > p.sms && by8 <= 2 * p.sms;   // (a wave without sharing)
-    int64_t tx = by8 * 8 <= p.sms ? 4 : p.N % 16 && by8 >= 40 && !fills ? 16 : 8;
-    while (tx < 64 && p.experts * ((pieces + tx - 1) / tx) > (GATED ? 2 : 5) * p.sms) tx *= 2;
+    const bool many = p.experts > 1, fills = p.dbias && by8 > p.sms && by8 <= 2 * p.sms;   // (a wave without sharing)
+    const bool wasteful = many && by8 * 3 <= 2 * p.sms && by8 * 80 > p.experts * pieces * 11;   // (more than a tenth of a block)
+    int64_t tx = by8 * 8 <= p.sms || wasteful ? 4 : p.N % 16 && by8 >= 40 && !fills ? 16 : 8;
+    while (tx < 64 && each < 512 && p.experts * ((pieces + tx - 1) / tx) > 5 * p.sms) tx *= 2;
     const int64_t blocks = (pieces + tx - 1) / tx, units = p.experts * blocks;
-    int threads = !GATED && units <= 2 * p.sms ? 2 * kGradThreads : kGradThreads;
     int64_t ctas = 1;
     while (units * ctas * 2 <= 2 * p.sms && each >= 128 * ctas && (ctas < 8 || !p.dbias)) ctas *= 2;
+    while (many && ctas < 8 && units * ctas < 512 && each >= 512 * ctas) ctas *= 2;
+    int threads = !GATED ? (units <= 2 * p.sms ? 2 : 1) * kGradThreads
+                  : (many && each >= 64 && ((ctas == 1 && units <= 2 * p.sms) || each >= 512 * ctas)) || (ctas == 1 && units <= p.sms) ? 2 * kGradThreads : kGradThreads;
     if (p.dbias && ctas == 8 && units * 16 <= 2 * p.sms && each >= 128 * 8) ctas = kGradMaxCtas, threads = kGradThreads;
-    if (ctas == 1 && units <= p.sms) threads = 2 * kGradThreads;   // (100 rows of 8192 gated 3.8, of 256 threads 4.5)
     const int64_t grid = units * ctas;
     const size_t smem = (GATED ? 2 : 1) * (threads + tx) * 8 * sizeof(float);
     const auto kernel = linear_grad_kernel<KIND, GATED>;
