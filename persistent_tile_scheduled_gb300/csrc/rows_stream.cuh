@@ -168,7 +168,7 @@ __device__ __forceinline__ int rows_scan(int mine, int &carry, int *sums)
 // Source: what a block is:
 //   count(), expert(b), have(b)          blocks; a block's expert and tokens
 //   row(b, place)                        a token's row of the operand
-//   early(b, have, f, two)               what finish adds, loaded when the item begins: bias, residual
+//   early(b, have, f, two)               what finish adds, loaded when a cluster's only item begins: bias, residual
 //   finish(b, place, have, f, s, two, early)
 //                                        s[0], s[1]: feature f of tokens place and place + 1, s[2], s[3]:
 //                                        feature f + 8 (gated: the gate's f and the other's f)
@@ -212,8 +212,7 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
     for (int n = 0; item < items; item += step, ++n) {
         const int b = item / tiles, f = (item - b * tiles) * kFeatures + g, have = source.have(b);
         const bool two = GATED || f + 8 < features;
-        const int turn = n % kw, bar = 1 + team * kw + turn;
-        if (NB == 1 && member == turn) early = source.early(b, have, f, two);   // (by 32 the registers are taken)
+        if (SHARED && warp == 0) early = source.early(b, have, f, two);
         float acc[NB][4] = {};
         for (int at = first; at < end; at += kChunks) {
             const bool more = at + kChunks < end;
@@ -224,6 +223,7 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
         // Over the team's warps: one of them in turn, the others run on.  It waits for all
         // at this item, so every warp does once in kw items: none can come back to an
         // item's place (and barrier) before its reader is through with it.
+        const int turn = n % kw, bar = 1 + team * kw + turn;
         float *mine = part + (team * kw + turn) * kw * NB * 128;   // [member][NB][32 lanes][4]
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -233,7 +233,7 @@ __device__ __forceinline__ void stream_items(const Source &source, const uint16_
             continue;
         }
         asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * kw) : "memory");
-        if (NB > 1) early = source.early(b, have, f, two);
+        if constexpr (!SHARED) early = source.early(b, have, f, two);   // (while weights are multiplied the registers are taken: 4 % slower)
         // a lane has rows g and g + 8 of two tokens
         for (int nb = 0; nb < NB && 8 * nb < have; ++nb) {
             float s[4] = {};
