@@ -55,7 +55,14 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     int bn = kExpertTileN;
     const int64_t length = mode == EXPERT_WGRAD ? rows / experts : contraction;
     if (cg == 0) cg = choose_cta_group((length + kelems - 1) / kelems);
-    if (mode == EXPERT_FWD && h->opts.cta_group != 2 && rows <= kExpertFewRows * experts) {
+    const int64_t used = rows < experts ? rows : experts;   // (experts with rows, at most)
+    const auto row_tiles = [&](int of) -> int64_t { return experts == 1 ? (rows + of - 1) / of : rows / of + used; };
+    bool few = rows <= kExpertFewRows * experts;
+    // With an epilogue also one tile of rows, and what makes a single wave: the tiles' CTAs
+    // then share contractions (us, this / pairs: 64 rows of 4096 x 8192 16.1 / 34.6, of 28672
+    // x 4096 48.3 / 47.6; 128 of 4096^2 14.0 / 22.9, 256 19.9 / 28.0, of 1024^2 6.2 / 12.3).
+    if (epi) few = few || (experts == 1 && rows <= kExpertTileNFew) || row_tiles(kExpertTileNFew) * ((features + tile_f - 1) / tile_f) <= h->sm_count;
+    if (mode == EXPERT_FWD && h->opts.cta_group != 2 && few) {
         cg = 1;
         bn = kExpertTileNFew;
     }
@@ -78,8 +85,7 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     }
     // tiles: at most one short one per expert on top of the rows' own
     const int64_t tf = (features + tile_f * cg - 1) / (tile_f * cg);
-    const int64_t used = rows < experts ? rows : experts;
-    const int64_t tiles = mode == EXPERT_WGRAD ? experts * tf * ((N + bn - 1) / bn) : (rows / bn + used) * tf;
+    const int64_t tiles = mode == EXPERT_WGRAD ? experts * tf * ((N + bn - 1) / bn) : row_tiles(bn) * tf;
     if (tiles > (int64_t(1) << 30)) return GEMM_ERR_INVALID_ARG;
     int64_t clusters = h->opts.max_clusters > 0 && h->opts.max_clusters < resident ? h->opts.max_clusters : resident;
     if (clusters > tiles) clusters = tiles;
