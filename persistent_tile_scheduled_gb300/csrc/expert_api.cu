@@ -60,7 +60,8 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     bool few = rows <= kExpertFewRows * experts;
     // With an epilogue also one tile of rows, and what makes a single wave: the tiles' CTAs
     // then share contractions (us, this / pairs: 64 rows of 4096 x 8192 16.1 / 34.6, of 28672
-    // x 4096 48.3 / 47.6; 128 of 4096^2 14.0 / 22.9, 256 19.9 / 28.0, of 1024^2 6.2 / 12.3).
+    // x 4096 48.3 / 47.6; 128 of 4096^2 14.0 / 22.9, 256 19.9 / 28.0, of 1024^2 6.2 / 12.3; but
+    // of two waves, 256 of 8192 x 4096, 35.4 / 30.2).
     if (epi) few = few || (experts == 1 && rows <= kExpertTileNFew) || row_tiles(kExpertTileNFew) * ((features + tile_f - 1) / tile_f) <= h->sm_count;
     if (mode == EXPERT_FWD && h->opts.cta_group != 2 && few) {
         cg = 1;

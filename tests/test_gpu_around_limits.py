@@ -186,6 +186,33 @@ def test_calls_on_several_streams_at_once(h):
             assert all(torch.equal(x, y) for x, y in zip(a.results(), results))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, pts.GEMM_E4M3], ids=["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("counts,N,K", [([33], 264, 8192), ([64], 2048, 4096), ([65], 1000, 1536), ([100], 136, 2048), ([300], 128, 4096), ([1000], 136, 1024),
+                                        ([0, 100, 3], 264, 2048), ([70, 0, 0, 64], 520, 4096), ([17, 130], 128, 8192)])
+@pytest.mark.parametrize("act,keep", [(3, False), (SILU | GATED, True)])
+def test_row_tiles_that_ctas_share(h, counts, N, K, act, keep, dtype):
+    """Several tiles of rows, ragged, whose contraction 2, 4 or 8 CTAs share: two runs have equal bits."""
+    rows, E, all_, out = sum(counts) + 2, len(counts), N * (2 if act & GATED else 1), torch.float16 if dtype == F16 else torch.bfloat16
+    t = {F16: torch.float16, BF16: torch.bfloat16, pts.GEMM_E4M3: torch.float8_e4m3fn}[dtype]
+    A, B = rand((rows, K), torch.float32, 1).clamp(-448, 448).to(t), rand((E, all_, K), torch.float32, 2, 1.0 if dtype == pts.GEMM_E4M3 else K ** -0.5).clamp(-448, 448).to(t)
+    scale = float(torch.tensor(K ** 0.5 if dtype == pts.GEMM_E4M3 else 1.0).float())
+    bias, res, off = rand((E, all_), out, 3), rand((rows, N), out, 4), offsets_of(counts)
+    got = []
+    for _ in range(2):
+        C, Z = torch.full((rows, N), 7.0, dtype=out, device="cuda"), torch.full((rows, all_), 7.0, dtype=out, device="cuda") if keep else None
+        pts.gemm_run_linear(h, rows if E > 1 else rows - 2, E, N, K, A, B, bias, res, off if E > 1 else None, C, Z, act, dtype, 1.0, scale)
+        got.append((C, Z))
+    assert torch.equal(got[0][0], got[1][0]) and (not keep or torch.equal(got[0][1], got[1][1]))
+    at = off.tolist()
+    for e in range(E):
+        r = slice(at[e], at[e + 1])
+        (c, dc), (z, dz) = ref.linear(act, A[r], B[e], bias[e], res[r], scale)
+        ref.close(C[r], c, dc, ("C", e))
+        if keep:
+            ref.close(Z[r], z, dz, ("Z", e))
+    assert (C[-2:] == 7.0).all() and (not keep or (Z[-2:] == 7.0).all())
+
+
 @pytest.mark.parametrize("N,act,dtype", [(19456 + 8, 2, F16), (22528, SILU, BF16), (28000, 0, F16), (9736, SILU | GATED, BF16), (14336, 3 | GATED, F16), (22528, 1, pts.GEMM_E4M3)])
 @pytest.mark.parametrize("rows", [9, 24, 32])
 def test_a_wave_and_a_part(h, rows, N, act, dtype):
