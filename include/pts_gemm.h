@@ -505,6 +505,9 @@ gemm_status_t gemm_expert_route_grad(gemm_handle_t h, int64_t tokens, int64_t to
  *   Hs    tokens * top_k x hidden: the hidden rows (rounded to the type) pass
  *         through it, a row per assignment; a token that names an expert twice
  *         has it computed once.
+ * It reads an expert's weights once for its first 8 (or 32) tokens and from L2 for
+ * the others: where experts have more than some 16 on average, sorting,
+ * gemm_run_linear twice and gemm_expert_combine are faster.
  * fp16 or bf16; sums fp32.  dim % 8 == 0, hidden % 8 == 0; tokens at most
  * GEMM_EXPERT_LAYER_MAX_TOKENS, tokens * top_k GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS,
  * experts GEMM_EXPERT_SORT_MAX_EXPERTS. */

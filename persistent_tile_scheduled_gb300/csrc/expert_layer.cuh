@@ -393,12 +393,21 @@ __global__ void __launch_bounds__(kRowsThreads, 2) layer_down_kernel(const Layer
     }
 }
 
-// Blocks of 8 tokens, or of 32 where experts have more than so many on average: a
-// second block reads its weights from L2, but of 32 fewer chunks are on their way
-// (us by 8 / by 32; 48 tokens, 4 of 32 experts of 2048^2 133 / 185; 32, 2 of 8 of
-// 4096^2 145 / 190; 64, 2 of 8 of 4096^2 236 / 201; 64, 8 of 8 of 2048^2 166 / 116).
-constexpr int kLayerManyMean = 12;
-constexpr int kLayerManyKw = 2;   // (teams of 8 warps: their sums take room that L1 needs)
+// Blocks of 8 tokens, or of 32 where experts have more than so many on average and there
+// is so much to multiply: a second block reads its weights from L2, but of 32 fewer chunks
+// are on their way, and fewer items (us by 8 / by 32, gated; 13 and 20 tokens, 4 of 4
+// experts of 4096 x 1024 31 / 40, 39 / 41; 32 51 / 44; 20 of 2048^2 42 / 34; 16 and 64,
+// 1 of 1 of 2048^2 13.7 / 15.3, 37.6 / 32.8; 64, 2 of 8 of 1024^2 26.6 / 24.6, of 4096^2
+// 246 / 176; 64, 8 of 32 of 2048^2 230 / 175).
+constexpr int kLayerManyMean = 14;
+constexpr long long kLayerManyProducts = 500000000;   // of a weight and a token's value
+
+// Warps of a team by 32: 2, since the sums of larger ones take room that L1 needs, unless
+// there are too few items for all teams.
+inline int layer_many_kw(long long items, const RowsRoom &room)
+{
+    return items <= room.clusters[1] / 2 ? 8 : items <= 2 * room.clusters[1] ? 4 : 2;
+}
 
 template <int NB>
 constexpr size_t layer_tables(int assignments, int experts)
@@ -408,7 +417,7 @@ constexpr size_t layer_tables(int assignments, int experts)
 template <int NB>
 constexpr size_t layer_smem(int tokens, int assignments, int experts)   // the larger of the two kernels'
 {
-    const size_t up = rows_part_bytes(NB, NB == 1 ? 8 : kLayerManyKw), down = kRowsWarps * kDownPitch * 4 * tokens;
+    const size_t up = rows_part_bytes(NB, 8), down = kRowsWarps * kDownPitch * 4 * tokens;
     return layer_tables<NB>(assignments, experts) + (up > down ? up : down);
 }
 
@@ -441,7 +450,7 @@ cudaError_t launch_layer_of(const LayerParams &p, const RowsRoom &room, cudaStre
     if (p.hidden > 0) {
         const int features = gated ? 8 : 16;
         const long long items = static_cast<long long>(blocks) * ((p.hidden + features - 1) / features);
-        const int kw = NB == 1 ? rows_kw(items, p.dim, room) : kLayerManyKw, ctas = NB == 1 ? rows_ctas(items, p.dim, room) : 1;
+        const int kw = NB == 1 ? rows_kw(items, p.dim, room) : layer_many_kw(items, room), ctas = NB == 1 ? rows_ctas(items, p.dim, room) : 1;
         const auto kernel = ctas > 1 ? (gated ? layer_up_kernel<KIND, true, NB, NB == 1> : layer_up_kernel<KIND, false, NB, NB == 1>)
                                      : (gated ? layer_up_kernel<KIND, true, NB, false> : layer_up_kernel<KIND, false, NB, false>);
         const cudaError_t e = launch_layer_kernel(kernel, items, ctas, rows_part_bytes(NB, kw) + tables, p, room, stream, overlap, blocks, kw, ctas, down_ctas);
@@ -455,8 +464,9 @@ cudaError_t launch_layer_of(const LayerParams &p, const RowsRoom &room, cudaStre
 template <int KIND>
 cudaError_t launch_layer(const LayerParams &p, const RowsRoom &room, cudaStream_t stream, bool overlap)
 {
-    return p.tokens * p.top_k <= kLayerManyMean * p.experts ? launch_layer_of<KIND, 1>(p, room, stream, overlap)
-                                                            : launch_layer_of<KIND, 4>(p, room, stream, overlap);
+    const int n = p.tokens * p.top_k;
+    const bool many = n > kLayerManyMean * p.experts && static_cast<double>(n) * p.dim * p.hidden * (p.act & ACT_GATED ? 3 : 2) > kLayerManyProducts;
+    return many ? launch_layer_of<KIND, 4>(p, room, stream, overlap) : launch_layer_of<KIND, 1>(p, room, stream, overlap);
 }
 
 }  // namespace pts

@@ -212,3 +212,12 @@ def test_sizes_that_are_refused(h):
     with pytest.raises(pts.GemmError):
         call(1, 1, 1, 8, 8, 0, x[1:])   # not 16-byte aligned
     assert call(0, 1, 1, 8, 8) == 0 and call(1, 1, 1, 0, 8) == 0
+
+
+@pytest.mark.parametrize("T,k,E,D,H,act", [(64, 8, 16, 520, 1048, 5 | GATED), (40, 8, 6, 1032, 520, 3 | GATED), (64, 8, 36, 72, 7600, 2), (33, 4, 1, 2056, 1000, 4),
+                                           (64, 2, 3, 5160, 552, 1 | GATED), (20, 3, 4, 4096, 1032, 0)])
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+def test_many_tokens_an_expert(h, T, k, E, D, H, act, dtype):
+    """Blocks of 32 tokens, teams of 2, 4 and 8 warps, ragged; ids outside the experts and twice."""
+    run(h, T, k, E, D, H, act, dtype, choose(T, k, E))
+    run(h, T, k, E, D, H, act, dtype, torch.full((T, k), E - 1, dtype=torch.int32, device="cuda"), bias=False, in_place=True)
