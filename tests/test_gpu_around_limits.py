@@ -243,6 +243,40 @@ def test_a_wave_and_a_part(h, rows, N, act, dtype):
     ref.close(D[3], d, dd, "D")
 
 
+def test_a_wave_and_a_part_captured(h):
+    """The two launches in a graph, between kernels that write what they read and read what they write: as eagerly."""
+    rows, N, K, t = 24, 20000, 1600, torch.float16
+    A, B, back = rand((rows, K), t, 1), large((N, K), t, 2, K ** -0.5), large((K, N), t, 3, N ** -0.5)
+    X, C, Y = torch.zeros_like(A), torch.zeros(rows, N, dtype=t, device="cuda"), torch.zeros(rows, K, dtype=t, device="cuda")
+
+    def step(s):
+        X.copy_(A)
+        for _ in range(3):
+            pts.gemm_run_linear(h, rows, 1, N, K, X, B, None, None, None, C, None, SILU, F16, stream=s)
+            pts.gemm_run_linear(h, rows, 1, K, N, C, back, None, X, None, X, None, 0, F16, stream=s)
+        Y.copy_(X)
+        C.zero_()
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step(s)
+    torch.cuda.synchronize()
+    want = Y.clone()
+    x = A.double()
+    for _ in range(3):
+        c = torch.nn.functional.silu(x @ B.double().T).to(t).double()
+        x = (c @ back.double().T + x).to(t).double()
+    assert float((want.double() - x).norm()) <= 3 * 2.0 ** -10 * float(x.norm())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(s)
+    for _ in range(5):
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)
+
+
 def test_products_that_are_refused(h):
     x = torch.zeros(1 << 16, dtype=torch.float16, device="cuda").data_ptr()
     off = offsets_of([8, 0]).data_ptr()
