@@ -91,10 +91,9 @@ gemm_status_t run_product(gemm_ctx *h, int mode, int64_t rows, int64_t experts, 
     int64_t clusters = h->opts.max_clusters > 0 && h->opts.max_clusters < resident ? h->opts.max_clusters : resident;
     if (clusters > tiles) clusters = tiles;
     // Tiles for less than half the SMs: CTAs share a tile's contraction, 0.2 us per
-    // k-block saved for 2.8 us of joining (us, this / one CTA per tile: one row of 1024 x
-    // 8192 10.0 / 32.7, of 2048^2 8.4 / 10.8, of 8192^2, 2 CTAs, 27.6 / 34.1; but of 512 x
-    // 1024 7.2 / 6.8 and of 8192 x 1024 8.5 / 7.1).  Few clusters of 8 find room at once:
-    // 16 tiles of that contraction take 20.7 by 8 CTAs each, 14.6 by 4.
+    // k-block saved for some 1.5 us of joining (us, this / one CTA per tile: one row of 1024
+    // x 8192 8.2 / 33.0, of 2048^2 6.0 / 11.0, of 8192^2, 2 CTAs, 25.0 / 34.1).  Few clusters
+    // of 8 find room at once: 16 tiles of 8192 by 8 CTAs each take longer than by 4.
     int split = 1;
     const int64_t length_kb = (contraction + kelems - 1) / kelems;
     const bool share = mode == EXPERT_FWD && bn == kExpertTileNFew && h->opts.cta_group == 0 && h->opts.max_clusters == 0;
