@@ -43,3 +43,21 @@ def pytest_terminal_summary(terminalreporter, exitstatus, config):
     if path:
         with open(path, "w") as f:
             json.dump(PARITY_LOG, f)
+
+
+@pytest.fixture(autouse=True)
+def new_streams_follow_the_current_one(request, monkeypatch):
+    """A stream that a GPU test makes first waits for what is queued on the current one.  torch's streams wait for nothing, and tests
+    fill their arrays on the default stream before they use them on one of their own."""
+    if request.node.get_closest_marker("gpu") is None:
+        return
+    import torch
+
+    class Stream(torch.cuda.Stream):
+        def __new__(cls, device=None, priority=0, **existing):
+            stream = super().__new__(cls, device, priority, **existing)
+            if not existing:   # (else one that is there already, as current_stream() gives it)
+                stream.wait_stream(torch.cuda.current_stream(stream.device))
+            return stream
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
