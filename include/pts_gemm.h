@@ -435,7 +435,8 @@ gemm_status_t gemm_run_nibble(gemm_handle_t h, int64_t rows, int64_t experts, in
  *   integral); GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2;
  *   SILU z / (1 + exp(-z)).
  * Of -infinity (a feature that its bias masks) all but NONE are their limit, 0 to
- * within 2^-54, and so are their slopes.  A NaN stays one.
+ * within 2^-54, and so are their slopes; of large z and +infinity the slopes of
+ * GELU, GELU_TANH and SILU are 1.  A NaN stays one.
  * With GEMM_ACT_GATED the matrix holds 2N features, a gate's N and then N that
  * it multiplies: act(z[n]) * z[N + n]. */
 typedef enum {

@@ -65,9 +65,21 @@ __device__ __forceinline__ float at_least(float z, float lo)
     return y;
 }
 
+// min(z, hi), and NaN for NaN
+__device__ __forceinline__ float at_most(float z, float hi)
+{
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(hi));
+    return y;
+}
+
 // silu and the tanh form of gelu of anything below this are less than 2^-54 away from 0:
 // there z counts as this, -infinity too, since the factor that it meets stops falling.
 constexpr float kLowest = -44.0f;
+
+// From here on the slopes of gelu, its tanh form and silu are 1 to within 2^-86: there z counts
+// as this in them, infinity too (it meets a 0, and so did a large z whose product overflowed).
+constexpr float kHighest = 64.0f;
 
 template <int ACT>
 __device__ __forceinline__ float act(float z)
@@ -151,6 +163,11 @@ __device__ __forceinline__ Pair at_least(Pair z, float lo)
     return each(z, [=](float v) { return at_least(v, lo); });
 }
 
+__device__ __forceinline__ Pair at_most(Pair z, float hi)
+{
+    return each(z, [=](float v) { return at_most(v, hi); });
+}
+
 // 2^y, y at most 60: 1 / (1 + 2^60), of kLowest at most, is next to nothing, and two of
 // them have a product (a NaN is taken for 60: it comes back with z, and not into the other value)
 __device__ __forceinline__ Pair exp2_limited(Pair y)
@@ -198,18 +215,19 @@ __device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
         const float2 q = values(tail), v = values(z);
         const Pair p = pair(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y);
         a = z * p;
-        slope = fma(z * both(kNormalPeak), e, p);
+        slope = fma(at_most(z, kHighest) * both(kNormalPeak), e, p);
     } else if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
         // z s(y), s = 1 / (1 + exp(-y)): s + z s (1 - s) y', with 1 - s = exp(-y) s
         z = at_least(z, kLowest);
+        const Pair x = at_most(z, kHighest);
         Pair y, dy;   // (y: the exponent of 2)
         if constexpr (ACT == ACT_GELU_TANH) {
-            const Pair z2 = each(z * z, [](float v) { return fminf(v, 4096.0f); });   // (dy stays finite; there the slope is 0 or 1)
-            y = z * fma(both(-kLog2E * kGeluTanhTwice * kGeluTanhCube), z2, both(-kLog2E * kGeluTanhTwice));
-            dy = z * fma(both(3.0f * kGeluTanhTwice * kGeluTanhCube), z2, both(kGeluTanhTwice));
+            const Pair x2 = x * x;
+            y = x * fma(both(-kLog2E * kGeluTanhTwice * kGeluTanhCube), x2, both(-kLog2E * kGeluTanhTwice));
+            dy = x * fma(both(3.0f * kGeluTanhTwice * kGeluTanhCube), x2, both(kGeluTanhTwice));
         } else {
-            y = z * both(-kLog2E);
-            dy = z;
+            y = x * both(-kLog2E);
+            dy = x;
         }
         const Pair e = exp2_limited(y), s = rcp_fast(e + both(1.0f));
         a = z * s;
