@@ -202,7 +202,7 @@ __device__ __forceinline__ void act_and_slope(Pair z, Pair &a, Pair &slope)
 {
     if constexpr (ACT == ACT_RELU) {
         a = each(z, [](float v) { return positive(v); });
-        slope = each(z, [](float v) { return v > 0.0f ? 1.0f : 0.0f; });
+        slope = each(z, [](float v) { return v > 0.0f ? 1.0f : positive(v); });   // (0, or NaN)
     } else if constexpr (ACT == ACT_RELU2) {
         const Pair p = each(z, [](float v) { return positive(v); });
         a = p * p;

@@ -71,3 +71,25 @@ def test_a_sum_that_overflows_its_type(h, code, gated):
     assert (dZ[0::2, :N] == INF).all() if code == 2 else torch.equal(dZ[0::2, :N], (dC * up)[0::2])
     if gated:
         assert (dZ[0::2, N:] == INF).all() and (dZ[1::2, N:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=NAMES)
+@pytest.mark.parametrize("gated", [0, GATED], ids=["plain", "gated"])
+@pytest.mark.parametrize("code", range(1, 6), ids=ref.ACTS[1:])
+def test_a_nan_stays_one(h, code, gated, dtype):
+    """A NaN in Z, in either place of a pair, reaches its own gradients, dbias with them, and no others; forward too."""
+    t, N, rows = TORCH[dtype], 48, 6
+    z = torch.linspace(-3, 3, rows * N).view(rows, N).to(t).cuda()
+    z[1, 6], z[4, 7] = NAN, NAN
+    Z = torch.cat([z, torch.full_like(z, 1.5)], 1)[:, :N * (2 if gated else 1)].contiguous()
+    dC, dZ, dbias = torch.full_like(z, 0.5), torch.zeros_like(Z), torch.zeros(1, Z.shape[1], device="cuda")
+    pts.gemm_linear_grad(h, rows, 1, N, dC, Z, None, dZ, dbias, code | gated, dtype)
+    bad, cols = torch.zeros_like(Z, dtype=torch.bool), [6, 7, N + 6, N + 7] if gated else [6, 7]
+    for r, c in ((1, 6), (4, 7)):
+        bad[r, c::N] = True
+    assert torch.equal(torch.isnan(dZ), bad) and torch.isfinite(dZ[~bad]).all()
+    assert torch.isnan(dbias[0, cols]).all() and int(torch.isnan(dbias).sum()) == len(cols)
+    K = 16
+    A, B, C = torch.zeros(rows, K, dtype=t, device="cuda"), torch.zeros(Z.shape[1], K, dtype=t, device="cuda"), torch.zeros(rows, N, dtype=t, device="cuda")
+    pts.gemm_run_linear(h, rows, 1, N, K, A, B, Z[1:2].contiguous(), None, None, C, None, code | gated, dtype)
+    assert torch.isnan(C[:, 6]).all() and int(torch.isnan(C).sum()) == rows
