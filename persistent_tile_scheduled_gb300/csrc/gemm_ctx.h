@@ -77,6 +77,7 @@ struct gemm_ctx {
     int linear_clusters[3][2][3] = {};        // gemm_run_linear: the same per dtype, plain or gated, and variant
     int linear_shared[3][2][3] = {};          // and clusters of 2, 4 and 8 CTAs that share a tile
     pts::RowsRoom rows_room = {};             // the kernels for few rows
+    int grad_clusters[2][2] = {};             // gemm_linear_grad's largest, per dtype, plain or gated; -1: none
     bool sort_smem[2] = {};                   // gemm_expert_sort: limits raised, per kernel
     pts::NibPrepared nibble[2] = {};          // gemm_run_nibble, per dtype
 };

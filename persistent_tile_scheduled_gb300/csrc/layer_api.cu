@@ -89,7 +89,12 @@ gemm_status_t gemm_linear_grad(gemm_handle_t h, int64_t rows, int64_t experts, i
     p.dz = dZ;
     p.dbias = dbias;
     p.sms = h->sm_count;
-    return launched(launch_linear_grad(static_cast<int>(dtype), p, static_cast<cudaStream_t>(stream), overlap(h)));
+    int &room = h->grad_clusters[dtype][(act & GEMM_ACT_GATED) != 0];
+    if (room == 0 && dbias != nullptr) {
+        room = ask_linear_grad_room(static_cast<int>(dtype), act & GEMM_ACT_GATED);
+        if (room < 1) room = -1;
+    }
+    return launched(launch_linear_grad(static_cast<int>(dtype), p, room, static_cast<cudaStream_t>(stream), overlap(h)));
 }
 
 gemm_status_t gemm_expert_layer(gemm_handle_t h, int64_t tokens, int64_t top_k, int64_t experts, int64_t dim,

@@ -34,7 +34,9 @@ struct LinearGradParams {
     int32_t sms;
 };
 
-cudaError_t launch_linear_grad(int kind, const LinearGradParams &p, cudaStream_t stream, bool overlap);
+// Clusters of the most CTAs that share an expert's rows, as many as the device holds at once.
+int ask_linear_grad_room(int kind, bool gated);
+cudaError_t launch_linear_grad(int kind, const LinearGradParams &p, int room, cudaStream_t stream, bool overlap);
 
 // ---- a layer of experts for a few tokens (expert_layer.cuh) -------------------------
 constexpr int kLayerMaxTokens = 64;         // a mask of an expert's tokens is 64 bits

@@ -15,15 +15,14 @@
 #include "activation.cuh"
 #include "launch.cuh"
 #include "layer_launch.h"
+#include "linear_plan.h"
 #include "ptx.cuh"
 
 namespace pts {
 
 namespace {
 
-constexpr int kGradThreads = 256;      // of a CTA, or twice that
-constexpr int kGradRows = 2;      // rows of a thread that are loaded together, while those before are computed
-constexpr int kGradMaxCtas = 16;   // CTAs of a cluster: they share an expert's rows
+constexpr int kGradRows = 2;   // rows of a thread that are loaded together, while those before are computed
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
 {
@@ -140,52 +139,54 @@ __global__ void __launch_bounds__(2 * kGradThreads)
     if (ctas > 1) cluster_sync();   // (the others have read this CTA's sums)
 }
 
+// Shared memory of the sums: of each thread's columns, then of the CTA's.
+constexpr size_t grad_smem(bool gated, int threads, int tx) { return (gated ? 2 : 1) * static_cast<size_t>(threads + tx) * 8 * sizeof(float); }
+
 template <int KIND, bool GATED>
-cudaError_t go(const LinearGradParams &p, cudaStream_t stream, bool overlap)
+cudaError_t go(const LinearGradParams &p, int room, cudaStream_t stream, bool overlap)
 {
-    // Blocks of 64 columns, and as many CTAs of 512 threads (two to an SM; gated, with more
-    // registers, one, and two of 256) to one as make a single wave, 8 at most; blocks of 32
-    // where columns are few, then also 16 CTAs of 256 threads (us, gelu's tanh form, bf16:
-    // 16384 rows of 8192 128 blocks by 2 133, by 4 of 256 threads 134, by 8 142; of 2048 32
-    // by 8 38.5, 64 blocks of 32 columns by 4 44; of 1024 32 of 32 by 8 24.5, 16 of 64 by 16
-    // 29.7; of 512 16 of 32 by 16 of 256 threads 17.2, by 8 19.1; 9115 gated of 1024 by 256
-    // threads 21, by 512 33).  Rows that are no multiple of 32 bytes share those at a
-    // block's edges: blocks of 128 columns (9115 rows of 7000 76, of 64 84).
-    // Experts' rows are uneven: where there are many of them a block is shared although a
-    // wave is full, so that the largest does not end last (16384 over 8 of 2048, uneven as
-    // exp of half a normal / even: 54 / 41, not shared 67 / 37; gated 67 / 68, 76 / 61).
-    // Few rows each and more blocks than five waves: wider ones (4000 over 64 of 4096 35 /
-    // 20, of 64 columns 32 / 30; gated 44 / 33, 51 / 50).
-    // Clusters need not be whole where nothing is added up.
-    const int64_t pieces = p.N / 8, each = p.rows / p.experts, by8 = p.experts * ((pieces + 7) / 8);
-    const bool many = p.experts > 1, fills = p.dbias && by8 > p.sms && by8 <= 2 * p.sms;   // (a wave without sharing)
-    const bool wasteful = many && by8 * 3 <= 2 * p.sms && by8 * 80 > p.experts * pieces * 11;   // (more than a tenth of a block)
-    int64_t tx = by8 * 8 <= p.sms || wasteful ? 4 : p.N % 16 && by8 >= 40 && !fills ? 16 : 8;
-    while (tx < 64 && each < 512 && p.experts * ((pieces + tx - 1) / tx) > 5 * p.sms) tx *= 2;
-    const int64_t blocks = (pieces + tx - 1) / tx, units = p.experts * blocks;
-    int64_t ctas = 1;
-    while (units * ctas * 2 <= 2 * p.sms && each >= 128 * ctas && (ctas < 8 || !p.dbias)) ctas *= 2;
-    while (many && ctas < 8 && units * ctas < 512 && each >= 512 * ctas) ctas *= 2;
-    int threads = !GATED ? (units <= 2 * p.sms ? 2 : 1) * kGradThreads
-                  : (many && each >= 64 && ((ctas == 1 && units <= 2 * p.sms) || each >= 512 * ctas)) || (ctas == 1 && units <= p.sms) ? 2 * kGradThreads : kGradThreads;
-    if (p.dbias && ctas == 8 && units * 16 <= 2 * p.sms && each >= 128 * 8) ctas = kGradMaxCtas, threads = kGradThreads;
-    const int64_t grid = units * ctas;
-    const size_t smem = (GATED ? 2 : 1) * (threads + tx) * 8 * sizeof(float);
+    const GradShape g = grad_shape(p.rows, p.experts, p.N, GATED, p.dbias != nullptr, p.sms, room);
+    // (clusters need not be whole where nothing is added up)
+    return launch_kernel(linear_grad_kernel<KIND, GATED>, dim3(static_cast<unsigned>(g.units * g.ctas)), g.threads, grad_smem(GATED, g.threads, g.tx),
+                         p.dbias ? g.ctas : 1, stream, overlap, p, g.tx, g.ctas, static_cast<int>(g.blocks));
+}
+
+// Clusters of kGradMaxCtas CTAs that the device holds at once, 0 where it places none.
+template <int KIND, bool GATED>
+int ask_room()
+{
     const auto kernel = linear_grad_kernel<KIND, GATED>;
-    if (p.dbias && ctas > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kGradMaxCtas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(kGradMaxCtas);
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.dynamicSmemBytes = grad_smem(GATED, kGradThreads, 8);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess
+        || cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
     }
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), threads, smem, p.dbias ? static_cast<int>(ctas) : 1, stream, overlap, p,
-                         static_cast<int>(tx), static_cast<int>(ctas), static_cast<int>(blocks));
+    return clusters;
 }
 
 }  // namespace
 
-cudaError_t launch_linear_grad(int kind, const LinearGradParams &p, cudaStream_t stream, bool overlap)
+int ask_linear_grad_room(int kind, bool gated)
 {
-    if (p.act & ACT_GATED) return kind == 0 ? go<0, true>(p, stream, overlap) : go<1, true>(p, stream, overlap);
-    return kind == 0 ? go<0, false>(p, stream, overlap) : go<1, false>(p, stream, overlap);
+    if (gated) return kind == 0 ? ask_room<0, true>() : ask_room<1, true>();
+    return kind == 0 ? ask_room<0, false>() : ask_room<1, false>();
+}
+
+cudaError_t launch_linear_grad(int kind, const LinearGradParams &p, int room, cudaStream_t stream, bool overlap)
+{
+    if (p.act & ACT_GATED) return kind == 0 ? go<0, true>(p, room, stream, overlap) : go<1, true>(p, room, stream, overlap);
+    return kind == 0 ? go<0, false>(p, room, stream, overlap) : go<1, false>(p, room, stream, overlap);
 }
 
 }  // namespace pts
