@@ -454,7 +454,8 @@ typedef enum {
  *   Z         rows x N', of C's type, or NULL: what gemm_linear_grad needs;
  *   act       a gemm_act_t.
  * Bias, activation and residual are computed on the fp32 sums, each output is
- * rounded once.  K == 0: Z is the bias. */
+ * rounded once.  K == 0: Z is the bias.  N % 8 == 0; N' at most
+ * GEMM_EXPERT_MAX_SIZE, and at most 2^30 tiles of output. */
 gemm_status_t gemm_run_linear(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, int64_t K, const void *A,
                               const void *B, const void *bias, const void *residual, const int32_t *offsets, void *C,
                               void *Z, int act, gemm_dtype_t dtype, float scale_a, float scale_b, void *stream);
@@ -465,7 +466,8 @@ gemm_status_t gemm_run_linear(gemm_handle_t h, int64_t rows, int64_t experts, in
  * rounded, in a fixed order; zeros for an expert without rows), experts x N', or
  * NULL for none.  dC: rows x N, Z and dZ: rows x N', fp16 or bf16.  dZ is then
  * the dC of gemm_run_experts_dgrad and _wgrad over N' (with offsets {0, rows}
- * where there is one matrix); the residual's gradient is dC. */
+ * where there is one matrix); the residual's gradient is dC.  N % 8 == 0; N' at
+ * most GEMM_EXPERT_MAX_SIZE, experts * ceil(N / 32) below 2^28. */
 gemm_status_t gemm_linear_grad(gemm_handle_t h, int64_t rows, int64_t experts, int64_t N, const void *dC, const void *Z,
                                const int32_t *offsets, void *dZ, float *dbias, int act, gemm_dtype_t dtype, void *stream);
 
@@ -480,7 +482,8 @@ typedef enum { GEMM_ROUTE_SELECTED = 0, GEMM_ROUTE_ALL = 1, GEMM_ROUTE_SIGMOID =
  * gemm_expert_sort, gemm_expert_combine and gemm_expert_layer take.  A logit of
  * -infinity, or NaN, is never chosen; where fewer than top_k are left, the
  * others' ids are -1 and their weights 0 (a padded token: all of them).
- * +infinity counts as a finite value above all others.
+ * +infinity counts as a finite value above all others (of fp32 logits as the
+ * largest finite one).
  * logits: tokens x experts, fp32, fp16 or bf16, aligned to its type.  experts in
  * [1, GEMM_EXPERT_SORT_MAX_EXPERTS], top_k in [1, min(experts,
  * GEMM_EXPERT_ROUTE_MAX_TOP_K)]; tokens * experts < 2^40. */
@@ -507,10 +510,13 @@ gemm_status_t gemm_expert_route_grad(gemm_handle_t h, int64_t tokens, int64_t to
  *         through it, a row per assignment; a token that names an expert twice
  *         has it computed once.
  * It reads an expert's weights once for its first 8 (or 32) tokens and from L2 for
- * the others: where experts have more than some 16 on average, sorting,
- * gemm_run_linear twice and gemm_expert_combine are faster.
- * fp16 or bf16; sums fp32.  dim % 8 == 0, hidden % 8 == 0; tokens at most
- * GEMM_EXPERT_LAYER_MAX_TOKENS, tokens * top_k GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS,
+ * the others: where experts have more than 8, sorting, gathering, gemm_run_linear
+ * twice and gemm_expert_combine are faster once the weights are large (8 gated
+ * experts of 4096 x 4096, us by this call / by those: 8 tokens each 125 / 143, 10 202 /
+ * 143, 16 174 / 144; of 2048 x 2048 39 / 50, 53 / 50, 56 / 51; of 1024 x 1024 18 / 25,
+ * 23 / 25, 25 / 25; 64 tokens each, 8 of 2048 x 2048, 105 / 59).
+ * fp16 or bf16; sums fp32.  dim % 8 == 0, hidden % 8 == 0 and at most 31580640;
+ * tokens at most GEMM_EXPERT_LAYER_MAX_TOKENS, tokens * top_k GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS,
  * experts GEMM_EXPERT_SORT_MAX_EXPERTS. */
 #define GEMM_EXPERT_LAYER_MAX_TOKENS 64
 #define GEMM_EXPERT_LAYER_MAX_ASSIGNMENTS 512

@@ -263,9 +263,9 @@ bool few_rows(const gemm_ctx *h, int64_t rows, int64_t experts, int64_t N, int64
     // (told which variant of the others to take, or to let a wait run out, it takes one of those)
     if (!is16(dtype) || h->opts.cta_group != 0 || h->opts.max_clusters != 0 || (h->opts.debug_flags & GEMM_DEBUG_FAULT_SKIP_TMA)) return false;
     // Up to 8 rows a matrix is read once from memory; of the 9th on a second time, from
-    // L2 (us, this / through shared memory: one row of 1024^2 3.6 / 4.0, of 4096^2 8.3 / 9.5,
-    // 8 of 4096 x 8192 13.6 / 14.6, 9 19.9 / 14.7; of 8192^2 either 24.5; 16 over 8 experts
-    // of 4096^2 43.8 / 45.4, 40 44.8 / 45.7, 64 45.3 / 45.8; 64 over 32 of 512^2 7.7 / 7.5).
+    // L2 (us, this / through shared memory: one row of 1024^2 2.8 / 4.0, of 4096^2 7.4 / 9.4,
+    // of 8192^2 23.1 / 24.8, 8 of 4096 x 8192 12.9 / 14.8, but 9 19.9 / 15.0; 16 over 8 experts
+    // of 4096^2 38.1 / 44.9, 40 44.5 / 46.9; 64 over 32 of 512^2 either 6.5).
     return K > 0 && rows <= kLinearRowsMax && experts <= kLinearRowsMax && rows <= (experts == 1 ? 8 : 5 * experts)
            && rows_items(rows, experts, N, gated) <= kIntMax;
 }

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) layer_down_kernel(const Layer
     const uint16_t *down = static_cast<const uint16_t *>(p.down), *hs = static_cast<const uint16_t *>(p.hs);
     float *mine = sums + warp * p.tokens * kDownPitch;
 
-    // the chunks from `at` on, up to kLayerChunks of one block
+    // the chunks from `at` on, up to rows_chunks() of one block
     auto group_of = [&](int tile, int at) {
         RowsGroup<NB> group;
         if (tile >= tiles || at >= end) {

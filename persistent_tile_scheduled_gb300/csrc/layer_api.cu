@@ -109,7 +109,8 @@ gemm_status_t gemm_expert_layer(gemm_handle_t h, int64_t tokens, int64_t top_k, 
         return GEMM_ERR_INVALID_ARG;
     if (experts < 0 || experts > kLayerMaxExperts || dim < 0 || dim > kMaxSize || hidden < 0 || hidden > kMaxSize) return GEMM_ERR_INVALID_ARG;
     if (dim % 8 != 0 || hidden % 8 != 0) return GEMM_ERR_INVALID_ARG;
-    // the kernels count pieces of work in 32 bits: blocks of tokens times tiles of 8 features, or stretches of 128
+    // the kernels count items in 32 bits, blocks times tiles of 8 features, and go up to a stride of the grid past
+    // the last: a block has a token at least, so there are no more of them than assignments
     if (static_cast<int64_t>(kLayerMaxAssignments + kLayerMaxAssignments / 16) * ((hidden + 7) / 8) > kIntMax) return GEMM_ERR_INVALID_ARG;
     if (tokens == 0 || dim == 0) return GEMM_OK;
     if (Y == nullptr || expert_ids == nullptr || weights == nullptr) return GEMM_ERR_INVALID_ARG;

@@ -26,13 +26,14 @@ inline GradShape grad_shape(int64_t rows, int64_t experts, int64_t N, bool gated
     // by 8 38.5, 64 blocks of 32 columns by 4 44; of 1024 32 of 32 by 8 24.5, 16 of 64 by 16
     // 29.7; of 512 16 of 32 by 16 of 256 threads 17.2, by 8 19.1; 9115 gated of 1024 by 256
     // threads 21, by 512 33).  Rows that are no multiple of 32 bytes share those at a
-    // block's edges: blocks of 128 columns (9115 rows of 7000 76, of 64 84).
+    // block's edges: blocks of 128 columns, unless they are too few for the SMs (9115 rows, by
+    // 128 / 64 columns: of 7000 75 / 81, of 5128 69 / 71, of 3848 45 / 51, of 2568, 41 blocks
+    // of 64, 37 / 37.5, but of 1928, 31 of them, 31.6 / 27, of 1288 25 / 21).
     // Experts' rows are uneven: where there are many of them a block is shared although a
     // wave is full, so that the largest does not end last (16384 over 8 of 2048, uneven as
     // exp of half a normal / even: 54 / 41, not shared 67 / 37; gated 67 / 68, 76 / 61).
     // Few rows each and more blocks than five waves: wider ones (4000 over 64 of 4096 35 /
     // 20, of 64 columns 32 / 30; gated 44 / 33, 51 / 50).
-    // Clusters need not be whole where nothing is added up.
     const int64_t pieces = N / 8, each = rows / experts, by8 = experts * ((pieces + 7) / 8);
     const bool many = experts > 1, fills = dbias && by8 > sms && by8 <= 2 * sms;   // (a wave without sharing)
     const bool wasteful = many && by8 * 3 <= 2 * sms && by8 * 80 > experts * pieces * 11;   // (more than a tenth of a block)

@@ -25,7 +25,6 @@ constexpr int kRowsWarps = kRowsThreads / 32;
 __host__ __device__ constexpr int rows_chunks(int nb) { return nb == 1 ? 8 : 4; }
 __host__ __device__ constexpr int rows_ahead(int nb) { return nb == 1 ? 4 : 2; }
 
-
 // 16 bytes of the weights: read once, kept out of L1, which holds the tokens' rows.
 // Memory is asked for 256 bytes of the row at a time (2 % faster than without).
 __device__ __forceinline__ uint4 ld_weights(const void *p)
@@ -277,8 +276,8 @@ inline int rows_ctas(long long items, int width, const RowsRoom &room)
 }
 
 // Warps of a team (blocks of 8): all, unless half of them have a full group each and
-// there are items for more teams (8 rows of 8192 x 1024 5.6 us by 4, 6.7 by 8; but
-// one of 1024^2 3.5 and 3.1, and of 4096 x 8192 17 and 13.2).
+// there are items for more teams (8 rows of 8192 x 1024 5.1 us by 4, 6.3 by 8; but
+// one of 1024^2 2.9 and 2.8, and of 4096 x 8192 16.6 and 12.6).
 inline int rows_kw(long long items, int width, const RowsRoom &room) { return width < 64 * 32 && items > room.clusters[1] ? 4 : 8; }
 
 // Shared memory of the sums.

@@ -2,10 +2,12 @@
 
 Bounds.  u is half a step of the output's type (2^-8 bf16, 2^-11 fp16, 2^-24 fp32), relative to the value.
   sums of K products in fp32   K 2^-23 sum |a||b| (a tensor core may truncate), and 2^-22 of the sum for scale and bias
-  activations                  2^-15 of their value.  exp(y) in CUDA's fast form is off by 2 + 1.2 |y| steps of 2^-23 and its
-                               argument by 3 roundings of 2^-24 |y|; where |y| > 80 nothing of it is left, so all is below
-                               (2 + 1.2 * 80 + 2 * 80) 2^-23 < 2^-15.  erfc's argument x (|x| < 10 while it is not 0) is off
-                               by 2^-24 |x|, which moves it by 2 x^2 2^-24 = 2^-16 of its value at most.
+  activations                  2^-15 of their value.  2^y in its fast form is off by 4 steps of 2^-24, and y by as many roundings
+                               of 2^-24 |y| as it has operations and constants, which moves the power by 0.7 times that.
+                               gelu: y = -z^2 log2(e) / 2 has 3; behind |z| = 13.5, |y| = 132, less than 2^-127 is left.  With
+                               the polynomial's 1.1e-6 (19 steps) and 4 roundings of the products around it that is
+                               (4 + 0.7 * 3 * 132 + 19 + 4) 2^-24 < 2^-15.  silu and the tanh form: y has at most 8, and behind
+                               |y| = 60 the power is cut off, the value then below 44 * 2^-60: (4 + 0.7 * 8 * 60 + 8) 2^-24.
   an error d of a sum          slope * d behind the activation; |slope| <= 1.13 (gelu and silu), 2 |z| + 2 d (relu^2)
 and 2^-25, half the smallest fp16 subnormal (bf16's are smaller), for each rounding to 16 bits."""
 import math
